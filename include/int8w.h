@@ -185,6 +185,99 @@ typedef struct {
  * x). */
 int int8w_fp8_gemv(const int8w_fp8_weight *w, const uint16_t *x, uint16_t *y, uint64_t stream);
 
+/* ---- MXFP4: 4-bit microscaled values (the microscaling format with 4-bit
+ * elements).  A row of k values, k a multiple of 32, is k/2 code bytes and k/32
+ * scale bytes.  The code of element j is the low (j even) or high half of byte
+ * j/2: bit 3 is the sign, bits 2..0 one of the magnitudes 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6.  Scale byte s multiplies its 32 values by 2^(s - 127); s = 255 makes them
+ * NaN.  Used for weights (rows = out_features, k = in_features) and for
+ * activations (rows = tokens). */
+typedef struct {
+  const uint8_t *codes;  /* device, [rows, k/2], 16-byte aligned */
+  const uint8_t *scales; /* device, [rows, k/32], any alignment */
+  uint32_t rows;
+  uint32_t k; /* a multiple of 32, below 2^22; rows * k / 16 < 2^31 */
+} int8w_mxfp4;
+
+enum { INT8W_VALUES_BF16 = 0, INT8W_VALUES_F32 = 1 };
+
+/* mxfp4_quantize: BF16 or f32 values x [rows, k] (row-major, 16-byte aligned) ->
+ * codes and scales.  Per block of 32 with largest magnitude a:
+ *   s = max(E(a) - 2, 0), E(a) the 8-bit exponent field of a in f32 (so that
+ *   a / 2^(s-127) lies in [4, 8) for a >= 2^-124);
+ *   code = the one nearest to v / 2^(s-127), ties to the even code, magnitudes
+ *   above 6 to 6, the sign kept.
+ * A block that holds an infinity or a NaN gets s = 255 and codes 0.  rows = 0 is a
+ * no-op.  Errors: INT8W_ERR_NULL, INT8W_ERR_SHAPE (k zero, not a multiple of 32,
+ * or a size beyond the limits above), INT8W_ERR_UNSUPPORTED (x_format),
+ * INT8W_ERR_ALIGN (x, codes), INT8W_ERR_ALIAS (x, codes and scales must not
+ * overlap). */
+int int8w_mxfp4_quantize(const void *x, uint32_t x_format, uint32_t rows, uint32_t k, uint8_t *codes,
+                         uint8_t *scales, uint64_t stream);
+
+/* mxfp4_dequantize_to: out[r, j] = the value in BF16, [rows, k] row-major, 16-byte
+ * aligned.  Exact below 2^128 (RNE to infinity above: scale bytes 253 and 254). */
+int int8w_mxfp4_dequantize_to(const int8w_mxfp4 *w, uint16_t *out, uint64_t stream);
+
+/* mxfp4_gemm: Y = X W^T with BF16 X [m, k] and Y [m, rows], row-major:
+ * Y[i,n] = RNE_bf16(sum_j w[n,j] X[i,j]), exact products, accumulated in fp32.  Any
+ * m (m = 1: decode); m = 0 is a no-op.  The sum's order depends on m alone for a
+ * given weight shape: results are deterministic.  INT8W_ERR_SHAPE also when
+ * m * k or m * rows exceeds 2^32 - 1. */
+int int8w_mxfp4_gemm(const int8w_mxfp4 *w, const uint16_t *x, uint16_t *y, uint32_t m, uint64_t stream);
+
+/* mxfp4_gemm_mx: the same with X in MXFP4 as well (x->k == w->k; x->rows is m),
+ * e.g. from mxfp4_quantize: the products run on the 4-bit matrix cores. */
+int int8w_mxfp4_gemm_mx(const int8w_mxfp4 *w, const int8w_mxfp4 *x, uint16_t *y, uint64_t stream);
+
+/* ---- A whole mixture-of-experts layer for a few tokens.  For token t with router
+ * logits l [num_experts]:
+ *   p = softmax(l); the topk experts of largest l are taken, the lower index first
+ *   among equals; an expert at -inf is never taken (fewer than topk experts may
+ *   remain; with none, the sum below is empty);
+ *   r_j = routed_scale * p_j, or routed_scale * p_j / (sum of the taken p) with
+ *   renormalize; an expert whose r_j is zero is not run;
+ *   y[t] = RNE_bf16( x_resid[t] + sum_j r_j Wd_j (silu(Wg_j x_t) * (Wu_j x_t)) ).
+ * A token whose logits hold a NaN or +inf gets NaN outputs.
+ *   gate, up  [num_experts * inner, hidden], down [num_experts * hidden, inner]:
+ *             experts stacked along rows, expert e first row e * inner (e * hidden);
+ *   x         BF16 [tokens, hidden], 16-byte aligned;
+ *   logits    f32 or BF16 [tokens, num_experts] (logits_format), on the device;
+ *   x_resid   BF16 [tokens, hidden] or NULL; y may be x_resid itself;
+ *   y         BF16 [tokens, hidden].
+ * The product r_j silu(g) u is rounded to BF16 between the projections; everything
+ * else is fp32 until the one rounding of y.  Any number of tokens: they go in passes
+ * of 64, each of which streams the weights of the experts that its tokens take.
+ * workspace: device scratch, 256-byte aligned, of at least
+ * int8w_moe_workspace_bytes(tokens, topk, inner) bytes; no initial value, none kept;
+ * calls that share it must not overlap.  tokens = 0 is a no-op.
+ * Errors: INT8W_ERR_NULL; INT8W_ERR_SHAPE (shapes that do not fit each other or
+ * num_experts, num_experts above INT8W_MAX_MOE_EXPERTS, topk outside
+ * 1..min(num_experts, INT8W_MAX_MOE_TOPK), hidden or inner not below 2^20, different group sizes,
+ * a workspace too small); INT8W_ERR_UNSUPPORTED (logits_format); INT8W_ERR_ALIGN;
+ * INT8W_ERR_ALIAS (y or workspace overlapping an input or each other, but
+ * y == x_resid). */
+#define INT8W_MAX_MOE_EXPERTS 512
+#define INT8W_MAX_MOE_TOPK 16
+typedef struct {
+  const uint16_t *x;
+  const void *logits;
+  const uint16_t *x_resid;
+  uint16_t *y;
+  uint32_t tokens;
+  uint32_t topk;
+  uint32_t logits_format; /* INT8W_VALUES_F32 or INT8W_VALUES_BF16 */
+  uint32_t renormalize;   /* 0 or 1 */
+  float routed_scale;
+} int8w_moe_call;
+
+uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inner);
+int int8_moe_layer(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down, uint32_t num_experts,
+                   const int8w_moe_call *call, void *workspace, uint64_t workspace_bytes, uint64_t stream);
+int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down,
+                          uint32_t num_experts, const int8w_moe_call *call, void *workspace,
+                          uint64_t workspace_bytes, uint64_t stream);
+
 /* Source: "MlxInt8Weight", method gemv_silu_gate (kernel
  * mlx_int8_gemv_silu_gate: one launch, the gated product kept off memory).
  * gemv_silu_gate: y = W (silu(gate) * up) in one launch, silu(g) = g/(1+e^-g).

@@ -39,10 +39,14 @@ EXPORTED = (
     "int8w_validate", "int8w_storage_bytes", "int8_dequantize_to", "int8_gemv", "int8_gemv_silu_gate",
     "int8_gemv_silu_gate_resid", "int8_gemm", "int8_gemv_multi", "int8_quantize", "int8_moe_gemv",
     "int8w_fp8_gemv", "int8w_last_error", "int8_gemm_workspace_bytes", "int8_gemm_ws", "int8_gemm_noalloc",
+    "int8w_mxfp4_quantize", "int8w_mxfp4_dequantize_to", "int8w_mxfp4_gemm", "int8w_mxfp4_gemm_mx",
+    "int8w_moe_workspace_bytes", "int8_moe_layer", "int8w_mxfp4_moe_layer",
 )
 # calibration streams declared in include/int8w_measure.h
 EXPORTED_MEASURE = ("int8w_stream_read", "int8w_stream_copy", "int8w_stream_expand")
 FP8_PER_ROW, FP8_BLOCK_BF16, FP8_BLOCK_F32, FP8_SINGLE = 0, 1, 2, 3  # INT8W_FP8_*
+VALUES_BF16, VALUES_F32 = 0, 1  # INT8W_VALUES_*
+MAX_MOE_EXPERTS, MAX_MOE_TOPK = 512, 16  # INT8W_MAX_MOE_EXPERTS, INT8W_MAX_MOE_TOPK
 MAX_MULTI = 4  # INT8W_MAX_MULTI
 MAX_MOE_SLOTS = 65536  # INT8W_MAX_MOE_SLOTS
 
@@ -76,6 +80,31 @@ class Fp8WeightDesc(ctypes.Structure):
         ("scale_format", ctypes.c_uint32),
         ("block_size", ctypes.c_uint32),
         ("single_scale", ctypes.c_float),
+    ]
+
+
+class Mxfp4Desc(ctypes.Structure):
+    """Mirror of ``int8w_mxfp4`` (include/int8w.h)."""
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_uint32),
+        ("k", ctypes.c_uint32),
+    ]
+
+
+class MoeCall(ctypes.Structure):
+    """Mirror of ``int8w_moe_call`` (include/int8w.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("logits", ctypes.c_void_p),
+        ("x_resid", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("tokens", ctypes.c_uint32),
+        ("topk", ctypes.c_uint32),
+        ("logits_format", ctypes.c_uint32),
+        ("renormalize", ctypes.c_uint32),
+        ("routed_scale", ctypes.c_float),
     ]
 
 
@@ -127,6 +156,22 @@ def load_library() -> ctypes.CDLL:
     lib.int8_gemm_ws.restype = ctypes.c_int
     lib.int8_gemm_noalloc.argtypes = [W, P, P, ctypes.c_uint32, u64]
     lib.int8_gemm_noalloc.restype = ctypes.c_int
+    M = ctypes.POINTER(Mxfp4Desc)
+    C = ctypes.POINTER(MoeCall)
+    lib.int8w_mxfp4_quantize.argtypes = [P, u32, u32, u32, P, P, u64]
+    lib.int8w_mxfp4_quantize.restype = ctypes.c_int
+    lib.int8w_mxfp4_dequantize_to.argtypes = [M, P, u64]
+    lib.int8w_mxfp4_dequantize_to.restype = ctypes.c_int
+    lib.int8w_mxfp4_gemm.argtypes = [M, P, P, u32, u64]
+    lib.int8w_mxfp4_gemm.restype = ctypes.c_int
+    lib.int8w_mxfp4_gemm_mx.argtypes = [M, M, P, u64]
+    lib.int8w_mxfp4_gemm_mx.restype = ctypes.c_int
+    lib.int8w_moe_workspace_bytes.argtypes = [u32, u32, u32]
+    lib.int8w_moe_workspace_bytes.restype = u64
+    lib.int8_moe_layer.argtypes = [W, W, W, u32, C, P, u64, u64]
+    lib.int8_moe_layer.restype = ctypes.c_int
+    lib.int8w_mxfp4_moe_layer.argtypes = [M, M, M, u32, C, P, u64, u64]
+    lib.int8w_mxfp4_moe_layer.restype = ctypes.c_int
     lib.int8w_stream_read.argtypes = [P, u64, P, u64]
     lib.int8w_stream_read.restype = ctypes.c_int
     lib.int8w_stream_copy.argtypes = [P, P, u64, u64]
@@ -214,6 +259,36 @@ def int8w_stream_copy(src: int, dst: int, nbytes: int, stream: int) -> int:
 
 def int8w_stream_expand(src: int, dst: int, nbytes: int, stream: int) -> int:
     return load_library().int8w_stream_expand(src, dst, nbytes, stream)
+
+
+def int8w_mxfp4_quantize(x: int, x_format: int, rows: int, k: int, codes: int, scales: int, stream: int) -> int:
+    return load_library().int8w_mxfp4_quantize(x, x_format, rows, k, codes, scales, stream)
+
+
+def int8w_mxfp4_dequantize_to(desc: Mxfp4Desc, out: int, stream: int) -> int:
+    return load_library().int8w_mxfp4_dequantize_to(desc, out, stream)
+
+
+def int8w_mxfp4_gemm(desc: Mxfp4Desc, x: int, y: int, m: int, stream: int) -> int:
+    return load_library().int8w_mxfp4_gemm(desc, x, y, m, stream)
+
+
+def int8w_mxfp4_gemm_mx(desc: Mxfp4Desc, x: Mxfp4Desc, y: int, stream: int) -> int:
+    return load_library().int8w_mxfp4_gemm_mx(desc, x, y, stream)
+
+
+def int8w_moe_workspace_bytes(tokens: int, topk: int, inner: int) -> int:
+    return int(load_library().int8w_moe_workspace_bytes(tokens, topk, inner))
+
+
+def int8_moe_layer(gate: WeightDesc, up: WeightDesc, down: WeightDesc, num_experts: int, call: MoeCall, ws: int,
+                   ws_bytes: int, stream: int) -> int:
+    return load_library().int8_moe_layer(gate, up, down, num_experts, call, ws, ws_bytes, stream)
+
+
+def int8w_mxfp4_moe_layer(gate: Mxfp4Desc, up: Mxfp4Desc, down: Mxfp4Desc, num_experts: int, call: MoeCall, ws: int,
+                          ws_bytes: int, stream: int) -> int:
+    return load_library().int8w_mxfp4_moe_layer(gate, up, down, num_experts, call, ws, ws_bytes, stream)
 
 
 def int8_gemv_multi(descs, x: int, ys, stream: int) -> int:
@@ -473,3 +548,118 @@ class Fp8Weight:
         _need_bf16(y, "y", self.n, self.device)
         _check(int8w_fp8_gemv(self.desc, x.data_ptr(), y.data_ptr(), _stream_of(self.device)))
         return y
+
+
+class Mxfp4Weight:
+    """A matrix in MXFP4 on the GPU (borrowed tensors): a weight, or quantized activations.
+
+    codes:  uint8 [rows, k/2], element j in the low (j even) or high half of byte j/2
+    scales: uint8 [rows, k/32], a block of 32 is worth its codes times 2^(scale - 127)
+    """
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() != 2 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise ValueError("codes and scales must be 2-D uint8 tensors")
+        rows, k = codes.shape[0], 2 * codes.shape[1]
+        if k == 0 or k % 32:
+            raise ValueError(f"k {k} must be a positive multiple of 32")
+        if tuple(scales.shape) != (rows, k // 32):
+            raise ValueError(f"scales must be [{rows}, {k // 32}] = [rows, k/32]")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        if codes.device != scales.device or codes.device.type != "cuda":
+            raise ValueError("codes and scales must be on one GPU")
+        self.codes, self.scales = codes, scales
+        self.rows, self.k = rows, k
+        self.device = codes.device
+        self.desc = Mxfp4Desc(codes.data_ptr(), scales.data_ptr(), rows, k)
+
+    @classmethod
+    def quantize(cls, x: torch.Tensor) -> "Mxfp4Weight":
+        """Encode BF16 or float32 values [rows, k] on the GPU (int8w_mxfp4_quantize)."""
+        if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32) or not x.is_contiguous() \
+                or x.device.type != "cuda":
+            raise ValueError("x must be a contiguous 2-D bfloat16 or float32 GPU tensor")
+        rows, k = x.shape
+        if k == 0 or k % 32:
+            raise ValueError(f"k {k} must be a positive multiple of 32")
+        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((rows, k // 32), dtype=torch.uint8, device=x.device)
+        _check(int8w_mxfp4_quantize(x.data_ptr(), VALUES_F32 if x.dtype == torch.float32 else VALUES_BF16, rows, k,
+                                    codes.data_ptr(), scales.data_ptr(), _stream_of(x.device)))
+        return cls(codes, scales)
+
+    def dequantize_to(self, out: torch.Tensor | None = None) -> torch.Tensor:
+        if out is None:
+            out = torch.empty((self.rows, self.k), dtype=torch.bfloat16, device=self.device)
+        _need_bf16(out, "out", self.rows * self.k, self.device)
+        _check(int8w_mxfp4_dequantize_to(self.desc, out.data_ptr(), _stream_of(self.device)))
+        return out
+
+    def gemm(self, x: torch.Tensor, y: torch.Tensor | None = None) -> torch.Tensor:
+        """Y = X W^T for BF16 X [m, k] (m = 1: one token's decode)."""
+        if x.dim() != 2 or x.shape[1] != self.k:
+            raise ValueError(f"X must be [m, {self.k}]")
+        m = x.shape[0]
+        _need_bf16(x, "X", m * self.k, self.device)
+        if y is None:
+            y = torch.empty((m, self.rows), dtype=torch.bfloat16, device=self.device)
+        _need_bf16(y, "Y", m * self.rows, self.device)
+        _check(int8w_mxfp4_gemm(self.desc, x.data_ptr(), y.data_ptr(), m, _stream_of(self.device)))
+        return y
+
+    def gemm_mx(self, x: "Mxfp4Weight", y: torch.Tensor | None = None) -> torch.Tensor:
+        """Y = X W^T with both operands in MXFP4 (x e.g. from Mxfp4Weight.quantize)."""
+        if x.k != self.k:
+            raise ValueError(f"X must be [m, {self.k}]")
+        if x.device != self.device:
+            raise ValueError(f"X is on {x.device}, weight on {self.device}")
+        if y is None:
+            y = torch.empty((x.rows, self.rows), dtype=torch.bfloat16, device=self.device)
+        _need_bf16(y, "Y", x.rows * self.rows, self.device)
+        _check(int8w_mxfp4_gemm_mx(self.desc, x.desc, y.data_ptr(), _stream_of(self.device)))
+        return y
+
+
+def moe_layer(gate, up, down, num_experts: int, x: torch.Tensor, logits: torch.Tensor, topk: int,
+              renormalize: bool = True, routed_scale: float = 1.0, x_resid: torch.Tensor | None = None,
+              y: torch.Tensor | None = None) -> torch.Tensor:
+    """A mixture-of-experts layer for a few tokens (int8_moe_layer, int8w_mxfp4_moe_layer).
+
+    gate, up: num_experts experts of [inner, hidden] stacked along rows, all Int8Weight or all Mxfp4Weight
+    down:     num_experts experts of [hidden, inner], of the same kind
+    x:        bfloat16 [tokens, hidden]
+    logits:   float32 or bfloat16 [tokens, num_experts], the router's scores before the softmax
+    returns   bfloat16 [tokens, hidden]: x_resid + the weighted sum over the topk experts of each token.
+    Scratch comes from the device's cached workspace: calls that overlap on several streams would race.
+    """
+    mx = isinstance(gate, Mxfp4Weight)
+    kind = Mxfp4Weight if mx else Int8Weight
+    if not (isinstance(gate, kind) and isinstance(up, kind) and isinstance(down, kind)):
+        raise TypeError("gate, up and down must be three Int8Weight or three Mxfp4Weight")
+    dev = gate.device
+    if up.device != dev or down.device != dev:
+        raise ValueError("moe_layer: weights on different devices")
+    hidden, inner = (gate.k, down.k) if mx else (gate.in_features, down.in_features)
+    if x.dim() != 2 or x.shape[1] != hidden:
+        raise ValueError(f"x must be [tokens, {hidden}]")
+    T, E = x.shape[0], int(num_experts)
+    _need_bf16(x, "x", T * hidden, dev)
+    if logits.dtype not in (torch.float32, torch.bfloat16) or tuple(logits.shape) != (T, E) or logits.device != dev \
+            or not logits.is_contiguous():
+        raise ValueError(f"logits must be a contiguous float32 or bfloat16 [{T}, {E}] tensor on the weights' GPU")
+    if x_resid is not None:
+        _need_bf16(x_resid, "x_resid", T * hidden, dev)
+    if y is None:
+        y = torch.empty((T, hidden), dtype=torch.bfloat16, device=dev)
+    _need_bf16(y, "y", T * hidden, dev)
+    need = int8w_moe_workspace_bytes(T, topk, inner)
+    ws = _workspace(dev, need)
+    if ws is None:  # under graph capture: scratch of the graph's own
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    call = MoeCall(x.data_ptr(), logits.data_ptr(), x_resid.data_ptr() if x_resid is not None else None, y.data_ptr(),
+                   T, topk, VALUES_F32 if logits.dtype == torch.float32 else VALUES_BF16, int(bool(renormalize)),
+                   float(routed_scale))
+    layer = int8w_mxfp4_moe_layer if mx else int8_moe_layer
+    _check(layer(gate.desc, up.desc, down.desc, E, call, ws.data_ptr(), ws.numel(), _stream_of(dev)))
+    return y

@@ -485,3 +485,204 @@ int int8w_stream_expand(const void *src, void *dst, uint64_t bytes, uint64_t str
 }
 
 }  // extern "C"
+
+// ---- MXFP4 and the mixture-of-experts layer
+
+namespace int8w {
+namespace {
+
+int validate_mx(const int8w_mxfp4 *w, const char *what) {
+  if (!w) return fail(INT8W_ERR_NULL, "%s descriptor is NULL", what);
+  if (!w->codes || !w->scales) return fail(INT8W_ERR_NULL, "%s is missing a tensor (codes or scales is NULL)", what);
+  if (w->rows == 0 || w->k == 0) return fail(INT8W_ERR_SHAPE, "%s: zero dimension (rows=%u k=%u)", what, w->rows, w->k);
+  if (w->k % 32u != 0) return fail(INT8W_ERR_SHAPE, "%s: k %u is not a multiple of 32", what, w->k);
+  // 256 BF16 rows of a tile are addressed with 32-bit byte offsets below 2^31
+  if (w->k >= (1u << 22) || (uint64_t)w->rows * (w->k / 16u) > 0x7FFFFFFFull)
+    return fail(INT8W_ERR_SHAPE, "%s too large (%u x %u codes)", what, w->rows, w->k);
+  if (!aligned(w->codes, 16)) return fail(INT8W_ERR_ALIGN, "%s: codes is not 16-byte aligned", what);
+  return INT8W_OK;
+}
+
+MxView view(const int8w_mxfp4 *w) { return MxView{w->codes, w->scales, w->rows, w->k}; }
+
+void ranges_of(const int8w_mxfp4 *w, Range *r, const char *codes = "codes", const char *scales = "scales") {
+  r[0] = range(codes, w->codes, (uint64_t)w->rows * (w->k / 2u));
+  r[1] = range(scales, w->scales, (uint64_t)w->rows * (w->k / 32u));
+}
+
+// The checks that both expert formats share.  ins: the three weights' ranges.
+int check_moe(uint64_t gate_rows, uint32_t hidden, uint64_t up_rows, uint32_t up_k, uint64_t down_rows, uint32_t inner,
+              uint32_t num_experts, const int8w_moe_call *c, void *ws, uint64_t ws_bytes, Range *ins, int n_ins) {
+  if (!c) return fail(INT8W_ERR_NULL, "call is NULL");
+  if (num_experts == 0 || num_experts > INT8W_MAX_MOE_EXPERTS)
+    return fail(INT8W_ERR_SHAPE, "num_experts %u outside 1..%d", num_experts, INT8W_MAX_MOE_EXPERTS);
+  if (up_rows != gate_rows || up_k != hidden) return fail(INT8W_ERR_SHAPE, "up is not of gate's shape");
+  if (gate_rows != (uint64_t)num_experts * inner || down_rows != (uint64_t)num_experts * hidden)
+    return fail(INT8W_ERR_SHAPE, "gate has %llu rows and down %llu, not %u experts of inner %u and hidden %u",
+                (unsigned long long)gate_rows, (unsigned long long)down_rows, num_experts, inner, hidden);
+  if (hidden >= (1u << 20) || inner >= (1u << 20))
+    return fail(INT8W_ERR_SHAPE, "hidden %u or inner %u is not below 2^20", hidden, inner);
+  if (c->topk == 0 || c->topk > INT8W_MAX_MOE_TOPK || c->topk > num_experts)
+    return fail(INT8W_ERR_SHAPE, "topk %u outside 1..min(%u experts, %d)", c->topk, num_experts, INT8W_MAX_MOE_TOPK);
+  if (c->logits_format > INT8W_VALUES_F32)
+    return fail(INT8W_ERR_UNSUPPORTED, "unknown logits_format %u", c->logits_format);
+  if (c->tokens == 0) return INT8W_OK;
+  const uint64_t T = c->tokens;
+  const uint32_t el = c->logits_format == INT8W_VALUES_F32 ? 4 : 2;
+  if (!c->x || !c->logits || !c->y || !ws) return fail(INT8W_ERR_NULL, "x, logits, y or workspace is NULL");
+  if (!aligned(c->x, 16)) return fail(INT8W_ERR_ALIGN, "x is not 16-byte aligned");
+  if (!aligned(c->logits, el)) return fail(INT8W_ERR_ALIGN, "logits is not %u-byte aligned", el);
+  if (!aligned(c->y, 2) || !aligned(c->x_resid, 2)) return fail(INT8W_ERR_ALIGN, "y/x_resid are not 2-byte aligned");
+  if (!aligned(ws, 256)) return fail(INT8W_ERR_ALIGN, "workspace is not 256-byte aligned");
+  const uint64_t need = int8w_moe_workspace_bytes(c->tokens, c->topk, inner);
+  if (ws_bytes < need)
+    return fail(INT8W_ERR_SHAPE, "workspace of %llu bytes, this call needs %llu", (unsigned long long)ws_bytes,
+                (unsigned long long)need);
+  ins[n_ins++] = range("x", c->x, T * hidden * 2);
+  ins[n_ins++] = range("logits", c->logits, T * num_experts * el);
+  const Range y = range("y", c->y, T * hidden * 2), work = range("workspace", ws, need);
+  const Range resid = range("x_resid", c->x_resid, T * hidden * 2);
+  if (c->x_resid && c->x_resid != c->y) {
+    int rc = check_alias(y, &resid, 1);
+    if (rc) return rc;
+  }
+  int rc = check_alias(y, ins, n_ins);
+  if (!rc) rc = check_alias(work, ins, n_ins);
+  if (!rc) rc = check_alias(work, &y, 1);
+  if (!rc && c->x_resid) rc = check_alias(work, &resid, 1);
+  return rc;
+}
+
+MoeArgs moe_args(const int8w_moe_call *c, uint32_t E, void *ws) {
+  return MoeArgs{E, c->x, c->logits, c->logits_format == INT8W_VALUES_BF16, c->tokens, c->topk, c->renormalize != 0,
+                 c->routed_scale, c->x_resid, c->y, ws};
+}
+
+}  // namespace
+}  // namespace int8w
+
+extern "C" {
+
+int int8w_mxfp4_quantize(const void *x, uint32_t x_format, uint32_t rows, uint32_t k, uint8_t *codes,
+                         uint8_t *scales, uint64_t stream) {
+  if (x_format > INT8W_VALUES_F32) return fail(INT8W_ERR_UNSUPPORTED, "unknown x_format %u", x_format);
+  if (rows == 0 && k != 0 && k % 32u == 0) return ok();
+  const int8w_mxfp4 out = {codes, scales, rows, k};
+  int rc = validate_mx(&out, "output");
+  if (rc) return rc;
+  if (!x) return fail(INT8W_ERR_NULL, "x is NULL");
+  if (!aligned(x, 16)) return fail(INT8W_ERR_ALIGN, "x is not 16-byte aligned");
+  Range outs[2];
+  ranges_of(&out, outs);
+  const Range in = range("x", x, (uint64_t)rows * k * (x_format == INT8W_VALUES_F32 ? 4 : 2));
+  for (const Range &o : outs) {
+    rc = check_alias(o, &in, 1);
+    if (rc) return rc;
+  }
+  if (overlaps(outs[0], outs[1])) return fail(INT8W_ERR_ALIAS, "outputs codes and scales overlap");
+  (void)hipGetLastError();
+  return finish_launch(launch_mx_quantize(x, x_format == INT8W_VALUES_F32, rows, k, codes, scales, as_stream(stream)),
+                       as_stream(stream));
+}
+
+int int8w_mxfp4_dequantize_to(const int8w_mxfp4 *w, uint16_t *out, uint64_t stream) {
+  int rc = validate_mx(w, "weight");
+  if (rc) return rc;
+  if (!out) return fail(INT8W_ERR_NULL, "out is NULL");
+  if (!aligned(out, 16)) return fail(INT8W_ERR_ALIGN, "out is not 16-byte aligned");
+  Range ins[2];
+  ranges_of(w, ins);
+  rc = check_alias(range("out", out, (uint64_t)w->rows * w->k * 2), ins, 2);
+  if (rc) return rc;
+  (void)hipGetLastError();
+  return finish_launch(launch_mx_dequantize(view(w), out, as_stream(stream)), as_stream(stream));
+}
+
+int int8w_mxfp4_gemm(const int8w_mxfp4 *w, const uint16_t *x, uint16_t *y, uint32_t m, uint64_t stream) {
+  int rc = validate_mx(w, "weight");
+  if (rc) return rc;
+  if (m == 0) return ok();
+  if (!x || !y) return fail(INT8W_ERR_NULL, "X or Y is NULL");
+  if (!aligned(x, 16)) return fail(INT8W_ERR_ALIGN, "X is not 16-byte aligned");
+  if (!aligned(y, 2)) return fail(INT8W_ERR_ALIGN, "Y is not 2-byte aligned");
+  if ((uint64_t)m * w->k > 0xFFFFFFFFull || (uint64_t)m * w->rows > 0xFFFFFFFFull)
+    return fail(INT8W_ERR_SHAPE, "m=%u rows too many for this weight", m);
+  Range ins[3];
+  ranges_of(w, ins);
+  ins[2] = range("X", x, (uint64_t)m * w->k * 2);
+  rc = check_alias(range("Y", y, (uint64_t)m * w->rows * 2), ins, 3);
+  if (rc) return rc;
+  (void)hipGetLastError();
+  return finish_launch(launch_mx_gemm(view(w), x, y, m, as_stream(stream)), as_stream(stream));
+}
+
+int int8w_mxfp4_gemm_mx(const int8w_mxfp4 *w, const int8w_mxfp4 *x, uint16_t *y, uint64_t stream) {
+  int rc = validate_mx(w, "weight");
+  if (rc) return rc;
+  if (!x) return fail(INT8W_ERR_NULL, "X descriptor is NULL");
+  if (x->k != w->k) return fail(INT8W_ERR_SHAPE, "X has k=%u, the weight %u", x->k, w->k);
+  if (x->rows == 0) return ok();
+  rc = validate_mx(x, "X");
+  if (rc) return rc;
+  if (!y) return fail(INT8W_ERR_NULL, "Y is NULL");
+  if (!aligned(y, 2)) return fail(INT8W_ERR_ALIGN, "Y is not 2-byte aligned");
+  if ((uint64_t)x->rows * w->rows > 0xFFFFFFFFull)
+    return fail(INT8W_ERR_SHAPE, "m=%u rows too many for this weight", x->rows);
+  Range ins[4];
+  ranges_of(w, ins);
+  ranges_of(x, ins + 2, "X codes", "X scales");
+  rc = check_alias(range("Y", y, (uint64_t)x->rows * w->rows * 2), ins, 4);
+  if (rc) return rc;
+  (void)hipGetLastError();
+  return finish_launch(launch_mx_gemm_mx(view(w), view(x), y, as_stream(stream)), as_stream(stream));
+}
+
+uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inner) {
+  if (tokens == 0) return 0;
+  const uint64_t slots = (uint64_t)(tokens < kMoePassTokens ? tokens : kMoePassTokens) * topk;
+  return kMoeHeadBytes + slots * inner * 2u;
+}
+
+int int8_moe_layer(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down, uint32_t num_experts,
+                   const int8w_moe_call *call, void *workspace, uint64_t workspace_bytes, uint64_t stream) {
+  const int8w_weight *w[3] = {gate, up, down};
+  Range ins[11];
+  for (int i = 0; i < 3; ++i) {
+    int rc = validate(w[i]);
+    if (rc) return rc;
+    if (w[i]->group_size != gate->group_size)
+      return fail(INT8W_ERR_SHAPE, "gate, up and down have different group sizes");
+    weight_ranges(w[i], ins + 3 * i);
+  }
+  int rc = check_moe(gate->out_features, gate->in_features, up->out_features, up->in_features, down->out_features,
+                     down->in_features, num_experts, call, workspace, workspace_bytes, ins, 9);
+  if (rc) return rc;
+  if (call->tokens == 0) return ok();
+  (void)hipGetLastError();
+  return finish_launch(launch_moe_int8(view(gate), view(up), view(down), moe_args(call, num_experts, workspace),
+                                       as_stream(stream)),
+                       as_stream(stream));
+}
+
+int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down,
+                          uint32_t num_experts, const int8w_moe_call *call, void *workspace,
+                          uint64_t workspace_bytes, uint64_t stream) {
+  const int8w_mxfp4 *w[3] = {gate, up, down};
+  const char *const names[3] = {"gate", "up", "down"};
+  Range ins[8];
+  for (int i = 0; i < 3; ++i) {
+    int rc = validate_mx(w[i], names[i]);
+    if (rc) return rc;
+    ranges_of(w[i], ins + 2 * i);
+  }
+  int rc = check_moe(gate->rows, gate->k, up->rows, up->k, down->rows, down->k, num_experts, call, workspace,
+                     workspace_bytes, ins, 6);
+  if (rc) return rc;
+  if (call->tokens == 0) return ok();
+  (void)hipGetLastError();
+  return finish_launch(launch_moe_mx(view(gate), view(up), view(down), moe_args(call, num_experts, workspace),
+                                     as_stream(stream)),
+                       as_stream(stream));
+}
+
+}  // extern "C"

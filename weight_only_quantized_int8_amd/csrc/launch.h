@@ -94,6 +94,39 @@ hipError_t launch_stream_read(const void *src, uint64_t bytes, uint32_t *sink, h
 hipError_t launch_stream_copy(const void *src, void *dst, uint64_t bytes, hipStream_t stream);
 hipError_t launch_stream_expand(const void *src, void *dst, uint64_t bytes, hipStream_t stream);
 
+// ---- MXFP4 (mxfp4.h): codes [N, K/2], scales [N, K/32], K a multiple of 32
+struct MxView {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  uint32_t N, K;
+};
+// BF16 (or f32) values [rows, K] -> codes, scales; and codes, scales -> BF16 values.
+hipError_t launch_mx_quantize(const void *x, bool f32, uint32_t rows, uint32_t K, uint8_t *codes, uint8_t *scales,
+                              hipStream_t stream);
+hipError_t launch_mx_dequantize(const MxView &w, uint16_t *out, hipStream_t stream);
+// Y[m, N] = X[m, K] W^T, X BF16; and X [x.N, K] in MXFP4.
+hipError_t launch_mx_gemm(const MxView &w, const uint16_t *x, uint16_t *y, uint32_t m, hipStream_t stream);
+hipError_t launch_mx_gemm_mx(const MxView &w, const MxView &x, uint16_t *y, hipStream_t stream);
+
+// ---- mixture-of-experts layer: gate and up [E I, H], down [E H, I] stacked by expert
+constexpr uint32_t kMoePassTokens = 64;         // tokens of one pass over the experts
+constexpr uint64_t kMoeHeadBytes = 80u << 10;   // routing tables at the head of the workspace
+struct MoeArgs {
+  uint32_t E;
+  const uint16_t *x;    // [tokens, H]
+  const void *logits;   // [tokens, E], f32 or BF16
+  bool logits_bf16;
+  uint32_t tokens, topk;
+  bool renorm;
+  float scale;
+  const uint16_t *resid;  // [tokens, H] or nullptr
+  uint16_t *y;            // [tokens, H]
+  void *ws;               // head, then h [min(tokens, kMoePassTokens) topk, I] BF16
+};
+hipError_t launch_moe_int8(const WeightView &gate, const WeightView &up, const WeightView &down, const MoeArgs &m,
+                           hipStream_t stream);
+hipError_t launch_moe_mx(const MxView &gate, const MxView &up, const MxView &down, const MoeArgs &m, hipStream_t stream);
+
 // ---- C-ABI internals shared by capi.cpp and noalloc.hip
 // Records the calling thread's last error message and returns code.
 int report_error(int code, const char *fmt, ...);

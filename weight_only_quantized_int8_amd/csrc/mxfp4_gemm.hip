@@ -1,0 +1,365 @@
+// mxfp4_gemm.hip -- Y[m, N] = X[m, K] W^T with W in MXFP4 (mxfp4.h) and X in
+// BF16 (weight-only) or in MXFP4 too.  fp32 accumulation, one rounding to BF16.
+//
+// m <= kMxRowsMax: HBM-bound, the weight is streamed once for all rows
+//   (k_mx_rows): a workgroup owns 16 weight rows, its waves split K chunk by
+//   chunk and load weight codes, scales and the matching activations straight
+//   into matrix-core operands (rows_stream.h); no staging, no barrier until the
+//   waves' partial sums meet in LDS in wave order.
+// more rows: a tiled kernel (k_mx_tile) on bf16 MFMA (X BF16: codes are
+//   converted with their scale in registers, exactly) or on the scaled fp4 MFMA
+//   (both MXFP4: 16 x 16 x 128 products with a scale per 32 k in the
+//   instruction).
+#include "rows_stream.h"
+#include "launch.h"
+
+namespace int8w {
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x4 mfma_mx(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
+  // fp4 operands take the first four registers of eight
+  const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// ---- few rows ---------------------------------------------------------------------------------
+
+// The activations of MT token tiles as they enter the products: BF16 rows, or MXFP4 rows.
+template <bool XMX, int MT>
+struct RowsX;
+
+template <int MT>
+struct RowsX<false, MT> {
+  struct Frag {
+    XFrag x[MT];
+  };
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t xo[MT];
+  __device__ __forceinline__ RowsX(const void *x, const uint8_t *, uint32_t m, uint32_t K, uint32_t lane) {
+    r = make_rsrc(x, m * K * 2u);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) xo[mt] = 16u * mt + (lane & 15u) < m ? (16u * mt + (lane & 15u)) * K * 2u : kOutOfRange;
+  }
+  __device__ __forceinline__ void load(Frag &f, uint32_t c, uint32_t K, uint32_t lane) const {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) MxFmt::load_x(f.x[mt], r, xo[mt], c, K, lane);
+  }
+  static __device__ __forceinline__ void mac(f32x4 (&acc)[MT], const MxFmt::Frag &w, const Frag &f) {
+    const f32x4 none[MT][4] = {};
+    MxFmt::mac<MT>(acc, w, f.x, none);
+  }
+};
+
+template <int MT>
+struct RowsX<true, MT> {
+  struct Frag {
+    MxFmt::Frag x[MT];
+  };
+  MxView v;
+  MxFmt::Tile t[MT];
+  __device__ __forceinline__ RowsX(const void *x, const uint8_t *scales, uint32_t m, uint32_t K, uint32_t lane) {
+    v = MxView{(const uint8_t *)x, scales, m, K};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) t[mt] = MxFmt::tile(v, 0, 16u * mt < m ? 16u * mt : m - 1u, m, lane);
+  }
+  __device__ __forceinline__ void load(Frag &f, uint32_t c, uint32_t, uint32_t lane) const {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) MxFmt::load(f.x[mt], t[mt], v, c, lane);
+  }
+  static __device__ __forceinline__ void mac(f32x4 (&acc)[MT], const MxFmt::Frag &w, const Frag &f) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_mx(f.x[mt].q, f.x[mt].s, w.q, w.s, acc[mt]);
+  }
+};
+
+template <bool XMX, int KS, int U, int MT>
+__global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
+                                                     const uint8_t *__restrict__ xs, uint32_t m,
+                                                     uint16_t *__restrict__ y) {
+  __shared__ __attribute__((aligned(16))) float red[KS * MT * 256];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), n0 = 16u * blockIdx.x, K = w.K;
+  const MxFmt::Tile t = MxFmt::tile(w, 0, n0, w.N, lane);
+  const RowsX<XMX, MT> X(x, xs, m, K, lane);
+  struct Ring {
+    MxFmt::Frag w;
+    typename RowsX<XMX, MT>::Frag x;
+  } r[U];
+  const uint32_t nc = (K + kChunk - 1u) / kChunk;
+  auto load = [&](Ring &b, uint32_t c) {
+    MxFmt::load(b.w, t, w, c, lane);
+    X.load(b.x, c, K, lane);
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
+  for (uint32_t c = wave; c < nc; c += KS * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      RowsX<XMX, MT>::mac(acc, r[u].w, r[u].x);
+      load(r[u], c + KS * (U + u));
+    }
+  }
+  f32x4 *out = reinterpret_cast<f32x4 *>(red) + wave * MT * 64u + lane;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) out[mt * 64] = acc[mt];
+  __syncthreads();
+  for (uint32_t o = threadIdx.x; o < 256u * MT; o += 64u * KS) {
+    const uint32_t row = o & 15u, tok = o >> 4;
+    if (tok < m && n0 + row < w.N) {
+      const uint32_t at = ((tok >> 4) * 64u + ((tok & 15u) >> 2) * 16u + row) * 4u + (tok & 3u);
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) v += red[i * MT * 256 + at];
+      y[(size_t)tok * w.N + n0 + row] = to_bf16_bits(v);
+    }
+  }
+}
+
+// ---- many rows --------------------------------------------------------------------------------
+
+// Tile BM rows of X times BN weight rows, WM x WN waves.  Both operands are
+// copied to LDS by DMA, two stages, a step of CH chunks each; 16-byte pieces of a
+// row are XOR-swizzled so that the rows of an operand read fall into distinct
+// banks.  A = weight rows, B = X rows: a lane's four results are neighbours in Y.
+template <bool XMX, int BM, int BN, int WM, int WN, int CH>
+struct MxTile {
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16-row tiles a wave
+  static constexpr uint32_t XB = (XMX ? 64u : 256u) * CH;     // bytes of an X row in a step
+  static constexpr uint32_t WB = 64u * CH;
+  static constexpr uint32_t X_BYTES = BM * XB, W_BYTES = BN * WB, STAGE = X_BYTES + W_BYTES;
+  static constexpr int NX = (int)(X_BYTES / 1024u / kWaves), NW = (int)(W_BYTES / 1024u / kWaves);
+  static_assert(X_BYTES % (1024u * kWaves) == 0 && W_BYTES % (1024u * kWaves) == 0, "whole loads a wave");
+};
+
+// piece index -> swizzled piece, rows of P 16-byte pieces
+template <uint32_t P>
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t c) {
+  if constexpr (P >= 16u) return c ^ (row & 15u);
+  if constexpr (P == 8u) return c ^ (row & 7u);
+  return c ^ ((row >> 1) & 3u);
+}
+
+template <bool XMX, int BM, int BN, int WM, int WN, int CH>
+__global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_t *__restrict__ x,
+                                                          const uint8_t *__restrict__ xs, uint32_t m,
+                                                          uint16_t *__restrict__ y, uint32_t mt_count) {
+  using S = MxTile<XMX, BM, BN, WM, WN, CH>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_mx[];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform32(tid >> 6), lr = lane & 15u, g = lane >> 4;
+  const uint32_t wm = wave % WM, wn = wave / WM, K = w.K;
+  // workgroups are dealt to the 8 XCDs in turn: give each XCD neighbouring tiles, X tiles of one weight tile first
+  const uint32_t total = gridDim.x, per = total / 8u, extra = total % 8u, xcd = blockIdx.x % 8u;
+  const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / 8u;
+  const uint32_t m0 = (id % mt_count) * BM, n0 = (id / mt_count) * BN;
+  const uint32_t mrows = m - m0 < BM ? m - m0 : BM, nrows = w.N - n0 < BN ? w.N - n0 : BN;
+  const uint32_t xrow = XMX ? K / 2u : K * 2u, wrow = K / 2u;  // bytes a row
+  const auto rx = make_rsrc(x + (size_t)m0 * xrow, mrows * xrow);
+  const auto rw = make_rsrc(w.codes + (size_t)n0 * wrow, nrows * wrow);
+  const auto rws = make_rsrc(w.scales + (size_t)n0 * (K / 32u), nrows * (K / 32u));
+  const auto rxs = make_rsrc(XMX ? xs + (size_t)m0 * (K / 32u) : w.scales, XMX ? mrows * (K / 32u) : 0u);
+
+  uint32_t vx[S::NX], vw[S::NW];  // byte offset of this lane's piece at step 0
+  uint32_t px[S::NX], pw[S::NW];  // ... and within its row's step
+#pragma unroll
+  for (int j = 0; j < S::NX; ++j) {
+    const uint32_t slot = (wave * S::NX + j) * 64u + lane, row = slot / (S::XB / 16u);
+    px[j] = 16u * swz<S::XB / 16u>(row, slot % (S::XB / 16u));
+    vx[j] = row < mrows ? row * xrow + px[j] : kOutOfRange;
+  }
+#pragma unroll
+  for (int j = 0; j < S::NW; ++j) {
+    const uint32_t slot = (wave * S::NW + j) * 64u + lane, row = slot / (S::WB / 16u);
+    pw[j] = 16u * swz<S::WB / 16u>(row, slot % (S::WB / 16u));
+    vw[j] = row < nrows ? row * wrow + pw[j] : kOutOfRange;
+  }
+  auto dma = [&](uint32_t step, uint8_t *base) {
+#pragma unroll
+    for (int j = 0; j < S::NX; ++j) {
+      const bool in = step * S::XB + px[j] < xrow;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (__attribute__((address_space(3))) void *)(base + (wave * S::NX + j) * 1024u),
+                                               16, (int)(in ? vx[j] + step * S::XB : kOutOfRange), 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < S::NW; ++j) {
+      const bool in = step * S::WB + pw[j] < wrow;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rw, (__attribute__((address_space(3))) void *)(base + S::X_BYTES + (wave * S::NW + j) * 1024u), 16,
+          (int)(in ? vw[j] + step * S::WB : kOutOfRange), 0, 0, 0);
+    }
+  };
+  // scale bytes of a step: one per lane, chunk and 16-row tile, straight to registers
+  struct Scales {
+    uint32_t w[CH][S::TN], x[XMX ? CH : 1][XMX ? S::TM : 1];
+  };
+  auto scales = [&](Scales &s, uint32_t step) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t blk = 4u * (step * CH + c) + g;
+      const bool in = blk < K / 32u;
+#pragma unroll
+      for (int t = 0; t < S::TN; ++t) {
+        const uint32_t row = (wn * S::TN + t) * 16u + lr;
+        s.w[c][t] = __builtin_amdgcn_raw_buffer_load_b8(rws, (int)(in && row < nrows ? row * (K / 32u) + blk : kOutOfRange), 0, 0);
+      }
+      if constexpr (XMX)
+#pragma unroll
+        for (int t = 0; t < S::TM; ++t) {
+          const uint32_t row = (wm * S::TM + t) * 16u + lr;
+          s.x[c][t] = __builtin_amdgcn_raw_buffer_load_b8(rxs, (int)(in && row < mrows ? row * (K / 32u) + blk : kOutOfRange), 0, 0);
+        }
+    }
+  };
+  f32x4 acc[S::TN][S::TM];
+#pragma unroll
+  for (int i = 0; i < S::TN; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const Scales &s, const uint8_t *base) {
+    const uint8_t *xb = base, *wb = base + S::X_BYTES;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if constexpr (XMX) {
+        u32x4 b[S::TM];
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j) {
+          const uint32_t row = (wm * S::TM + j) * 16u + lr;
+          b[j] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 4u * c + g));
+        }
+#pragma unroll
+        for (int i = 0; i < S::TN; ++i) {
+          const uint32_t row = (wn * S::TN + i) * 16u + lr;
+          const u32x4 a = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
+#pragma unroll
+          for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma_mx(a, s.w[c][i], b[j], s.x[c][j], acc[i][j]);
+        }
+      } else {
+        u32x4 b[S::TM][4];
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j) {
+          const uint32_t row = (wm * S::TM + j) * 16u + lr;
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            b[j][f] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 16u * c + 4u * g + f));
+        }
+#pragma unroll
+        for (int i = 0; i < S::TN; ++i) {
+          const uint32_t row = (wn * S::TN + i) * 16u + lr;
+          const u32x4 q = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
+          const float sc = mx_scale_f32(s.w[c][i]);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const uint4 a = mx_to_bf16x8(q[f], sc);
+#pragma unroll
+            for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma16(u32x4{a.x, a.y, a.z, a.w}, b[j][f], acc[i][j]);
+          }
+        }
+      }
+    }
+  };
+
+  const uint32_t steps = (K + kChunk * CH - 1u) / (kChunk * CH);
+  Scales s0, s1;
+  dma(0, lds_mx);
+  scales(s0, 0);
+  // One barrier a step.  Before it every wave has waited for its own loads of the
+  // next step (all of them: DMA and register loads are never counted apart) and
+  // has read its operands of this one, so after it the next stage is whole and
+  // this one may be filled again.
+  auto sync = [&]() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+  sync();
+  for (uint32_t s = 0;;) {
+    if (s + 1u < steps) {
+      dma(s + 1u, lds_mx + S::STAGE);
+      scales(s1, s + 1u);
+    }
+    compute(s0, lds_mx);
+    if (++s >= steps) break;
+    sync();
+    if (s + 1u < steps) {
+      dma(s + 1u, lds_mx);
+      scales(s0, s + 1u);
+    }
+    compute(s1, lds_mx + S::STAGE);
+    if (++s >= steps) break;
+    sync();
+  }
+  // D[4 g + r][lr]: weight row 4 g + r, X row lr
+  const bool wide = w.N % 4u == 0u && (reinterpret_cast<uintptr_t>(y) & 7u) == 0u;
+#pragma unroll
+  for (int j = 0; j < S::TM; ++j) {
+    const uint32_t row = (wm * S::TM + j) * 16u + lr;
+    if (row >= mrows) continue;
+    uint16_t *yr = y + (size_t)(m0 + row) * w.N + n0;
+#pragma unroll
+    for (int i = 0; i < S::TN; ++i) {
+      const uint32_t n = (wn * S::TN + i) * 16u + 4u * g;
+      const f32x4 v = acc[i][j];
+      if (wide) {
+        if (n < nrows) *reinterpret_cast<uint2 *>(yr + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (uint32_t r = 0; r < 4u; ++r)
+          if (n + r < nrows) yr[n + r] = to_bf16_bits(v[r]);
+      }
+    }
+  }
+}
+
+template <bool XMX, int MT>
+hipError_t launch_rows(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  const uint32_t tiles = (w.N + 15u) / 16u, nc = (w.K + kChunk - 1u) / kChunk;
+  constexpr int U = XMX ? (MT <= 2 ? 4 : 2) : (MT == 1 ? 4 : 2);
+  if (nc >= 64u && tiles <= 512u)
+    k_mx_rows<XMX, 16, (MT <= 2 ? U : 1), MT><<<tiles, 1024, 0, stream>>>(w, x, xs, m, y);
+  else if (nc >= 16u)
+    k_mx_rows<XMX, 8, U, MT><<<tiles, 512, 0, stream>>>(w, x, xs, m, y);
+  else
+    k_mx_rows<XMX, 4, U, MT><<<tiles, 256, 0, stream>>>(w, x, xs, m, y);
+  return hipGetLastError();
+}
+
+template <bool XMX, int BM, int BN, int WM, int WN, int CH>
+hipError_t launch_tile(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  using S = MxTile<XMX, BM, BN, WM, WN, CH>;
+  const uint32_t mt = (m + BM - 1u) / BM, nt = (w.N + BN - 1u) / BN;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<XMX, BM, BN, WM, WN, CH>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)(2u * S::STAGE));
+  if (e != hipSuccess) return e;
+  k_mx_tile<XMX, BM, BN, WM, WN, CH><<<mt * nt, S::kThreads, 2u * S::STAGE, stream>>>(w, (const uint8_t *)x, xs, m, y, mt);
+  return hipGetLastError();
+}
+
+template <bool XMX>
+hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  if (m <= 16u) return launch_rows<XMX, 1>(w, x, xs, m, y, stream);
+  if (m <= 32u) return launch_rows<XMX, 2>(w, x, xs, m, y, stream);
+  if (m <= 64u) return launch_rows<XMX, 4>(w, x, xs, m, y, stream);
+  const uint32_t big = XMX ? ((m + 255u) / 256u) * ((w.N + 255u) / 256u) : ((m + 127u) / 128u) * ((w.N + 255u) / 256u);
+  if (big < (uint32_t)device_cu_count() / 2u) return launch_tile<XMX, 64, 64, 2, 2, XMX ? 2 : 1>(w, x, xs, m, y, stream);
+  if constexpr (XMX)
+    return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
+  else
+    return launch_tile<false, 128, 256, 2, 2, 1>(w, x, xs, m, y, stream);
+}
+
+}  // namespace
+
+hipError_t launch_mx_gemm(const MxView &w, const uint16_t *x, uint16_t *y, uint32_t m, hipStream_t stream) {
+  return launch_any<false>(w, x, nullptr, m, y, stream);
+}
+
+hipError_t launch_mx_gemm_mx(const MxView &w, const MxView &x, uint16_t *y, hipStream_t stream) {
+  return launch_any<true>(w, x.codes, x.scales, x.N, y, stream);
+}
+
+}  // namespace int8w
