@@ -110,7 +110,7 @@ hipError_t launch_mx_gemm_mx(const MxView &w, const MxView &x, uint16_t *y, hipS
 
 // ---- mixture-of-experts layer: gate and up [E I, H], down [E H, I] stacked by expert
 constexpr uint32_t kMoePassTokens = 64;         // tokens of one pass over the experts
-constexpr uint64_t kMoeHeadBytes = 80u << 10;   // routing tables at the head of the workspace
+constexpr uint64_t kMoeHeadBytes = 48u << 10;   // routing tables at the head of the workspace
 struct MoeArgs {
   uint32_t E;
   const uint16_t *x;    // [tokens, H]

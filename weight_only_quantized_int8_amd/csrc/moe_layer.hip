@@ -6,23 +6,21 @@
 //   y[t] = x_resid[t] + sum_j r_j  Wd_j ( silu(Wg_j x_t) * (Wu_j x_t) ).
 //
 // Three launches on one stream, up to 64 tokens a pass:
-//  k_moe_route   one workgroup: each wave takes tokens, and the result is written
-//                as one list of the experts that any token takes, with a table
-//                slot[a][t] (1 + the slot t*topk + j that takes active expert a,
-//                0: none) and the slots' weights.
-//  k_moe_up      workgroup (active expert, 16 inner rows): gate and up rows are
-//                streamed once for all the expert's tokens (rows_stream.h); the
-//                epilogue writes h[slot] = r * silu(g) * u.
-//  k_moe_down    workgroup (16 output rows): the chosen experts' down rows one
-//                after the other into the same fp32 accumulators, so the weighted
-//                sum over experts needs no second pass and no atomics; the rows
-//                of A are the tokens, and a token that does not take the expert
-//                at hand has zeros there.
-// Bound: HBM, each chosen expert's three matrices once.
+//  k_moe_route   one workgroup: each wave takes tokens.  Its result is a list of
+//                segments: an expert and up to C of the slots (t, j) that take it.
+//  k_moe_up      workgroup (segment, 16 inner rows): gate and up rows are streamed
+//                once for all the segment's tokens (rows_stream.h); the epilogue
+//                writes h[slot] = r * silu(g) * u.
+//  k_moe_down    workgroup (16 output rows): the segments' down rows one after the
+//                other, the waves sharing the list evenly; a wave adds a segment's
+//                products to its own fp32 sums by token, so the weighted sum over
+//                experts needs no atomics and no further pass.
+// Bound: HBM, each chosen expert's three matrices once.  An expert with more than C
+// tokens has several segments, whose further reads of its rows come from the caches.
 //
-// h is kept in BF16 (the matrix cores' operand type): its relative rounding of
-// 2^-9 per value averages out over the inner sum to less than the output's own
-// BF16 rounding.  All sums, the softmax and the routing weights are fp32.
+// h is kept in BF16 (the matrix cores' operand type): its relative rounding of at
+// most 2^-9 a value averages out over the inner sum to about the output's own BF16
+// rounding.  All sums, the softmax and the routing weights are fp32.
 #include "rows_stream.h"
 #include "launch.h"
 
@@ -33,15 +31,20 @@ namespace {
 constexpr uint32_t kTok = kMoePassTokens;  // tokens a pass
 constexpr uint32_t kMaxE = INT8W_MAX_MOE_EXPERTS;
 constexpr uint32_t kMaxTopk = INT8W_MAX_MOE_TOPK;
+constexpr uint32_t kSegTokens = 16;  // most tokens a segment
+
+struct MoeSegment {
+  uint32_t expert, n;
+  uint16_t slot[kSegTokens];  // t * topk + j, n of them
+};
 
 // Head of the workspace; h [slots, I] BF16 follows at kMoeHeadBytes.
 struct MoeHead {
-  uint32_t active;              // experts taken by any token
+  uint32_t segments;
   uint32_t pad[63];
-  uint32_t expert[kMaxE];       // their indices, ascending
-  uint32_t nan[kTok];           // token's logits hold a NaN or +inf: its output is NaN
+  uint32_t nan[kTok];             // token's logits hold a NaN or +inf: its output is NaN
   float weight[kTok * kMaxTopk];  // of slot t * topk + j
-  uint16_t slot[kMaxE][kTok];   // 1 + slot, by active expert and token; 0: none
+  MoeSegment seg[kTok * kMaxTopk];
 };
 static_assert(sizeof(MoeHead) <= kMoeHeadBytes, "workspace head");
 
@@ -51,102 +54,113 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// 16 waves; wave w routes tokens w, w + 16, ...
-__global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ logits, bool bf16, uint32_t T, uint32_t E,
-                                                    uint32_t topk, bool renorm, float scale, MoeHead *__restrict__ head) {
-  constexpr int R = kMaxE / 64;
-  __shared__ uint16_t ids[kTok][kMaxTopk];
-  __shared__ unsigned long long takers[kMaxE];  // tokens that take the expert
-  __shared__ uint32_t place[kMaxE / 64 + 1];
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform32(tid >> 6);
-  for (uint32_t e = tid; e < kMaxE; e += 1024u) takers[e] = 0ull;
-  __syncthreads();
+// One wave routes one token: lane j < topk gets choice j's expert (0xFFFF: none) and
+// weight.  Returns whether the logits hold a NaN or +inf (then nothing is chosen).
+template <int R>  // ceil(E / 64) at most
+__device__ __forceinline__ bool route_token(const void *logits, bool bf16, uint32_t t, uint32_t E, uint32_t topk,
+                                            bool renorm, float scale, uint32_t lane, uint32_t &id, float &w) {
   const float ninf = -__builtin_inff();
-  for (uint32_t t = wave; t < T; t += 16u) {
-    float v[R];
-    bool odd = false;  // NaN or +inf
+  float v[R], top = ninf;
+  bool odd = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t e = 64u * r + lane;
+    v[r] = ninf;
+    if (e < E) {
+      v[r] = bf16 ? bf16_bits_to_f32(((const uint16_t *)logits)[(size_t)t * E + e]) : ((const float *)logits)[(size_t)t * E + e];
+      odd |= !(v[r] < __builtin_inff());
+    }
+    top = fmaxf(top, v[r]);
+  }
+  id = 0xFFFFu;
+  w = 0.f;
+  if (__ballot(odd) != 0ull) return true;
+  top = wave_max(top);
+  if (!(top > ninf)) return false;  // every expert masked out
+  float total = 0.f, p = 0.f, best = top;
+  if (!renorm) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) total += v[r] > ninf ? expf(v[r] - top) : 0.f;
+    total = wave_sum(total);
+  }
+  for (uint32_t j = 0; j < topk && best > ninf; ++j) {  // the largest left, the lowest index among equals
+    uint32_t at = kMaxE;
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      const unsigned long long is = __ballot(v[r] == best);
+      if (is) at = 64u * r + (uint32_t)__builtin_ctzll(is);
+    }
+    float left = ninf;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t e = 64u * r + lane;
-      v[r] = ninf;
-      if (e < E) {
-        v[r] = bf16 ? bf16_bits_to_f32(((const uint16_t *)logits)[(size_t)t * E + e])
-                    : ((const float *)logits)[(size_t)t * E + e];
-        odd |= !(v[r] < __builtin_inff());
-      }
+      if (64u * r + lane == at) v[r] = ninf;
+      left = fmaxf(left, v[r]);
     }
-    const bool is_nan = __ballot(odd) != 0ull;
-    float top = ninf;
-#pragma unroll
-    for (int r = 0; r < R; ++r) top = fmaxf(top, v[r]);
-    top = wave_max(top);
-    const bool none = !(top > ninf);  // every expert masked out
-    float total = 0.f;
-    if (!renorm) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) total += v[r] > ninf ? expf(v[r] - top) : 0.f;
-      total = wave_sum(total);
+    if (lane == j) {
+      id = at;
+      p = expf(best - top);
     }
-    // the topk largest: one at a time, the lowest index among equals
-    uint32_t my_id = 0xFFFFu;  // lane j: expert of choice j
-    float my_p = 0.f;
-    if (!is_nan && !none) {
-      for (uint32_t j = 0; j < topk; ++j) {
-        float best = ninf;
-#pragma unroll
-        for (int r = 0; r < R; ++r) best = fmaxf(best, v[r]);
-        best = wave_max(best);
-        if (!(best > ninf)) break;
-        uint32_t id = kMaxE;
-#pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-          const unsigned long long at = __ballot(v[r] == best);
-          if (at) id = 64u * r + (uint32_t)__builtin_ctzll(at);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (64u * r + lane == id) v[r] = ninf;
-        if (lane == j) {
-          my_id = id;
-          my_p = expf(best - top);
-        }
-      }
-    }
-    if (renorm) total = wave_sum(my_p);
-    const float w = my_p > 0.f ? my_p / total * scale : 0.f;
-    if (w == 0.f) my_id = 0xFFFFu;  // a weight of zero (underflow, scale 0): the expert adds nothing and is not run
+    if (j + 1u < topk) best = wave_max(left);
+  }
+  if (renorm) total = wave_sum(p);
+  w = p > 0.f ? p / total * scale : 0.f;
+  if (w == 0.f) id = 0xFFFFu;  // underflow, or a scale of 0: the expert adds nothing and is not run
+  return false;
+}
+
+// 16 waves; wave w routes tokens w, w + 16, ...; segments of up to C tokens.
+template <int R>
+__global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ logits, bool bf16, uint32_t T, uint32_t E,
+                                                    uint32_t topk, bool renorm, float scale, uint32_t C,
+                                                    MoeHead *__restrict__ head) {
+  __shared__ uint16_t ids[kTok * kMaxTopk];
+  __shared__ unsigned long long takers[64 * R];  // tokens that take the expert
+  __shared__ uint32_t first[64 * R];             // its first segment
+  __shared__ uint32_t place[R];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform32(tid >> 6);
+  if (tid < 64u * R) takers[tid] = 0ull;
+  __syncthreads();
+  for (uint32_t t = wave; t < T; t += 16u) {
+    uint32_t id;
+    float w;
+    const bool is_nan = route_token<R>(logits, bf16, t, E, topk, renorm, scale, lane, id, w);
     if (lane < topk) {
-      ids[t][lane] = (uint16_t)my_id;
+      ids[t * topk + lane] = (uint16_t)id;
       head->weight[t * topk + lane] = w;
-      if (my_id < kMaxE) atomicOr(&takers[my_id], 1ull << t);  // order-free
+      if (id < kMaxE) atomicOr(&takers[id], 1ull << t);  // order-free
     }
     if (lane == 0) head->nan[t] = is_nan ? 1u : 0u;
   }
   __syncthreads();
-  // active experts in ascending order: waves 0 .. R-1 take 64 experts each
-  unsigned long long mine = 0ull, any = 0ull;
+  // segments in ascending order of experts: waves 0 .. R-1 take 64 experts each
+  uint32_t n = 0, segs = 0, before = 0;
   if (wave < (uint32_t)R) {
-    mine = takers[64u * wave + lane];
-    any = __ballot(mine != 0ull);
-    if (lane == 0) place[wave] = (uint32_t)__popcll(any);
+    n = (uint32_t)__popcll(takers[64u * wave + lane]);
+    segs = (n + C - 1u) / C;
+    uint32_t sum = segs;  // inclusive prefix over the lanes
+#pragma unroll
+    for (uint32_t off = 1; off < 64u; off <<= 1) {
+      const uint32_t up = (uint32_t)__shfl_up((int)sum, off, kWave);
+      if (lane >= off) sum += up;
+    }
+    before = sum - segs;
+    if (lane == 63u) place[wave] = sum;
   }
   __syncthreads();
   if (wave < (uint32_t)R) {
-    uint32_t a = 0;
-    for (uint32_t i = 0; i < wave; ++i) a += place[i];
-    if (wave == (uint32_t)R - 1u && lane == 0) head->active = a + place[wave];
-    a += (uint32_t)__popcll(any & ((1ull << lane) - 1ull));
-    const uint32_t e = 64u * wave + lane;
-    if (mine) {
-      head->expert[a] = e;
-      for (uint32_t t = 0; t < kTok; ++t) {
-        uint32_t s = 0;
-        if (mine >> t & 1ull)
-          for (uint32_t j = 0; j < topk; ++j)
-            if (ids[t][j] == e) s = t * topk + j + 1u;
-        head->slot[a][t] = (uint16_t)s;
-      }
+    for (uint32_t i = 0; i < wave; ++i) before += place[i];
+    first[64u * wave + lane] = before;
+    for (uint32_t i = 0; i < segs; ++i) {
+      head->seg[before + i].expert = 64u * wave + lane;
+      head->seg[before + i].n = n - i * C < C ? n - i * C : C;
     }
+    if (wave == (uint32_t)R - 1u && lane == 63u) head->segments = before + segs;
+  }
+  __syncthreads();
+  if (tid < T * topk && ids[tid] < kMaxE) {
+    const uint32_t e = ids[tid], t = tid / topk;
+    const uint32_t at = (uint32_t)__popcll(takers[e] & ((1ull << t) - 1ull));
+    head->seg[first[e] + at / C].slot[at % C] = (uint16_t)tid;
   }
 }
 
@@ -160,156 +174,138 @@ __device__ __forceinline__ float red_sum(const float *red, uint32_t tiles, uint3
   return v;
 }
 
-// Gate and up of 16 inner rows for the expert's n tokens, MT tiles of 16.
-template <class F, int KS, int U, int MT>
-__device__ __forceinline__ void up_tile(const typename F::View &wg, const typename F::View &wu, uint64_t base, uint32_t i0,
-                                        uint32_t I, const uint16_t *__restrict__ x, uint32_t T, const uint16_t *list,
-                                        const uint16_t *slots, uint32_t n, uint32_t topk, const float *__restrict__ weight,
-                                        uint16_t *__restrict__ h, float *red, uint32_t wave, uint32_t lane) {
-  const uint32_t K = wg.K;
-  const typename F::Tile tg = F::tile(wg, base, i0, I, lane), tu = F::tile(wu, base, i0, I, lane);
-  const auto rx = make_rsrc(x, T * K * 2u);
-  uint32_t xo[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const uint32_t i = 16u * mt + (lane & 15u);
-    xo[mt] = i < n ? (uint32_t)list[i] * K * 2u : kOutOfRange;
-  }
-  const uint32_t nc = (K + kChunk - 1u) / kChunk;
-  struct Ring {
-    typename F::Frag g, u;
-    XFrag x[MT];
-  } r[U];
-  auto load = [&](Ring &b, uint32_t c) {
-    F::load(b.g, tg, wg, c, lane);
-    F::load(b.u, tu, wu, c, lane);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) F::load_x(b.x[mt], rx, xo[mt], c, K, lane);
-  };
-  f32x4 ag[MT], au[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) ag[mt] = au[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
-  for (uint32_t c = wave; c < nc; c += KS * U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      f32x4 S[MT][4];
-      F::template sums<MT>(S, r[u].x);
-      F::template mac<MT>(ag, r[u].g, r[u].x, S);
-      F::template mac<MT>(au, r[u].u, r[u].x, S);
-      load(r[u], c + KS * (U + u));  // past the row's end: zeros, no traffic
-    }
-  }
-  // red [wave][2 MT tiles]
-  f32x4 *out = reinterpret_cast<f32x4 *>(red) + (wave * 2u * MT) * 64u + lane;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    out[(2 * mt) * 64] = ag[mt];
-    out[(2 * mt + 1) * 64] = au[mt];
-  }
-  __syncthreads();
-  for (uint32_t o = threadIdx.x; o < 256u * MT; o += 64u * KS) {
-    const uint32_t row = o & 15u, tok = (o >> 4) & 15u, mt = o >> 8, i = 16u * mt + tok;
-    if (i < n && i0 + row < I) {
-      const float g = red_sum<KS>(red, 2u * MT, 2u * mt, row, tok), u = red_sum<KS>(red, 2u * MT, 2u * mt + 1u, row, tok);
-      const uint32_t p = slots[i] - 1u;
-      h[(size_t)p * I + i0 + row] = to_bf16_bits(weight[p] * silu_mul(g, u));
-    }
-  }
-}
-
-// grid (16-row tiles of I, active experts at most)
-template <class F, int KS, int U, int MT>
+// grid (16-row tiles of I, segments at most).  NX: loads that a quarter's activations take.
+template <class F, int KS, int U, int NX, int AUX>
 __global__ __launch_bounds__(64 * KS) void k_moe_up(typename F::View wg, typename F::View wu, uint32_t I,
                                                     const uint16_t *__restrict__ x, uint32_t T, uint32_t topk,
                                                     const MoeHead *__restrict__ head, uint16_t *__restrict__ h) {
-  extern __shared__ __attribute__((aligned(16))) float moe_red[];
-  __shared__ uint16_t list[kTok], slots[kTok];
-  const uint32_t a = blockIdx.y, lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6);
-  const uint32_t s = head->slot[a][lane];  // meaningless, and unused, for a past the active ones
-  if (a >= uniform32(head->active)) return;
-  const uint64_t base = (uint64_t)uniform32(head->expert[a]) * I;
-  const unsigned long long on = __ballot(lane < T && s != 0u);
-  const uint32_t n = (uint32_t)__popcll(on);
-  if (wave == 0 && (on >> lane & 1ull)) {
-    const uint32_t at = (uint32_t)__popcll(on & ((1ull << lane) - 1ull));
-    list[at] = (uint16_t)lane;
-    slots[at] = (uint16_t)s;
+  typedef XBf16<F, NX> X;
+  constexpr uint32_t kWaveLds = stream_lds<X, 2>();
+  static_assert(KS * kWaveLds >= KS * 2048u, "the partial sums reuse the stream's LDS");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[KS * kWaveLds];
+  const MoeSegment *seg = &head->seg[blockIdx.y];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wg.K, i0 = 16u * blockIdx.x;
+  const uint32_t n = uniform32(seg->n), e = uniform32(seg->expert);  // meaningless, and unused, past the last segment
+  if (blockIdx.y >= uniform32(head->segments)) return;
+  const typename F::Tile tg = F::tile(wg, (uint64_t)e * I, i0, I, lane), tu = F::tile(wu, (uint64_t)e * I, i0, I, lane);
+  const X xs(x, T * K * 2u, K, lane, [&](uint32_t i) { return i < n ? seg->slot[i] / topk * (K * 2u) : kOutOfRange; });
+  const uint32_t np = (K + F::kPiece - 1u) / F::kPiece;
+  Pieces<F, X, 2> r[U];
+  auto load = [&](Pieces<F, X, 2> &b, uint32_t c) {
+    xs.load(b.x, c, lane);
+    F::template load<AUX>(b.w[0], tg, wg, c, lane);
+    F::template load<AUX>(b.w[1], tu, wu, c, lane);
+    keep_order();
+  };
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
+  for (uint32_t c = wave; c < np; c += KS * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      stream_piece<F, X, 2>(acc, r[u], xs, lds + wave * kWaveLds, lane);
+      keep_order();
+      load(r[u], c + KS * (U + u));  // past the row's end: zeros, no traffic
+    }
   }
   __syncthreads();
-  const uint32_t i0 = 16u * blockIdx.x;
-  if (MT == 1 || n <= 16u)
-    up_tile<F, KS, U, 1>(wg, wu, base, i0, I, x, T, list, slots, n, topk, head->weight, h, moe_red, wave, lane);
-  else if (MT == 2 || n <= 32u)
-    up_tile<F, KS, U, 2>(wg, wu, base, i0, I, x, T, list, slots, n, topk, head->weight, h, moe_red, wave, lane);
-  else
-    up_tile<F, KS, U, 4>(wg, wu, base, i0, I, x, T, list, slots, n, topk, head->weight, h, moe_red, wave, lane);
+  float *red = reinterpret_cast<float *>(lds);
+  reinterpret_cast<f32x4 *>(red)[(wave * 2u) * 64u + lane] = acc[0];
+  reinterpret_cast<f32x4 *>(red)[(wave * 2u + 1u) * 64u + lane] = acc[1];
+  __syncthreads();
+  for (uint32_t o = threadIdx.x; o < 16u * n; o += 64u * KS) {
+    const uint32_t row = o & 15u, tok = o >> 4;
+    if (i0 + row < I) {
+      const float g = red_sum<KS>(red, 2u, 0, row, tok), u = red_sum<KS>(red, 2u, 1, row, tok);
+      const uint32_t p = seg->slot[tok];
+      h[(size_t)p * I + i0 + row] = to_bf16_bits(head->weight[p] * silu_mul(g, u));
+    }
+  }
 }
 
-// grid: 16-row tiles of H.  LDS: red, then expert[active], then slot[active][16 MT].
-template <class F, int KS, int U, int MT>
+// grid: 16-row tiles of H.  Dynamic LDS: the streams', then the waves' sums
+// [KS][tokens][16], then the segments.  ONE: a single token, whose sums stay in registers.
+template <class F, int KS, int U, int NX, bool ONE, int AUX>
 __global__ __launch_bounds__(64 * KS) void k_moe_down(typename F::View wd, uint32_t H, const uint16_t *__restrict__ h,
                                                       uint32_t T, uint32_t topk, const MoeHead *__restrict__ head,
                                                       const uint16_t *__restrict__ resid, uint16_t *__restrict__ y) {
-  extern __shared__ __attribute__((aligned(16))) float moe_red[];
-  uint32_t *experts = reinterpret_cast<uint32_t *>(moe_red + KS * MT * 256);
+  typedef XBf16<F, NX> X;
+  constexpr uint32_t kWaveLds = stream_lds<X, 1>();
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float *sums = reinterpret_cast<float *>(lds + KS * kWaveLds);  // [KS][T][16]
+  MoeSegment *segs = reinterpret_cast<MoeSegment *>(sums + KS * T * 16u);
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), n0 = 16u * blockIdx.x, K = wd.K;
-  const uint32_t active = uniform32(head->active);
-  uint16_t *slot = reinterpret_cast<uint16_t *>(experts + active);
-  for (uint32_t i = threadIdx.x; i < active; i += 64u * KS) experts[i] = head->expert[i];
-  for (uint32_t i = threadIdx.x; i < active * 16u * MT; i += 64u * KS) {
-    const uint32_t t = i % (16u * MT);
-    slot[i] = t < T ? head->slot[i / (16u * MT)][t] : (uint16_t)0;
-  }
+  const uint32_t count = uniform32(head->segments);
+  for (uint32_t i = threadIdx.x; i < count * (sizeof(MoeSegment) / 4u); i += 64u * KS)
+    reinterpret_cast<uint32_t *>(segs)[i] = reinterpret_cast<const uint32_t *>(head->seg)[i];
+  for (uint32_t i = threadIdx.x; i < KS * T * 16u; i += 64u * KS) sums[i] = 0.f;
   __syncthreads();
-  const auto rh = make_rsrc(h, T * topk * K * 2u);
-  const uint32_t nc = (K + kChunk - 1u) / kChunk;
-  struct Ring {
-    typename F::Frag w;
-    XFrag x[MT];
-  } r[U];
-  // this wave's items: chunk c of active expert a, KS apart in the flat order
-  uint32_t la = 0, lc = wave;
-  auto load = [&](Ring &b) {
-    while (lc >= nc && la < active) {
-      lc -= nc;
-      ++la;
-    }
-    const bool in = la < active;
-    const uint32_t a = in ? la : 0u, c = in ? lc : nc;
-    const uint32_t e = uniform32(active ? experts[a] : 0u);
-    const typename F::Tile t = F::tile(wd, (uint64_t)e * H, n0, H, lane);
-    F::load(b.w, t, wd, c, lane);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const uint32_t s = in ? slot[(a * MT + mt) * 16u + (lane & 15u)] : 0u;
-      F::load_x(b.x[mt], rh, s ? (s - 1u) * K * 2u : kOutOfRange, c, K, lane);
-    }
-    lc += KS;
+  const uint32_t np = (K + F::kPiece - 1u) / F::kPiece, items = count * np;
+  // this wave's items: neighbouring pieces of one segment after the other
+  const uint32_t i0 = (uint32_t)((uint64_t)items * wave / KS), i1 = (uint32_t)((uint64_t)items * (wave + 1u) / KS);
+  uint32_t ls = 0, lp = 0;  // segment and piece of the next load
+  typename F::Tile tile = {};
+  X xs(h, T * topk * K * 2u, K, lane, [&](uint32_t) { return kOutOfRange; });
+  auto segment = [&](uint32_t s) {
+    const MoeSegment &g = segs[s];
+    tile = F::tile(wd, (uint64_t)uniform32(g.expert) * H, n0, H, lane);
+    const uint32_t n = g.n;
+    xs = X(h, T * topk * K * 2u, K, lane, [&](uint32_t i) { return i < n ? g.slot[i] * (K * 2u) : kOutOfRange; });
   };
-  f32x4 acc[MT];
+  if (i0 < i1) {
+    ls = i0 / np;
+    lp = i0 - ls * np;
+    segment(ls);
+  }
+  uint32_t cs = ls, cp = lp;  // ... of the next products
+  Pieces<F, X, 1> r[U];
+  uint32_t next = i0;
+  auto load = [&](Pieces<F, X, 1> &b) {
+    if (lp == np) {
+      lp = 0;
+      if (++ls < count) segment(ls);
+    }
+    const uint32_t p = next < i1 ? lp : np;  // piece np: past the row's end, zeros
+    xs.load(b.x, p, lane);
+    F::template load<AUX>(b.w[0], tile, wd, p, lane);
+    ++lp;
+    ++next;
+    keep_order();
+  };
+  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+  auto flush = [&](uint32_t s) {  // D[4 g + i][row]: token i of the segment, output row
+    const uint32_t n = segs[s].n;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (uint32_t i = 0; i < 4u; ++i) {
+      const uint32_t k = 4u * (lane >> 4) + i;
+      if (k < n) sums[(wave * T + segs[s].slot[k] / topk) * 16u + (lane & 15u)] += acc[0][i];
+    }
+    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(r[u]);
-  for (uint32_t i = wave; i < active * nc; i += KS * U) {
+  for (uint32_t i = i0; i < i1;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      f32x4 S[MT][4];
-      F::template sums<MT>(S, r[u].x);
-      F::template mac<MT>(acc, r[u].w, r[u].x, S);
+      stream_piece<F, X, 1>(acc, r[u], xs, lds + wave * kWaveLds, lane);
+      keep_order();
       load(r[u]);
+      ++i;
+      if (!ONE && i <= i1 && (++cp == np || i == i1)) {
+        flush(cs);
+        cp = 0;
+        ++cs;
+      }
     }
   }
-  f32x4 *out = reinterpret_cast<f32x4 *>(moe_red) + (wave * MT) * 64u + lane;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) out[mt * 64] = acc[mt];
+  if (ONE && lane < 16u) sums[wave * 16u + lane] = acc[0][0];
   __syncthreads();
-  for (uint32_t o = threadIdx.x; o < 256u * MT; o += 64u * KS) {
+  for (uint32_t o = threadIdx.x; o < 16u * T; o += 64u * KS) {
     const uint32_t row = o & 15u, tok = o >> 4, n = n0 + row;
-    if (tok < T && n < H) {
-      float v = red_sum<KS>(moe_red, MT, tok >> 4, row, tok & 15u);
+    if (n < H) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < KS; ++w) v += sums[((uint32_t)w * T + tok) * 16u + row];
       if (head->nan[tok]) v = __builtin_nanf("");
       if (resid) v += bf16_bits_to_f32(resid[(size_t)tok * H + n]);
       y[(size_t)tok * H + n] = to_bf16_bits(v);
@@ -317,18 +313,18 @@ __global__ __launch_bounds__(64 * KS) void k_moe_down(typename F::View wd, uint3
   }
 }
 
-template <class F, int MT>
+template <class F, int NX, bool ONE>
 hipError_t launch_pass(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
-                       MoeHead *head, uint16_t *h, uint32_t T, const uint16_t *x, const uint16_t *resid, uint16_t *y,
-                       hipStream_t stream) {
-  const uint32_t I = g.N / m.E, H = d.N / m.E, most = T * m.topk < m.E ? T * m.topk : m.E;
-  constexpr int KU = 4, KD = 16, U = MT == 1 ? 3 : 2;
-  k_moe_up<F, KU, U, MT><<<dim3((I + 15u) / 16u, most), 64 * KU, KU * 2 * MT * 1024, stream>>>(g, u, I, x, T, m.topk, head, h);
-  const uint32_t lds = KD * MT * 1024 + most * (4u + 32u * MT);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_moe_down<F, KD, U, MT>),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                       MoeHead *head, uint16_t *h, uint32_t T, uint32_t most, const uint16_t *x, const uint16_t *resid,
+                       uint16_t *y, hipStream_t stream) {
+  const uint32_t I = g.N / m.E, H = d.N / m.E;
+  constexpr int KU = 4, KD = NX == 1 ? 16 : 8, U = NX == 1 ? 2 : 1, AUX = ONE ? kAuxNontemporal : 0;
+  k_moe_up<F, KU, U, NX, AUX><<<dim3((I + 15u) / 16u, most), 64 * KU, 0, stream>>>(g, u, I, x, T, m.topk, head, h);
+  const uint32_t lds = KD * (stream_lds<XBf16<F, NX>, 1>() + T * 64u) + most * (uint32_t)sizeof(MoeSegment);
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_moe_down<F, KD, U, NX, ONE, AUX>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  k_moe_down<F, KD, U, MT><<<(H + 15u) / 16u, 64 * KD, lds, stream>>>(d, H, h, T, m.topk, head, resid, y);
+  k_moe_down<F, KD, U, NX, ONE, AUX><<<(H + 15u) / 16u, 64 * KD, lds, stream>>>(d, H, h, T, m.topk, head, resid, y);
   return hipGetLastError();
 }
 
@@ -339,14 +335,21 @@ hipError_t launch_layer(const typename F::View &g, const typename F::View &u, co
   uint16_t *h = reinterpret_cast<uint16_t *>((uint8_t *)m.ws + kMoeHeadBytes);
   const size_t H = d.N / m.E;
   for (uint32_t t0 = 0; t0 < m.tokens; t0 += kTok) {
-    const uint32_t T = m.tokens - t0 < kTok ? m.tokens - t0 : kTok;
+    const uint32_t T = m.tokens - t0 < kTok ? m.tokens - t0 : kTok, slots = T * m.topk;
     const uint8_t *logits = (const uint8_t *)m.logits + (size_t)t0 * m.E * (m.logits_bf16 ? 2u : 4u);
-    k_moe_route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, T, m.E, m.topk, m.renorm, m.scale, head);
+    // tokens a segment: the rows of one activation load where experts have few tokens
+    constexpr uint32_t kOne = 64u / F::kXChunks;
+    const bool few = T <= kOne || slots <= m.E * (kOne / 2u);
+    const uint32_t C = few ? kOne : kSegTokens;
+    // segments at most: one an expert taken, one more for each C further tokens
+    const uint32_t taken = slots < m.E ? slots : m.E, most = taken + (slots - taken) / C;
+    auto route = m.E <= 64u ? k_moe_route<1> : m.E <= 128u ? k_moe_route<2> : m.E <= 256u ? k_moe_route<4> : k_moe_route<8>;
+    route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, T, m.E, m.topk, m.renorm, m.scale, C, head);
     const uint16_t *x = m.x + t0 * H, *resid = m.resid ? m.resid + t0 * H : nullptr;
     uint16_t *y = m.y + t0 * H;
-    const hipError_t e = T <= 16u   ? launch_pass<F, 1>(g, u, d, m, head, h, T, x, resid, y, stream)
-                         : T <= 32u ? launch_pass<F, 2>(g, u, d, m, head, h, T, x, resid, y, stream)
-                                    : launch_pass<F, 4>(g, u, d, m, head, h, T, x, resid, y, stream);
+    const hipError_t e = T == 1u ? launch_pass<F, 1, true>(g, u, d, m, head, h, T, most, x, resid, y, stream)
+                         : few   ? launch_pass<F, 1, false>(g, u, d, m, head, h, T, most, x, resid, y, stream)
+                                 : launch_pass<F, kSegTokens / kOne, false>(g, u, d, m, head, h, T, most, x, resid, y, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -1,7 +1,7 @@
 // mxfp4_gemm.hip -- Y[m, N] = X[m, K] W^T with W in MXFP4 (mxfp4.h) and X in
 // BF16 (weight-only) or in MXFP4 too.  fp32 accumulation, one rounding to BF16.
 //
-// m <= kMxRowsMax: HBM-bound, the weight is streamed once for all rows
+// m <= 64: HBM-bound, the weight is streamed once for all rows
 //   (k_mx_rows): a workgroup owns 16 weight rows, its waves split K chunk by
 //   chunk and load weight codes, scales and the matching activations straight
 //   into matrix-core operands (rows_stream.h); no staging, no barrier until the
@@ -10,6 +10,8 @@
 //   converted with their scale in registers, exactly) or on the scaled fp4 MFMA
 //   (both MXFP4: 16 x 16 x 128 products with a scale per 32 k in the
 //   instruction).
+#include <type_traits>
+
 #include "rows_stream.h"
 #include "launch.h"
 
@@ -17,111 +19,94 @@ namespace int8w {
 
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f32x4 mfma_mx(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
-  // fp4 operands take the first four registers of eight
-  const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
 // ---- few rows ---------------------------------------------------------------------------------
 
-// The activations of MT token tiles as they enter the products: BF16 rows, or MXFP4 rows.
-template <bool XMX, int MT>
-struct RowsX;
-
-template <int MT>
-struct RowsX<false, MT> {
-  struct Frag {
-    XFrag x[MT];
-  };
-  __amdgpu_buffer_rsrc_t r;
-  uint32_t xo[MT];
-  __device__ __forceinline__ RowsX(const void *x, const uint8_t *, uint32_t m, uint32_t K, uint32_t lane) {
-    r = make_rsrc(x, m * K * 2u);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) xo[mt] = 16u * mt + (lane & 15u) < m ? (16u * mt + (lane & 15u)) * K * 2u : kOutOfRange;
-  }
-  __device__ __forceinline__ void load(Frag &f, uint32_t c, uint32_t K, uint32_t lane) const {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) MxFmt::load_x(f.x[mt], r, xo[mt], c, K, lane);
-  }
-  static __device__ __forceinline__ void mac(f32x4 (&acc)[MT], const MxFmt::Frag &w, const Frag &f) {
-    const f32x4 none[MT][4] = {};
-    MxFmt::mac<MT>(acc, w, f.x, none);
-  }
-};
-
-template <int MT>
-struct RowsX<true, MT> {
-  struct Frag {
-    MxFmt::Frag x[MT];
-  };
+// Activations in MXFP4: another tile of rows.
+struct XMx {
+  static constexpr uint32_t kLds = 1024u;
+  typedef MxFmt::Piece Piece;
   MxView v;
-  MxFmt::Tile t[MT];
-  __device__ __forceinline__ RowsX(const void *x, const uint8_t *scales, uint32_t m, uint32_t K, uint32_t lane) {
+  MxFmt::Tile t;
+  __device__ __forceinline__ XMx(const void *x, const uint8_t *scales, uint32_t m0, uint32_t m, uint32_t K, uint32_t lane) {
     v = MxView{(const uint8_t *)x, scales, m, K};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) t[mt] = MxFmt::tile(v, 0, 16u * mt < m ? 16u * mt : m - 1u, m, lane);
+    t = MxFmt::tile(v, 0, m0, m, lane);
   }
-  __device__ __forceinline__ void load(Frag &f, uint32_t c, uint32_t, uint32_t lane) const {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) MxFmt::load(f.x[mt], t[mt], v, c, lane);
-  }
-  static __device__ __forceinline__ void mac(f32x4 (&acc)[MT], const MxFmt::Frag &w, const Frag &f) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma_mx(f.x[mt].q, f.x[mt].s, w.q, w.s, acc[mt]);
-  }
+  __device__ __forceinline__ void load(Piece &f, uint32_t piece, uint32_t lane) const { MxFmt::load<0>(f, t, v, piece, lane); }
 };
 
-template <bool XMX, int KS, int U, int MT>
-__global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
-                                                     const uint8_t *__restrict__ xs, uint32_t m,
-                                                     uint16_t *__restrict__ y) {
-  __shared__ __attribute__((aligned(16))) float red[KS * MT * 256];
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), n0 = 16u * blockIdx.x, K = w.K;
-  const MxFmt::Tile t = MxFmt::tile(w, 0, n0, w.N, lane);
-  const RowsX<XMX, MT> X(x, xs, m, K, lane);
-  struct Ring {
-    MxFmt::Frag w;
-    typename RowsX<XMX, MT>::Frag x;
-  } r[U];
-  const uint32_t nc = (K + kChunk - 1u) / kChunk;
-  auto load = [&](Ring &b, uint32_t c) {
-    MxFmt::load(b.w, t, w, c, lane);
-    X.load(b.x, c, K, lane);
-  };
-  f32x4 acc[MT];
+__device__ __forceinline__ void stream_piece_mx(f32x4 &acc, const Pieces<MxFmt, XMx, 1> &p, uint8_t *lds, uint32_t lane) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < 4; ++h) {
+    uint8_t *at = lds + (h & 1) * (stream_lds<XMx, 1>() / 2u);
+    put_quarter(at, p.w[0].q[h], lane);
+    put_quarter(at + 1024u, p.x.q[h], lane);
+    wave_fence();
+    acc = mfma_mx(get_quarter(at + 1024u, lane), MxFmt::scale(p.x, h, lane), get_quarter(at, lane),
+                  MxFmt::scale(p.w[0], h, lane), acc);
+    wave_fence();
+  }
+}
+
+// grid: (16-row weight tiles) x (groups of 16 rows of X), the groups of a tile side by side.
+template <bool XMX, int KS, int U, int NX, int AUX>
+__global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
+                                                     const uint8_t *__restrict__ xs, uint32_t m, uint32_t groups,
+                                                     uint16_t *__restrict__ y) {
+  typedef std::conditional_t<XMX, XMx, XBf16<MxFmt, NX>> X;
+  constexpr uint32_t kWaveLds = stream_lds<X, 1>();
+  __shared__ __attribute__((aligned(16))) uint8_t lds[KS * kWaveLds];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = w.K;
+  const uint32_t n0 = 16u * (blockIdx.x / groups), m0 = 16u * (blockIdx.x % groups);
+  const uint32_t rows = m - m0 < 16u ? m - m0 : 16u;
+  const MxFmt::Tile t = MxFmt::tile(w, 0, n0, w.N, lane);
+  auto make = [&]() {
+    if constexpr (XMX)
+      return X(x, xs, m0, m, K, lane);
+    else
+      return X((const uint16_t *)x + (size_t)m0 * K, rows * K * 2u, K, lane,
+               [&](uint32_t i) { return i < rows ? i * K * 2u : kOutOfRange; });
+  };
+  const X xr = make();
+  Pieces<MxFmt, X, 1> r[U];
+  const uint32_t np = (K + MxFmt::kPiece - 1u) / MxFmt::kPiece;
+  auto load = [&](Pieces<MxFmt, X, 1> &b, uint32_t c) {
+    xr.load(b.x, c, lane);
+    MxFmt::load<AUX>(b.w[0], t, w, c, lane);
+    keep_order();
+  };
+  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
   for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
-  for (uint32_t c = wave; c < nc; c += KS * U) {
+  for (uint32_t c = wave; c < np; c += KS * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      RowsX<XMX, MT>::mac(acc, r[u].w, r[u].x);
-      load(r[u], c + KS * (U + u));
+      if constexpr (XMX)
+        stream_piece_mx(acc[0], r[u], lds + wave * kWaveLds, lane);
+      else
+        stream_piece<MxFmt, X, 1>(acc, r[u], xr, lds + wave * kWaveLds, lane);
+      keep_order();
+      load(r[u], c + KS * (U + u));  // past the row's end: zeros, no traffic
     }
   }
-  f32x4 *out = reinterpret_cast<f32x4 *>(red) + wave * MT * 64u + lane;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) out[mt * 64] = acc[mt];
   __syncthreads();
-  for (uint32_t o = threadIdx.x; o < 256u * MT; o += 64u * KS) {
+  float *red = reinterpret_cast<float *>(lds);  // the partial sums reuse the streams' LDS
+  reinterpret_cast<f32x4 *>(red)[wave * 64u + lane] = acc[0];
+  __syncthreads();
+  for (uint32_t o = threadIdx.x; o < 16u * rows; o += 64u * KS) {
     const uint32_t row = o & 15u, tok = o >> 4;
-    if (tok < m && n0 + row < w.N) {
-      const uint32_t at = ((tok >> 4) * 64u + ((tok & 15u) >> 2) * 16u + row) * 4u + (tok & 3u);
+    if (n0 + row < w.N) {
+      const uint32_t at = ((tok >> 2) * 16u + row) * 4u + (tok & 3u);
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < KS; ++i) v += red[i * MT * 256 + at];
-      y[(size_t)tok * w.N + n0 + row] = to_bf16_bits(v);
+      for (int i = 0; i < KS; ++i) v += red[i * 256 + at];
+      y[(size_t)(m0 + tok) * w.N + n0 + row] = to_bf16_bits(v);
     }
   }
 }
 
 // ---- many rows --------------------------------------------------------------------------------
+
+constexpr uint32_t kChunk = 128;  // k of one fp4 MFMA
 
 // Tile BM rows of X times BN weight rows, WM x WN waves.  Both operands are
 // copied to LDS by DMA, two stages, a step of CH chunks each; 16-byte pieces of a
@@ -315,16 +300,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_
   }
 }
 
-template <bool XMX, int MT>
+template <bool XMX, int NX, int AUX>
 hipError_t launch_rows(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
-  const uint32_t tiles = (w.N + 15u) / 16u, nc = (w.K + kChunk - 1u) / kChunk;
-  constexpr int U = XMX ? (MT <= 2 ? 4 : 2) : (MT == 1 ? 4 : 2);
-  if (nc >= 64u && tiles <= 512u)
-    k_mx_rows<XMX, 16, (MT <= 2 ? U : 1), MT><<<tiles, 1024, 0, stream>>>(w, x, xs, m, y);
-  else if (nc >= 16u)
-    k_mx_rows<XMX, 8, U, MT><<<tiles, 512, 0, stream>>>(w, x, xs, m, y);
+  const uint32_t groups = (m + 15u) / 16u, grid = (w.N + 15u) / 16u * groups, np = (w.K + MxFmt::kPiece - 1u) / MxFmt::kPiece;
+  constexpr int U = NX <= 2 && !XMX ? 2 : 1, K16 = NX == 1 ? 16 : 8;
+  if (np >= 16u && grid <= 512u)
+    k_mx_rows<XMX, K16, U, NX, AUX><<<grid, 64 * K16, 0, stream>>>(w, x, xs, m, groups, y);
+  else if (np >= 8u)
+    k_mx_rows<XMX, 8, U, NX, AUX><<<grid, 512, 0, stream>>>(w, x, xs, m, groups, y);
   else
-    k_mx_rows<XMX, 4, U, MT><<<tiles, 256, 0, stream>>>(w, x, xs, m, y);
+    k_mx_rows<XMX, 4, U, NX, AUX><<<grid, 256, 0, stream>>>(w, x, xs, m, groups, y);
   return hipGetLastError();
 }
 
@@ -341,9 +326,11 @@ hipError_t launch_tile(const MxView &w, const void *x, const uint8_t *xs, uint32
 
 template <bool XMX>
 hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
-  if (m <= 16u) return launch_rows<XMX, 1>(w, x, xs, m, y, stream);
-  if (m <= 32u) return launch_rows<XMX, 2>(w, x, xs, m, y, stream);
-  if (m <= 64u) return launch_rows<XMX, 4>(w, x, xs, m, y, stream);
+  if (XMX && m <= 16u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
+  if (m <= 4u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
+  if (m <= 8u) return launch_rows<XMX, 2, kAuxNontemporal>(w, x, xs, m, y, stream);
+  if (m <= 16u) return launch_rows<XMX, 4, kAuxNontemporal>(w, x, xs, m, y, stream);
+  if (m <= 64u) return launch_rows<XMX, XMX ? 1 : 4, 0>(w, x, xs, m, y, stream);
   const uint32_t big = XMX ? ((m + 255u) / 256u) * ((w.N + 255u) / 256u) : ((m + 127u) / 128u) * ((w.N + 255u) / 256u);
   if (big < (uint32_t)device_cu_count() / 2u) return launch_tile<XMX, 64, 64, 2, 2, XMX ? 2 : 1>(w, x, xs, m, y, stream);
   if constexpr (XMX)

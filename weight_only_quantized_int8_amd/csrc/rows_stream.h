@@ -1,21 +1,29 @@
-// rows_stream.h -- weight rows streamed from memory straight into matrix-core
-// operands, shared by the MXFP4 product for few rows and the
-// mixture-of-experts layer.
+// rows_stream.h -- weight rows streamed through one wave into matrix-core operands,
+// shared by the MXFP4 product for few rows and the mixture-of-experts layer.
 //
-// Unit: a tile of 16 weight rows times a chunk of 128 k.  v_mfma_f32_16x16x32_bf16
-// computes D[i][j] = sum_k A[i][k] B[k][j] with A = activation rows (16 tokens)
-// and B = weight rows; lane l holds A[l%16][8 (l/16) + 0..7], B[the same k][l%16]
-// and D[4 (l/16) + r][l%16].  Which k stands behind a lane's eight values does not
-// matter as long as A and B agree, so a lane loads 16 contiguous code bytes of its
-// row and the activations that go with them, with no staging and no barrier:
-//  * MXFP4: lane group g = l/16 takes block 4c + g of chunk c (32 codes, 16 bytes,
-//    one scale); MFMA f of four takes its codes 8f .. 8f+7, converted to BF16 with
-//    the scale applied (exact).
-//  * 8-bit affine: sum_k (q s + b) x = s sum q x + b sum x per run of one group:
-//    codes enter the MFMA as exact BF16 integers, sum x comes from an MFMA against
-//    ones (shared by all tiles of the chunk), and the group's s and b are applied to
-//    the fp32 results.  Group size 64 and 128: a lane takes 16 bytes of each 64-code
-//    half; 32: 8 bytes of each 32 codes.
+// v_mfma_f32_16x16x32_bf16 computes D[i][j] = sum_k A[i][k] B[k][j]; here A = 16
+// activation rows, B = 16 weight rows.  Lane l holds A[l%16][8 (l/16) + 0..7], B[the
+// same k][l%16] and D[4 (l/16) + r][l%16].  Which k stands behind a lane's eight
+// values does not matter as long as A and B agree.
+//
+// Unit of work: a piece of 256 code bytes of each of 16 weight rows, in four quarters
+// of 64 bytes a row.
+//  * In the operand layout neighbouring lanes belong to different rows, and a load in
+//    that layout costs the address unit a cycle a lane (measured: 64 a load, 2.4 TB/s
+//    over the whole GPU).  So all loads are made with neighbouring lanes on
+//    neighbouring bytes (lane l: row l/4, 16-byte chunk l%4 of a quarter) and a quarter
+//    changes lanes through 1 KB of LDS that only this wave uses: one ds_write_b128, one
+//    ds_read_b128, no barrier.  Chunks are XOR-swizzled by row against bank conflicts.
+//  * Activations of a quarter take the same way (rows of 256 or 128 bytes).
+//  * Scales: one load a piece, lane l: row l/4, quarter l%4; a lane fetches its row's by
+//    a lane permute.
+//  * MXFP4: lane group g = l/16 takes block g of the quarter's four (32 codes, 16
+//    bytes, one scale); MFMA f of four takes its codes 8f .. 8f+7, converted to BF16
+//    with the scale applied (exact).
+//  * 8-bit affine: sum_k (q s + b) x = s sum q x + b sum x per run of one group: codes
+//    enter the MFMA as exact BF16 integers, sum x comes from an MFMA against ones
+//    (shared by the tiles), s and b are applied to the fp32 results.  Group size 64 and
+//    128: a quarter is one run; 32: two.
 // Loads past the end of a row, a weight or a list go to an offset beyond the buffer
 // resource: they return zeros and touch no memory.
 #pragma once
@@ -24,9 +32,7 @@
 
 namespace int8w {
 
-constexpr uint32_t kChunk = 128;  // k per chunk
-
-typedef u32x4 XFrag[4];  // one token tile's A operands of a chunk
+constexpr uint32_t kPieceBytes = 256;  // code bytes of a row in a piece
 
 __device__ __forceinline__ uint32_t uniform32(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
@@ -35,53 +41,101 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 }
 __device__ __forceinline__ u32x4 bf16_ones() { return u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}; }
 
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ f32x4 mfma_mx(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
+  // fp4 operands take the first four registers of eight
+  const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// Loads are waited for in the order of their issue, so a ring of pieces in flight only
+// works if the compiler keeps each piece's loads together and behind the ones before.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// LDS writes of this wave's lanes before reads by its other lanes: LDS instructions of a
+// wave execute in order, so only the compiler has to keep it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ uint32_t lane_get(uint32_t v, uint32_t from) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute((int)(4u * from), (int)v);
+}
+
+// A quarter of a tile of 16 rows x 64 bytes in LDS: chunk p of row r at 64 r + 16 (p ^ (r/2 % 4)).
+__device__ __forceinline__ uint32_t quarter_at(uint32_t r, uint32_t p) { return 64u * r + 16u * (p ^ ((r >> 1) & 3u)); }
+__device__ __forceinline__ void put_quarter(uint8_t *lds, u32x4 v, uint32_t lane) {
+  *reinterpret_cast<u32x4 *>(lds + quarter_at(lane >> 2, lane & 3u)) = v;
+}
+__device__ __forceinline__ u32x4 get_quarter(const uint8_t *lds, uint32_t lane) {  // chunk l/16 of row l%16
+  return *reinterpret_cast<const u32x4 *>(lds + quarter_at(lane & 15u, lane >> 4));
+}
+
 // ---- MXFP4 ------------------------------------------------------------------------------------
 struct MxFmt {
   typedef MxView View;
+  static constexpr uint32_t kQuarter = 128;           // k a quarter
+  static constexpr uint32_t kPiece = 4 * kQuarter;    // k a piece
+  static constexpr uint32_t kXChunks = 16;            // 16-byte chunks of an activation row in a quarter
+  static constexpr int kXFrags = 4;                   // A operands of a quarter
+  static constexpr int kRuns = 1;
   struct Tile {  // 16 weight rows
     __amdgpu_buffer_rsrc_t codes, scales;
-    uint32_t oc, os;  // this lane's byte offsets at chunk 0 (kOutOfRange for a row past the end)
+    uint32_t oc, os;  // this lane's byte offsets at piece 0 (kOutOfRange for a row past the end)
+    bool dwords;      // scales can be loaded four at a time
   };
-  struct Frag {
-    u32x4 q;
-    uint32_t s;
+  struct Piece {
+    u32x4 q[4];
+    uint32_t s;  // row l/4, the four scales of quarter l%4
   };
-  static constexpr int kSums = 0;
 
   // rows [n0, n0 + 16) of the N rows that start at row `base` of the weight
   static __device__ __forceinline__ Tile tile(const MxView &w, uint64_t base, uint32_t n0, uint32_t N, uint32_t lane) {
     Tile t;
-    const uint32_t rows = N - n0 < 16u ? N - n0 : 16u, lr = lane & 15u, g = lane >> 4;
+    const uint32_t rows = N - n0 < 16u ? N - n0 : 16u, r = lane >> 2, p = lane & 3u;
     const uint64_t row0 = base + n0;
+    const uint8_t *sc = w.scales + row0 * (w.K / 32u);
     t.codes = make_rsrc(w.codes + row0 * (w.K / 2u), rows * (w.K / 2u));
-    t.scales = make_rsrc(w.scales + row0 * (w.K / 32u), rows * (w.K / 32u));
-    t.oc = lr < rows ? lr * (w.K / 2u) + 16u * g : kOutOfRange;
-    t.os = lr < rows ? lr * (w.K / 32u) + g : kOutOfRange;
+    t.scales = make_rsrc(sc, rows * (w.K / 32u));
+    t.oc = r < rows ? r * (w.K / 2u) + 16u * p : kOutOfRange;
+    t.os = r < rows ? r * (w.K / 32u) + 4u * p : kOutOfRange;
+    t.dwords = w.K % 128u == 0 && (reinterpret_cast<uintptr_t>(sc) & 3u) == 0;
     return t;
   }
-  static __device__ __forceinline__ bool live(uint32_t c, uint32_t K, uint32_t g) { return 4u * c + g < K / 32u; }
-  static __device__ __forceinline__ void load(Frag &f, const Tile &t, const MxView &w, uint32_t c, uint32_t lane) {
-    const bool in = live(c, w.K, lane >> 4);
-    f.q = buf_load_b128<kAuxNontemporal>(t.codes, in ? t.oc + 64u * c : kOutOfRange);
-    f.s = __builtin_amdgcn_raw_buffer_load_b8(t.scales, (int)(in ? t.os + 4u * c : kOutOfRange), 0, 0);
-  }
-  // xo: byte offset of the lane's activation row (kOutOfRange: none)
-  static __device__ __forceinline__ void load_x(XFrag &x, __amdgpu_buffer_rsrc_t r, uint32_t xo, uint32_t c, uint32_t K,
-                                                uint32_t lane) {
-    const uint32_t o = live(c, K, lane >> 4) ? xo + 256u * c + 64u * (lane >> 4) : kOutOfRange;
+  template <int AUX>
+  static __device__ __forceinline__ void load(Piece &f, const Tile &t, const MxView &w, uint32_t piece, uint32_t lane) {
+    const uint32_t p = lane & 3u, b0 = kPieceBytes * piece;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) x[f] = buf_load_b128(r, o + 16u * f);
+    for (int h = 0; h < 4; ++h)
+      f.q[h] = buf_load_b128<AUX>(t.codes, b0 + 64u * h + 16u * p < w.K / 2u ? t.oc + b0 + 64u * h : kOutOfRange);
+    const uint32_t blk = 16u * piece + 4u * p;  // first block of quarter p
+    if (t.dwords) {
+      f.s = __builtin_amdgcn_raw_buffer_load_b32(t.scales, (int)(blk < w.K / 32u ? t.os + 16u * piece : kOutOfRange), 0, 0);
+    } else {
+      f.s = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < 4u; ++i)
+        f.s |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                   t.scales, (int)(blk + i < w.K / 32u ? t.os + 16u * piece + i : kOutOfRange), 0, 0) << (8u * i);
+    }
   }
-  template <int MT>
-  static __device__ __forceinline__ void sums(f32x4 (&)[MT][4], const XFrag (&)[MT]) {}
-  template <int MT>
-  static __device__ __forceinline__ void mac(f32x4 (&acc)[MT], const Frag &f, const XFrag (&x)[MT], const f32x4 (&)[MT][4]) {
-    const float s = mx_scale_f32(f.s);
+  // scale byte of row l%16, block l/16 of quarter h
+  static __device__ __forceinline__ uint32_t scale(const Piece &f, int h, uint32_t lane) {
+    return (lane_get(f.s, 4u * (lane & 15u) + h) >> (8u * (lane >> 4))) & 0xFFu;
+  }
+  static __device__ __forceinline__ uint32_t x_chunk(int f, uint32_t g) { return 4u * g + f; }
+  struct Sums {};
+  static __device__ __forceinline__ void sums(Sums &, const u32x4 (&)[kXFrags]) {}
+  static __device__ __forceinline__ void mac(f32x4 &acc, u32x4 q, const Piece &f, int h, const u32x4 (&x)[kXFrags],
+                                             const Sums &, uint32_t lane) {
+    const float s = mx_scale_f32(scale(f, h, lane));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 b = mx_to_bf16x8(f.q[i], s);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma16(x[mt][i], u32x4{b.x, b.y, b.z, b.w}, acc[mt]);
+      const uint4 b = mx_to_bf16x8(q[i], s);
+      acc = mfma16(x[i], u32x4{b.x, b.y, b.z, b.w}, acc);
     }
   }
 };
@@ -95,99 +149,171 @@ __device__ __forceinline__ u32x4 int8_codes_bf16(uint32_t a, uint32_t b) {  // e
 template <bool G32>
 struct Int8Fmt {
   typedef WeightView View;
-  static constexpr int kRuns = G32 ? 4 : 2;  // runs of one group in a chunk
-  static constexpr int kSums = kRuns;
+  static constexpr uint32_t kQuarter = 64;
+  static constexpr uint32_t kPiece = 4 * kQuarter;
+  static constexpr uint32_t kXChunks = 8;
+  static constexpr int kXFrags = 2;
+  static constexpr int kRuns = G32 ? 2 : 1;  // runs of one group in a quarter
   struct Tile {
     __amdgpu_buffer_rsrc_t codes, scales, biases;
     uint32_t oc, os;
   };
-  struct Frag {
-    u32x4 q[2];
-    uint16_t s[kRuns], b[kRuns];
+  struct Piece {
+    u32x4 q[4];
+    uint16_t s[kRuns], b[kRuns];  // row l/4, quarter l%4
   };
 
   static __device__ __forceinline__ Tile tile(const WeightView &w, uint64_t base, uint32_t n0, uint32_t N, uint32_t lane) {
     Tile t;
-    const uint32_t rows = N - n0 < 16u ? N - n0 : 16u, lr = lane & 15u, g = lane >> 4, G = w.K / w.gs;
+    const uint32_t rows = N - n0 < 16u ? N - n0 : 16u, r = lane >> 2, p = lane & 3u, G = w.K / w.gs;
     const uint64_t row0 = base + n0;
     t.codes = make_rsrc((const uint8_t *)w.packed + row0 * w.K, rows * w.K);
     t.scales = make_rsrc(w.scales + row0 * G, rows * G * 2u);
     t.biases = make_rsrc(w.biases + row0 * G, rows * G * 2u);
-    t.oc = lr < rows ? lr * w.K + (G32 ? 8u : 16u) * g : kOutOfRange;
-    t.os = lr < rows ? lr * G * 2u : kOutOfRange;
+    t.oc = r < rows ? r * w.K + 16u * p : kOutOfRange;
+    t.os = r < rows ? r * G * 2u : kOutOfRange;
     return t;
   }
-  static __device__ __forceinline__ void load(Frag &f, const Tile &t, const WeightView &w, uint32_t c, uint32_t lane) {
+  template <int AUX>
+  static __device__ __forceinline__ void load(Piece &f, const Tile &t, const WeightView &w, uint32_t piece, uint32_t lane) {
+    const uint32_t p = lane & 3u, b0 = kPieceBytes * piece;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t k = kChunk * c + 64u * h;
-      if constexpr (G32) {
-        const u32x2 lo = buf_load_b64<kAuxNontemporal>(t.codes, k < w.K ? t.oc + k : kOutOfRange);
-        const u32x2 hi = buf_load_b64<kAuxNontemporal>(t.codes, k + 32u < w.K ? t.oc + k + 32u : kOutOfRange);
-        f.q[h] = u32x4{lo.x, lo.y, hi.x, hi.y};
-      } else {
-        f.q[h] = buf_load_b128<kAuxNontemporal>(t.codes, k < w.K ? t.oc + k : kOutOfRange);
-      }
-    }
+    for (int h = 0; h < 4; ++h)
+      f.q[h] = buf_load_b128<AUX>(t.codes, b0 + 64u * h + 16u * p < w.K ? t.oc + b0 + 64u * h : kOutOfRange);
+    const uint32_t gl = 31u - (uint32_t)__builtin_clz(w.gs);
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
-      const uint32_t k = kChunk * c + (kChunk / kRuns) * r;
-      const uint32_t o = k < w.K ? t.os + 2u * (k / w.gs) : kOutOfRange;
+      const uint32_t k = b0 + 64u * p + 32u * r;  // first k of the run
+      const uint32_t o = k < w.K ? t.os + 2u * (k >> gl) : kOutOfRange;
       f.s[r] = buf_load_b16(t.scales, o);
       f.b[r] = buf_load_b16(t.biases, o);
     }
   }
-  static __device__ __forceinline__ void load_x(XFrag &x, __amdgpu_buffer_rsrc_t r, uint32_t xo, uint32_t c, uint32_t K,
-                                                uint32_t lane) {
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const uint32_t k = kChunk * c + (G32 ? 32u * f : 64u * (f >> 1));  // first k of the run
-      const uint32_t kl = G32 ? k + 8u * (lane >> 4) : k + 16u * (lane >> 4) + 8u * (f & 1);
-      x[f] = buf_load_b128(r, k < K ? xo + 2u * kl : kOutOfRange);
-    }
-  }
-  template <int MT>
-  static __device__ __forceinline__ void sums(f32x4 (&S)[MT][4], const XFrag (&x)[MT]) {
+  static __device__ __forceinline__ uint32_t x_chunk(int f, uint32_t g) { return G32 ? 4u * f + g : 2u * g + f; }
+  struct Sums {
+    f32x4 v[kRuns];
+  };
+  static __device__ __forceinline__ void sums(Sums &S, const u32x4 (&x)[kXFrags]) {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int r = 0; r < kRuns; ++r) {
-        if constexpr (G32) {
-          S[mt][r] = mfma16(x[mt][r], bf16_ones(), zero);
-        } else {
-          S[mt][r] = mfma16(x[mt][2 * r], bf16_ones(), zero);
-          S[mt][r] = mfma16(x[mt][2 * r + 1], bf16_ones(), S[mt][r]);
-        }
-      }
+    S.v[0] = mfma16(x[0], bf16_ones(), zero);
+    if constexpr (G32)
+      S.v[1] = mfma16(x[1], bf16_ones(), zero);
+    else
+      S.v[0] = mfma16(x[1], bf16_ones(), S.v[0]);
   }
-  template <int MT>
-  static __device__ __forceinline__ void mac(f32x4 (&acc)[MT], const Frag &f, const XFrag (&x)[MT], const f32x4 (&S)[MT][4]) {
+  static __device__ __forceinline__ void mac(f32x4 &acc, u32x4 q, const Piece &f, int h, const u32x4 (&x)[kXFrags],
+                                             const Sums &S, uint32_t lane) {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
-      const float s = bf16_bits_to_f32(f.s[r]), b = bf16_bits_to_f32(f.b[r]);
-      u32x4 lo, hi;
+      const uint32_t sb = lane_get((uint32_t)f.s[r] | (uint32_t)f.b[r] << 16, 4u * (lane & 15u) + h);
+      const float s = bf16_lo(sb), b = bf16_hi(sb);
+      f32x4 P;
       if constexpr (G32) {
-        lo = r & 1 ? int8_codes_bf16(f.q[r >> 1].z, f.q[r >> 1].w) : int8_codes_bf16(f.q[r >> 1].x, f.q[r >> 1].y);
+        P = r ? mfma16(x[1], int8_codes_bf16(q.z, q.w), zero) : mfma16(x[0], int8_codes_bf16(q.x, q.y), zero);
       } else {
-        lo = int8_codes_bf16(f.q[r].x, f.q[r].y);
-        hi = int8_codes_bf16(f.q[r].z, f.q[r].w);
+        P = mfma16(x[0], int8_codes_bf16(q.x, q.y), zero);
+        P = mfma16(x[1], int8_codes_bf16(q.z, q.w), P);
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        f32x4 P;
-        if constexpr (G32) {
-          P = mfma16(x[mt][r], lo, zero);
-        } else {
-          P = mfma16(x[mt][2 * r], lo, zero);
-          P = mfma16(x[mt][2 * r + 1], hi, P);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[mt][i] = __builtin_fmaf(s, P[i], __builtin_fmaf(b, S[mt][r][i], acc[mt][i]));
-      }
+      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(s, P[i], __builtin_fmaf(b, S.v[r][i], acc[i]));
     }
   }
+  // G32: a lane's 16 bytes of the quarter are 8 of each run
+  static __device__ __forceinline__ u32x4 get(const uint8_t *lds, uint32_t lane) {
+    const uint32_t r = lane & 15u, g = lane >> 4;
+    const u32x2 lo = *reinterpret_cast<const u32x2 *>(lds + quarter_at(r, g >> 1) + 8u * (g & 1u));
+    const u32x2 hi = *reinterpret_cast<const u32x2 *>(lds + quarter_at(r, 2u + (g >> 1)) + 8u * (g & 1u));
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+  }
 };
+
+template <class F>
+__device__ __forceinline__ u32x4 weight_operand(const uint8_t *lds, uint32_t lane) {
+  return get_quarter(lds, lane);
+}
+template <>
+__device__ __forceinline__ u32x4 weight_operand<Int8Fmt<true>>(const uint8_t *lds, uint32_t lane) {
+  return Int8Fmt<true>::get(lds, lane);
+}
+
+// ---- one wave's stream ------------------------------------------------------------------------
+
+// BF16 activations of up to 4 NX (MXFP4) or 8 NX (8-bit) rows.
+template <class F, int NX>
+struct XBf16 {
+  static constexpr uint32_t kRows = 64u / F::kXChunks;         // rows a load
+  static constexpr uint32_t kLds = 1024u * NX;                 // a quarter's
+  struct Piece {
+    u32x4 v[4][NX];
+  };
+  __amdgpu_buffer_rsrc_t rsrc;
+  uint32_t K, xo[NX];  // byte offset of the lane's row of load j, with its chunk
+  // row(i): byte offset of activation row i, or kOutOfRange
+  template <class Row>
+  __device__ __forceinline__ XBf16(const void *x, uint32_t bytes, uint32_t K_, uint32_t lane, Row row) : K(K_) {
+    rsrc = make_rsrc(x, bytes);
+#pragma unroll
+    for (int j = 0; j < NX; ++j) xo[j] = row(kRows * j + lane / F::kXChunks) + 16u * (lane % F::kXChunks);
+  }
+  __device__ __forceinline__ void load(Piece &f, uint32_t piece, uint32_t lane) const {
+    const uint32_t b0 = piece * (2u * F::kPiece), c = 16u * (lane % F::kXChunks);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint32_t b = b0 + 2u * F::kQuarter * h;
+#pragma unroll
+      for (int j = 0; j < NX; ++j) f.v[h][j] = buf_load_b128(rsrc, b + c < 2u * K ? xo[j] + b : kOutOfRange);
+    }
+  }
+  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t c) {
+    return row * (16u * F::kXChunks) + 16u * (c ^ (row & (F::kXChunks - 1u)));
+  }
+  __device__ __forceinline__ void put(uint8_t *lds, const Piece &f, int h, uint32_t lane) const {
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+      *reinterpret_cast<u32x4 *>(lds + at(kRows * j + lane / F::kXChunks, lane % F::kXChunks)) = f.v[h][j];
+  }
+  // rows past the ones kept repeat the last: their results are not used
+  static __device__ __forceinline__ void get(u32x4 (&x)[F::kXFrags], const uint8_t *lds, uint32_t lane) {
+    uint32_t row = lane & 15u;
+    if (row >= kRows * NX) row = kRows * NX - 1u;
+#pragma unroll
+    for (int f = 0; f < F::kXFrags; ++f) x[f] = *reinterpret_cast<const u32x4 *>(lds + at(row, F::x_chunk(f, lane >> 4)));
+  }
+};
+
+// LDS bytes of one wave: two quarters (one is written while the other is read) of RT tiles and the activations.
+template <class X, int RT>
+constexpr uint32_t stream_lds() {
+  return 2u * (1024u * RT + X::kLds);
+}
+
+template <class F, class X, int RT>
+struct Pieces {
+  typename F::Piece w[RT];
+  typename X::Piece x;
+};
+
+// acc[t] += A B^T of one piece.
+template <class F, class X, int RT>
+__device__ __forceinline__ void stream_piece(f32x4 (&acc)[RT], const Pieces<F, X, RT> &p, const X &X_, uint8_t *lds,
+                                             uint32_t lane) {
+  constexpr uint32_t kHalf = stream_lds<X, RT>() / 2u;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint8_t *at = lds + (h & 1) * kHalf;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) put_quarter(at + 1024u * t, p.w[t].q[h], lane);
+    X_.put(at + 1024u * RT, p.x, h, lane);
+    wave_fence();
+    u32x4 x[F::kXFrags];
+    X::get(x, at + 1024u * RT, lane);
+    typename F::Sums S;
+    F::sums(S, x);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) F::mac(acc[t], weight_operand<F>(at + 1024u * t, lane), p.w[t], h, x, S, lane);
+    wave_fence();
+  }
+}
 
 }  // namespace int8w
