@@ -106,12 +106,18 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
 
 // ---- many rows --------------------------------------------------------------------------------
 
-constexpr uint32_t kChunk = 128;  // k of one fp4 MFMA
+constexpr uint32_t kChunk = 128;         // k of one fp4 MFMA
+constexpr uint32_t kGroup = 4 * kChunk;  // k of one scale load: 16 scale bytes a row
 
-// Tile BM rows of X times BN weight rows, WM x WN waves.  Both operands are
-// copied to LDS by DMA, two stages, a step of CH chunks each; 16-byte pieces of a
-// row are XOR-swizzled so that the rows of an operand read fall into distinct
-// banks.  A = weight rows, B = X rows: a lane's four results are neighbours in Y.
+// Tile BM rows of X times BN weight rows, WM x WN waves, steps of CH chunks.  Both
+// operands are copied to LDS by DMA, two stages; 16-byte pieces of a row are
+// XOR-swizzled so that the rows of an operand read fall into distinct banks.  A =
+// weight rows, B = X rows: a lane's four results are neighbours in Y.
+// Scales: loaded a group ahead, a lane per row and 16 bytes (block g of chunk c at
+// byte 4c + g), transposed to bytes 4g + c and put in LDS, so that a lane gets its
+// row's scales of block g for all four chunks as one dword whose byte c the scaled
+// MFMA selects.  (Loading each lane's own byte took 24 scattered loads a wave and
+// step: 236 us instead of the figure below at m = 2048.)
 template <bool XMX, int BM, int BN, int WM, int WN, int CH>
 struct MxTile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -119,8 +125,12 @@ struct MxTile {
   static constexpr uint32_t XB = (XMX ? 64u : 256u) * CH;     // bytes of an X row in a step
   static constexpr uint32_t WB = 64u * CH;
   static constexpr uint32_t X_BYTES = BM * XB, W_BYTES = BN * WB, STAGE = X_BYTES + W_BYTES;
+  static constexpr uint32_t SROWS = BN + (XMX ? BM : 0);  // scale rows: the weight's, then X's
+  static constexpr int NS = (int)((SROWS + kThreads - 1) / kThreads);  // scale rows a lane
+  static constexpr uint32_t LDS = 2u * STAGE + 2u * 16u * SROWS;
   static constexpr int NX = (int)(X_BYTES / 1024u / kWaves), NW = (int)(W_BYTES / 1024u / kWaves);
   static_assert(X_BYTES % (1024u * kWaves) == 0 && W_BYTES % (1024u * kWaves) == 0, "whole loads a wave");
+  static_assert(CH == 1 || CH == 2, "a group is two or four steps");
 };
 
 // piece index -> swizzled piece, rows of P 16-byte pieces
@@ -129,6 +139,21 @@ __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t c) {
   if constexpr (P >= 16u) return c ^ (row & 15u);
   if constexpr (P == 8u) return c ^ (row & 7u);
   return c ^ ((row >> 1) & 3u);
+}
+
+template <int C>
+__device__ __forceinline__ f32x4 mfma_mx_sel(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
+  const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, C, (int)sa, C, (int)sb);
+}
+
+// 4 x 4 bytes: byte 4c + g -> 4g + c
+__device__ __forceinline__ u32x4 transpose_bytes(u32x4 v) {
+  const uint32_t ab02 = __builtin_amdgcn_perm(v.y, v.x, 0x06020400u), ab13 = __builtin_amdgcn_perm(v.y, v.x, 0x07030501u);
+  const uint32_t cd02 = __builtin_amdgcn_perm(v.w, v.z, 0x06020400u), cd13 = __builtin_amdgcn_perm(v.w, v.z, 0x07030501u);
+  return u32x4{__builtin_amdgcn_perm(cd02, ab02, 0x05040100u), __builtin_amdgcn_perm(cd13, ab13, 0x05040100u),
+               __builtin_amdgcn_perm(cd02, ab02, 0x07060302u), __builtin_amdgcn_perm(cd13, ab13, 0x07060302u)};
 }
 
 template <bool XMX, int BM, int BN, int WM, int WN, int CH>
@@ -144,11 +169,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_
   const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / 8u;
   const uint32_t m0 = (id % mt_count) * BM, n0 = (id / mt_count) * BN;
   const uint32_t mrows = m - m0 < BM ? m - m0 : BM, nrows = w.N - n0 < BN ? w.N - n0 : BN;
-  const uint32_t xrow = XMX ? K / 2u : K * 2u, wrow = K / 2u;  // bytes a row
+  const uint32_t xrow = XMX ? K / 2u : K * 2u, wrow = K / 2u, srow = K / 32u;  // bytes a row
   const auto rx = make_rsrc(x + (size_t)m0 * xrow, mrows * xrow);
   const auto rw = make_rsrc(w.codes + (size_t)n0 * wrow, nrows * wrow);
-  const auto rws = make_rsrc(w.scales + (size_t)n0 * (K / 32u), nrows * (K / 32u));
-  const auto rxs = make_rsrc(XMX ? xs + (size_t)m0 * (K / 32u) : w.scales, XMX ? mrows * (K / 32u) : 0u);
+  const uint8_t *const wsp = w.scales + (size_t)n0 * srow, *const xsp = XMX ? xs + (size_t)m0 * srow : nullptr;
+  const auto rws = make_rsrc(wsp, nrows * srow), rxs = make_rsrc(xsp, XMX ? mrows * srow : 0u);
+  // scales sixteen at a time where every row of them is whole dwords
+  const bool dwords = K % kChunk == 0 && ((reinterpret_cast<uintptr_t>(wsp) | reinterpret_cast<uintptr_t>(xsp)) & 3u) == 0;
 
   uint32_t vx[S::NX], vw[S::NW];  // byte offset of this lane's piece at step 0
   uint32_t px[S::NX], pw[S::NW];  // ... and within its row's step
@@ -179,27 +206,57 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_
           (int)(in ? vw[j] + step * S::WB : kOutOfRange), 0, 0, 0);
     }
   };
-  // scale bytes of a step: one per lane, chunk and 16-row tile, straight to registers
-  struct Scales {
-    uint32_t w[CH][S::TN], x[XMX ? CH : 1][XMX ? S::TM : 1];
-  };
-  auto scales = [&](Scales &s, uint32_t step) {
+  auto load_scales = [&](u32x4 (&v)[S::NS], uint32_t group) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const uint32_t blk = 4u * (step * CH + c) + g;
-      const bool in = blk < K / 32u;
+    for (int j = 0; j < S::NS; ++j) {
+      const uint32_t row = (uint32_t)S::kThreads * j + tid;
+      const bool isw = row < BN;
+      const uint32_t r = isw ? row : row - BN;
+      const bool have = isw ? r < nrows : XMX && row < S::SROWS && r < mrows;
+      const uint32_t at = r * srow + 16u * group;
+      auto one = [&](const __amdgpu_buffer_rsrc_t rs, bool mine) {
+        u32x4 o = {0u, 0u, 0u, 0u};
+        if (dwords && srow % 16u == 0u) {
+          o = buf_load_b128(rs, mine && 16u * group < srow ? at : kOutOfRange);
+        } else {
 #pragma unroll
-      for (int t = 0; t < S::TN; ++t) {
-        const uint32_t row = (wn * S::TN + t) * 16u + lr;
-        s.w[c][t] = __builtin_amdgcn_raw_buffer_load_b8(rws, (int)(in && row < nrows ? row * (K / 32u) + blk : kOutOfRange), 0, 0);
-      }
-      if constexpr (XMX)
+          for (uint32_t c = 0; c < 4u; ++c)
+            if (dwords) {
+              o[c] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(mine && 16u * group + 4u * c < srow ? at + 4u * c : kOutOfRange), 0, 0);
+            } else {
 #pragma unroll
-        for (int t = 0; t < S::TM; ++t) {
-          const uint32_t row = (wm * S::TM + t) * 16u + lr;
-          s.x[c][t] = __builtin_amdgcn_raw_buffer_load_b8(rxs, (int)(in && row < mrows ? row * (K / 32u) + blk : kOutOfRange), 0, 0);
+              for (uint32_t i = 0; i < 4u; ++i)
+                o[c] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                            rs, (int)(mine && 16u * group + 4u * c + i < srow ? at + 4u * c + i : kOutOfRange), 0, 0) << (8u * i);
+            }
         }
+        return o;
+      };
+      // a wave's 64 rows are all the weight's or all X's (BN is a multiple of 64)
+      if (!XMX || uniform32(row) < BN)
+        v[j] = one(rws, have);
+      else
+        v[j] = one(rxs, have);
     }
+  };
+  uint8_t *const sbase = lds_mx + 2u * S::STAGE;
+  auto put_scales = [&](const u32x4 (&v)[S::NS], uint32_t buf) {
+#pragma unroll
+    for (int j = 0; j < S::NS; ++j) {
+      const uint32_t row = (uint32_t)S::kThreads * j + tid;
+      if (S::SROWS % S::kThreads == 0 || row < S::SROWS)
+        *reinterpret_cast<u32x4 *>(sbase + buf * (16u * S::SROWS) + 16u * row) = transpose_bytes(v[j]);
+    }
+  };
+  uint32_t sw[S::TN], sx[XMX ? S::TM : 1];  // this group's: byte c is chunk c's
+  auto get_scales = [&](uint32_t buf) {
+    const uint8_t *at = sbase + buf * (16u * S::SROWS) + 4u * g;
+#pragma unroll
+    for (int t = 0; t < S::TN; ++t) sw[t] = *reinterpret_cast<const uint32_t *>(at + 16u * ((wn * S::TN + t) * 16u + lr));
+    if constexpr (XMX)
+#pragma unroll
+      for (int t = 0; t < S::TM; ++t)
+        sx[t] = *reinterpret_cast<const uint32_t *>(at + 16u * (BN + (wm * S::TM + t) * 16u + lr));
   };
   f32x4 acc[S::TN][S::TM];
 #pragma unroll
@@ -207,76 +264,90 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_
 #pragma unroll
     for (int j = 0; j < S::TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](const Scales &s, const uint8_t *base) {
+  // chunk C of the group, the step's chunk c
+  auto chunk = [&](auto tag, int c, const uint8_t *base) {
+    constexpr int C = decltype(tag)::value;
     const uint8_t *xb = base, *wb = base + S::X_BYTES;
+    if constexpr (XMX) {
+      u32x4 b[S::TM];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if constexpr (XMX) {
-        u32x4 b[S::TM];
+      for (int j = 0; j < S::TM; ++j) {
+        const uint32_t row = (wm * S::TM + j) * 16u + lr;
+        b[j] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 4u * c + g));
+      }
 #pragma unroll
-        for (int j = 0; j < S::TM; ++j) {
-          const uint32_t row = (wm * S::TM + j) * 16u + lr;
-          b[j] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 4u * c + g));
-        }
+      for (int i = 0; i < S::TN; ++i) {
+        const uint32_t row = (wn * S::TN + i) * 16u + lr;
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
 #pragma unroll
-        for (int i = 0; i < S::TN; ++i) {
-          const uint32_t row = (wn * S::TN + i) * 16u + lr;
-          const u32x4 a = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
+        for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma_mx_sel<C>(a, sw[i], b[j], sx[j], acc[i][j]);
+      }
+    } else {
+      u32x4 b[S::TM][4];
 #pragma unroll
-          for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma_mx(a, s.w[c][i], b[j], s.x[c][j], acc[i][j]);
-        }
-      } else {
-        u32x4 b[S::TM][4];
+      for (int j = 0; j < S::TM; ++j) {
+        const uint32_t row = (wm * S::TM + j) * 16u + lr;
 #pragma unroll
-        for (int j = 0; j < S::TM; ++j) {
-          const uint32_t row = (wm * S::TM + j) * 16u + lr;
+        for (int f = 0; f < 4; ++f)
+          b[j][f] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 16u * c + 4u * g + f));
+      }
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            b[j][f] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 16u * c + 4u * g + f));
-        }
+      for (int i = 0; i < S::TN; ++i) {
+        const uint32_t row = (wn * S::TN + i) * 16u + lr;
+        const u32x4 q = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
+        const float sc = mx_scale_f32((sw[i] >> (8 * C)) & 0xFFu);
 #pragma unroll
-        for (int i = 0; i < S::TN; ++i) {
-          const uint32_t row = (wn * S::TN + i) * 16u + lr;
-          const u32x4 q = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
-          const float sc = mx_scale_f32(s.w[c][i]);
+        for (int f = 0; f < 4; ++f) {
+          const uint4 a = mx_to_bf16x8(q[f], sc);
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const uint4 a = mx_to_bf16x8(q[f], sc);
-#pragma unroll
-            for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma16(u32x4{a.x, a.y, a.z, a.w}, b[j][f], acc[i][j]);
-          }
+          for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma16(u32x4{a.x, a.y, a.z, a.w}, b[j][f], acc[i][j]);
         }
       }
     }
   };
-
-  const uint32_t steps = (K + kChunk * CH - 1u) / (kChunk * CH);
-  Scales s0, s1;
-  dma(0, lds_mx);
-  scales(s0, 0);
   // One barrier a step.  Before it every wave has waited for its own loads of the
-  // next step (all of them: DMA and register loads are never counted apart) and
-  // has read its operands of this one, so after it the next stage is whole and
-  // this one may be filled again.
-  auto sync = [&]() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
+  // next step (all of them: DMA and register loads are never counted apart) and has
+  // read its operands of this one, so after it the next stage is whole and this one
+  // may be filled again.
+  auto sync = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  const uint32_t groups = (K + kGroup - 1u) / kGroup;
+  u32x4 sv[S::NS];
+  load_scales(sv, 0);
+  dma(0, lds_mx);
+  put_scales(sv, 0);
   sync();
-  for (uint32_t s = 0;;) {
-    if (s + 1u < steps) {
-      dma(s + 1u, lds_mx + S::STAGE);
-      scales(s1, s + 1u);
+  // steps past K read zeros (a whole group is always walked)
+  uint8_t *const st0 = lds_mx, *const st1 = lds_mx + S::STAGE;
+  for (uint32_t q = 0; q < groups; ++q) {
+    get_scales(q & 1u);
+    if constexpr (CH == 2) {
+      dma(2u * q + 1u, st1);
+      load_scales(sv, q + 1u);
+      chunk(std::integral_constant<int, 0>{}, 0, st0);
+      chunk(std::integral_constant<int, 1>{}, 1, st0);
+      sync();
+      dma(2u * q + 2u, st0);
+      chunk(std::integral_constant<int, 2>{}, 0, st1);
+      chunk(std::integral_constant<int, 3>{}, 1, st1);
+      put_scales(sv, (q + 1u) & 1u);
+      sync();
+    } else {
+      dma(4u * q + 1u, st1);
+      load_scales(sv, q + 1u);
+      chunk(std::integral_constant<int, 0>{}, 0, st0);
+      sync();
+      dma(4u * q + 2u, st0);
+      chunk(std::integral_constant<int, 1>{}, 0, st1);
+      sync();
+      dma(4u * q + 3u, st1);
+      chunk(std::integral_constant<int, 2>{}, 0, st0);
+      sync();
+      dma(4u * q + 4u, st0);
+      chunk(std::integral_constant<int, 3>{}, 0, st1);
+      put_scales(sv, (q + 1u) & 1u);
+      sync();
     }
-    compute(s0, lds_mx);
-    if (++s >= steps) break;
-    sync();
-    if (s + 1u < steps) {
-      dma(s + 1u, lds_mx);
-      scales(s0, s + 1u);
-    }
-    compute(s1, lds_mx + S::STAGE);
-    if (++s >= steps) break;
-    sync();
   }
   // D[4 g + r][lr]: weight row 4 g + r, X row lr
   const bool wide = w.N % 4u == 0u && (reinterpret_cast<uintptr_t>(y) & 7u) == 0u;
@@ -318,9 +389,9 @@ hipError_t launch_tile(const MxView &w, const void *x, const uint8_t *xs, uint32
   using S = MxTile<XMX, BM, BN, WM, WN, CH>;
   const uint32_t mt = (m + BM - 1u) / BM, nt = (w.N + BN - 1u) / BN;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<XMX, BM, BN, WM, WN, CH>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)(2u * S::STAGE));
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS);
   if (e != hipSuccess) return e;
-  k_mx_tile<XMX, BM, BN, WM, WN, CH><<<mt * nt, S::kThreads, 2u * S::STAGE, stream>>>(w, (const uint8_t *)x, xs, m, y, mt);
+  k_mx_tile<XMX, BM, BN, WM, WN, CH><<<mt * nt, S::kThreads, S::LDS, stream>>>(w, (const uint8_t *)x, xs, m, y, mt);
   return hipGetLastError();
 }
 
@@ -336,7 +407,7 @@ hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_
   if constexpr (XMX)
     return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
   else
-    return launch_tile<false, 128, 256, 2, 2, 1>(w, x, xs, m, y, stream);
+    return launch_tile<false, 128, 256, 2, 4, 1>(w, x, xs, m, y, stream);
 }
 
 }  // namespace
