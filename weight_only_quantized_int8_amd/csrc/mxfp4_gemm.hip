@@ -118,19 +118,20 @@ constexpr uint32_t kGroup = 4 * kChunk;  // k of one scale load: 16 scale bytes 
 // row's scales of block g for all four chunks as one dword whose byte c the scaled
 // MFMA selects.  (Loading each lane's own byte took 24 scattered loads a wave and
 // step: 236 us instead of the figure below at m = 2048.)
-template <bool XMX, int BM, int BN, int WM, int WN, int CH>
+template <bool XMX, int BM, int BN, int WM, int WN, int CH, int KG>
 struct MxTile {
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;  // of one K part
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16-row tiles a wave
   static constexpr uint32_t XB = (XMX ? 64u : 256u) * CH;     // bytes of an X row in a step
   static constexpr uint32_t WB = 64u * CH;
   static constexpr uint32_t X_BYTES = BM * XB, W_BYTES = BN * WB, STAGE = X_BYTES + W_BYTES;
   static constexpr uint32_t SROWS = BN + (XMX ? BM : 0);  // scale rows: the weight's, then X's
   static constexpr int NS = (int)((SROWS + kThreads - 1) / kThreads);  // scale rows a lane
-  static constexpr uint32_t LDS = 2u * STAGE + 2u * 16u * SROWS;
+  static constexpr uint32_t PART = 2u * STAGE + 2u * 16u * SROWS, LDS = KG * PART;  // LDS of a K part, of all
   static constexpr int NX = (int)(X_BYTES / 1024u / kWaves), NW = (int)(W_BYTES / 1024u / kWaves);
   static_assert(X_BYTES % (1024u * kWaves) == 0 && W_BYTES % (1024u * kWaves) == 0, "whole loads a wave");
   static_assert(CH == 1 || CH == 2, "a group is two or four steps");
+  static_assert(KG == 1 || KG * (uint32_t)kThreads * 16u <= LDS, "one 16 x 16 result of every wave fits");
 };
 
 // piece index -> swizzled piece, rows of P 16-byte pieces
@@ -156,13 +157,17 @@ __device__ __forceinline__ u32x4 transpose_bytes(u32x4 v) {
                __builtin_amdgcn_perm(cd02, ab02, 0x07060302u), __builtin_amdgcn_perm(cd13, ab13, 0x07060302u)};
 }
 
-template <bool XMX, int BM, int BN, int WM, int WN, int CH>
-__global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_t *__restrict__ x,
+template <bool XMX, int BM, int BN, int WM, int WN, int CH, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG) void k_mx_tile(MxView w, const uint8_t *__restrict__ x,
                                                           const uint8_t *__restrict__ xs, uint32_t m,
                                                           uint16_t *__restrict__ y, uint32_t mt_count) {
-  using S = MxTile<XMX, BM, BN, WM, WN, CH>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds_mx[];
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform32(tid >> 6), lr = lane & 15u, g = lane >> 4;
+  using S = MxTile<XMX, BM, BN, WM, WN, CH, KG>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_all[];
+  // the K part's own threads, waves and LDS
+  const uint32_t part = KG == 1 ? 0u : uniform32(threadIdx.x / (uint32_t)S::kThreads);
+  const uint32_t tid = threadIdx.x - part * (uint32_t)S::kThreads, lane = tid & 63u, wave = uniform32(tid >> 6);
+  const uint32_t lr = lane & 15u, g = lane >> 4;
+  uint8_t *const lds_mx = lds_all + part * S::PART;
   const uint32_t wm = wave % WM, wn = wave / WM, K = w.K;
   // workgroups are dealt to the 8 XCDs in turn: give each XCD neighbouring tiles, X tiles of one weight tile first
   const uint32_t total = gridDim.x, per = total / 8u, extra = total % 8u, xcd = blockIdx.x % 8u;
@@ -311,30 +316,33 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_
   // may be filled again.
   auto sync = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-  const uint32_t groups = (K + kGroup - 1u) / kGroup;
+  // K part p walks groups p, p + KG, ...; all parts make the same number of steps, and
+  // steps past K read zeros
+  const uint32_t groups = (K + kGroup - 1u) / kGroup, rounds = (groups + KG - 1u) / KG;
+  constexpr uint32_t SPG = 4 / CH;  // steps a group
   u32x4 sv[S::NS];
-  load_scales(sv, 0);
-  dma(0, lds_mx);
+  load_scales(sv, part);
+  dma(part * SPG, lds_mx);
   put_scales(sv, 0);
   sync();
-  // steps past K read zeros (a whole group is always walked)
   uint8_t *const st0 = lds_mx, *const st1 = lds_mx + S::STAGE;
-  for (uint32_t q = 0; q < groups; ++q) {
-    get_scales(q & 1u);
+  for (uint32_t i = 0; i < rounds; ++i) {
+    const uint32_t q = part + KG * i;
+    get_scales(i & 1u);
     if constexpr (CH == 2) {
       dma(2u * q + 1u, st1);
-      load_scales(sv, q + 1u);
+      load_scales(sv, q + KG);
       chunk(std::integral_constant<int, 0>{}, 0, st0);
       chunk(std::integral_constant<int, 1>{}, 1, st0);
       sync();
-      dma(2u * q + 2u, st0);
+      dma(2u * (q + KG), st0);
       chunk(std::integral_constant<int, 2>{}, 0, st1);
       chunk(std::integral_constant<int, 3>{}, 1, st1);
-      put_scales(sv, (q + 1u) & 1u);
+      put_scales(sv, (i + 1u) & 1u);
       sync();
     } else {
       dma(4u * q + 1u, st1);
-      load_scales(sv, q + 1u);
+      load_scales(sv, q + KG);
       chunk(std::integral_constant<int, 0>{}, 0, st0);
       sync();
       dma(4u * q + 2u, st0);
@@ -343,11 +351,27 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tile(MxView w, const uint8_
       dma(4u * q + 3u, st1);
       chunk(std::integral_constant<int, 2>{}, 0, st0);
       sync();
-      dma(4u * q + 4u, st0);
+      dma(4u * (q + KG), st0);
       chunk(std::integral_constant<int, 3>{}, 0, st1);
-      put_scales(sv, (q + 1u) & 1u);
+      put_scales(sv, (i + 1u) & 1u);
       sync();
     }
+  }
+  if constexpr (KG > 1) {  // the parts' sums, added in order by part 0
+    f32x4 *const red = reinterpret_cast<f32x4 *>(lds_all);
+#pragma unroll
+    for (int i = 0; i < S::TN; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TM; ++j) {
+        red[threadIdx.x] = acc[i][j];
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+          for (int p = 1; p < KG; ++p) acc[i][j] += red[tid + (uint32_t)(p * S::kThreads)];
+        }
+        __syncthreads();
+      }
+    if (part != 0) return;
   }
   // D[4 g + r][lr]: weight row 4 g + r, X row lr
   const bool wide = w.N % 4u == 0u && (reinterpret_cast<uintptr_t>(y) & 7u) == 0u;
@@ -384,14 +408,14 @@ hipError_t launch_rows(const MxView &w, const void *x, const uint8_t *xs, uint32
   return hipGetLastError();
 }
 
-template <bool XMX, int BM, int BN, int WM, int WN, int CH>
+template <bool XMX, int BM, int BN, int WM, int WN, int CH, int KG = 1>
 hipError_t launch_tile(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
-  using S = MxTile<XMX, BM, BN, WM, WN, CH>;
+  using S = MxTile<XMX, BM, BN, WM, WN, CH, KG>;
   const uint32_t mt = (m + BM - 1u) / BM, nt = (w.N + BN - 1u) / BN;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<XMX, BM, BN, WM, WN, CH>),
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<XMX, BM, BN, WM, WN, CH, KG>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS);
   if (e != hipSuccess) return e;
-  k_mx_tile<XMX, BM, BN, WM, WN, CH><<<mt * nt, S::kThreads, S::LDS, stream>>>(w, (const uint8_t *)x, xs, m, y, mt);
+  k_mx_tile<XMX, BM, BN, WM, WN, CH, KG><<<mt * nt, S::kThreads * KG, S::LDS, stream>>>(w, (const uint8_t *)x, xs, m, y, mt);
   return hipGetLastError();
 }
 
@@ -401,13 +425,26 @@ hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_
   if (m <= 4u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
   if (m <= 8u) return launch_rows<XMX, 2, kAuxNontemporal>(w, x, xs, m, y, stream);
   if (m <= 16u) return launch_rows<XMX, 4, kAuxNontemporal>(w, x, xs, m, y, stream);
-  if (m <= 64u) return launch_rows<XMX, XMX ? 1 : 4, 0>(w, x, xs, m, y, stream);
-  const uint32_t big = XMX ? ((m + 255u) / 256u) * ((w.N + 255u) / 256u) : ((m + 127u) / 128u) * ((w.N + 255u) / 256u);
-  if (big < (uint32_t)device_cu_count() / 2u) return launch_tile<XMX, 64, 64, 2, 2, XMX ? 2 : 1>(w, x, xs, m, y, stream);
-  if constexpr (XMX)
-    return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
-  else
-    return launch_tile<false, 128, 256, 2, 4, 1>(w, x, xs, m, y, stream);
+  // 17..64 rows: one workgroup per group of 16 rows and tile, as long as that is a few
+  // workgroups a CU (m = 64, us against the tiled kernel: 4096x14336 40 / 46, X MXFP4 20 / 23,
+  // but 14336x4096 59 / 18 and 25 / 12).
+  const uint32_t cus = (uint32_t)device_cu_count();
+  if (m <= 64u && (m + 15u) / 16u * ((w.N + 15u) / 16u) <= 4u * cus) return launch_rows<XMX, XMX ? 1 : 4, 0>(w, x, xs, m, y, stream);
+  // Tiles of 64 x 64 where the large ones would leave half the GPU idle.  Such a launch is
+  // bound by the latency of a step, so K is dealt to parts of the workgroup, the more the
+  // fewer tiles there are (4096x14336, one part / several, us: X BF16 m = 128 66 / 47,
+  // m = 512 77 / 71 as 64 x 128; X MXFP4 m = 128 40 / 27 with 4 parts, m = 512 44 / 36 with 2).
+  const uint32_t big = ((m + (XMX ? 255u : 127u)) / (XMX ? 256u : 128u)) * ((w.N + 255u) / 256u);
+  const bool few = (m + 63u) / 64u * ((w.N + 63u) / 64u) <= cus;
+  if constexpr (XMX) {
+    if (big >= cus / 2u) return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
+    if (few) return launch_tile<true, 64, 64, 2, 2, 2, 4>(w, x, xs, m, y, stream);
+    return launch_tile<true, 64, 64, 2, 2, 2, 2>(w, x, xs, m, y, stream);
+  } else {
+    if (big >= cus / 2u) return launch_tile<false, 128, 256, 2, 4, 1>(w, x, xs, m, y, stream);
+    if (few) return launch_tile<false, 64, 64, 2, 2, 1, 2>(w, x, xs, m, y, stream);
+    return launch_tile<false, 64, 128, 2, 2, 1, 2>(w, x, xs, m, y, stream);
+  }
 }
 
 }  // namespace
