@@ -22,6 +22,7 @@
 // most 2^-9 a value averages out over the inner sum to about the output's own BF16
 // rounding.  All sums, the softmax and the routing weights are fp32.
 #include "rows_stream.h"
+#include "token_stream.h"
 #include "launch.h"
 
 namespace int8w {
@@ -313,6 +314,262 @@ __global__ __launch_bounds__(64 * KS) void k_moe_down(typename F::View wd, uint3
   }
 }
 
+// ---- one token --------------------------------------------------------------------------------
+// Two launches: each wave of the first routes the token itself (a few hundred cycles, against
+// a launch of its own), so that no kernel has to come before the first weight load.
+
+// Waves share the gate/up row pairs of the chosen experts evenly.  LDS: x.
+template <class F, int KW, int U, int R>
+__global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typename F::View wu, uint32_t I,
+                                                     const uint16_t *__restrict__ x, const void *__restrict__ logits,
+                                                     bool bf16, uint32_t E, uint32_t topk, bool renorm, float scale,
+                                                     MoeHead *__restrict__ head, uint16_t *__restrict__ h) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wg.K, segs = token_segs<F>(K);
+  uint32_t id;
+  float w;
+  const bool is_nan = route_token<R>(logits, bf16, 0, E, topk, renorm, scale, lane, id, w);
+  const uint32_t n = (uint32_t)__popcll(__ballot(id < kMaxE));  // choices 0 .. n-1: their weights fall
+  if (blockIdx.x == 0 && wave == 0) {
+    if (lane < topk) {
+      head->seg[lane].expert = id;
+      head->seg[lane].n = 1u;
+    }
+    if (lane == 0) {
+      head->segments = n;
+      head->nan[0] = is_nan ? 1u : 0u;
+    }
+  }
+  const uint32_t units = gridDim.x * KW, unit = blockIdx.x * KW + wave, pairs = n * I;
+  const uint32_t p0 = (uint32_t)((uint64_t)pairs * unit / units), p1 = (uint32_t)((uint64_t)pairs * (unit + 1u) / units);
+  uint32_t lj = p0 / I, li = p0 - lj * I, ls = 0, left = (p1 - p0) * segs;  // the next load
+  typename F::Row rg, ru;
+  auto rows = [&]() {
+    const bool have = lj < n;
+    const uint64_t r = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)id, (int)(have ? lj : 0u)) * I + li;
+    rg = F::row(wg, have ? r : 0u, have);
+    ru = F::row(wu, have ? r : 0u, have);
+  };
+  rows();
+  TokenPair<F> ring[U];
+  auto load = [&](TokenPair<F> &t) {
+    const uint32_t s = left ? ls : segs;  // segment segs: past the row's end, zeros
+    F::load(t.a, rg, wg, s, lane);
+    F::load(t.b, ru, wu, s, lane);
+    token_order();
+    if (left) {
+      --left;
+      if (++ls == segs) {
+        ls = 0;
+        if (++li == I) {
+          li = 0;
+          ++lj;
+        }
+        rows();
+      }
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(ring[u]);
+  stage_token<F>(lds, x, K, threadIdx.x, 64u * KW);
+  __syncthreads();
+  uint32_t cp = p0, cs = 0;
+  float g = 0.f, up = 0.f;
+  for (uint32_t i = 0, items = (p1 - p0) * segs; i < items; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < items) {
+        u32x4 xv[F::kX];
+        float xsum;
+        get_token<F>(xv, xsum, lds, segs, cs, lane);
+        g = F::dot(g, ring[u].a, xv, xsum);
+        up = F::dot(up, ring[u].b, xv, xsum);
+        if (++cs == segs) {
+          cs = 0;
+          const float gs = token_sum(g), us = token_sum(up);
+          const uint32_t j = cp / I;
+          const float r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(w), (int)j));
+          if (lane == 0) h[cp] = to_bf16_bits(r * silu_mul(gs, us));
+          g = up = 0.f;
+          ++cp;
+        }
+      }
+      token_order();
+      load(ring[u]);
+    }
+  }
+}
+
+// Waves share the pairs of output rows; KS neighbouring waves share a pair's experts and
+// segments where there are few pairs.  LDS: h of the chosen experts.
+template <class F, int KW, int U, int KS>
+__global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint32_t H, const uint16_t *__restrict__ h,
+                                                       const MoeHead *__restrict__ head,
+                                                       const uint16_t *__restrict__ resid, uint16_t *__restrict__ y) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ float red[KW][2];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wd.K, segs = token_segs<F>(K);
+  const uint32_t n = uniform32(head->segments), ids = head->seg[lane < kMaxTopk ? lane : 0u].expert;
+  const uint32_t units = gridDim.x * (KW / KS), unit = blockIdx.x * (KW / KS) + wave / KS, ks = wave % KS;
+  const uint32_t pairs = (H + 1u) / 2u;
+  const uint32_t p0 = (uint32_t)((uint64_t)pairs * unit / units), p1 = (uint32_t)((uint64_t)pairs * (unit + 1u) / units);
+  const uint32_t q0 = n * segs * ks / KS, q1 = n * segs * (ks + 1u) / KS;  // the wave's share of a pair
+  const uint32_t j0 = q0 / segs, s0 = q0 - j0 * segs;
+  uint32_t lp = p0, lq = q0, lj = j0, ls = s0;  // the next load
+  typename F::Row ra, rb;
+  auto rows = [&]() {
+    const bool have = lp < p1 && lj < n;
+    const uint64_t r = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)ids, (int)(have ? lj : 0u)) * H + 2u * lp;
+    ra = F::row(wd, have ? r : 0u, have);
+    rb = F::row(wd, have && 2u * lp + 1u < H ? r + 1u : 0u, have && 2u * lp + 1u < H);
+  };
+  rows();
+  TokenPair<F> ring[U];
+  auto load = [&](TokenPair<F> &t) {
+    F::load(t.a, ra, wd, ls, lane);
+    F::load(t.b, rb, wd, ls, lane);
+    token_order();
+    ++lq;
+    if (++ls == segs || lq == q1) {
+      ls = 0;
+      ++lj;
+      if (lq >= q1) {
+        ++lp;
+        lq = q0;
+        lj = j0;
+        ls = s0;
+      }
+      rows();
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(ring[u]);
+  const uint32_t stride = token_lds<F>(K);
+  for (uint32_t j = 0; j < n; ++j) stage_token<F>(lds + j * stride, h + (size_t)j * K, K, threadIdx.x, 64u * KW);
+  __syncthreads();
+  float a = 0.f, b = 0.f;
+  uint32_t cp = p0, cq = q0, cj = j0, cs = s0;
+  auto store = [&](uint32_t p, float va, float vb) {
+    const uint32_t r = 2u * p + lane;
+    if (lane < 2u && r < H) {
+      float v = lane ? vb : va;
+      if (head->nan[0]) v = __builtin_nanf("");
+      if (resid) v += bf16_bits_to_f32(resid[r]);
+      y[r] = to_bf16_bits(v);
+    }
+  };
+  for (uint32_t i = 0, items = (p1 - p0) * (q1 - q0); i < items; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < items) {
+        u32x4 xv[F::kX];
+        float xsum;
+        get_token<F>(xv, xsum, lds + cj * stride, segs, cs, lane);
+        a = F::dot(a, ring[u].a, xv, xsum);
+        b = F::dot(b, ring[u].b, xv, xsum);
+        if (++cs == segs) {
+          cs = 0;
+          ++cj;
+        }
+        if (++cq == q1) {
+          cq = q0;
+          cj = j0;
+          cs = s0;
+          if constexpr (KS == 1) {
+            store(cp, token_sum(a), token_sum(b));
+            a = b = 0.f;
+          }
+          ++cp;
+        }
+      }
+      token_order();
+      load(ring[u]);
+    }
+  }
+  if (KS == 1 && n == 0u)  // no expert taken
+    for (uint32_t p = p0; p < p1; ++p) store(p, 0.f, 0.f);
+  if constexpr (KS > 1) {
+    a = token_sum(a);
+    b = token_sum(b);
+    if (lane == 0) {
+      red[wave][0] = a;
+      red[wave][1] = b;
+    }
+    __syncthreads();
+    if (ks == 0 && p0 < p1) {
+      a = b = 0.f;
+#pragma unroll
+      for (uint32_t k = 0; k < (uint32_t)KS; ++k) {
+        a += red[wave + k][0];
+        b += red[wave + k][1];
+      }
+      store(p0, a, b);
+    }
+  }
+}
+
+constexpr uint32_t kLdsBytes = 160u << 10;
+
+// Whether the one-token kernels' activations fit the LDS.
+template <class F>
+bool one_token_fits(uint32_t H, uint32_t I, uint32_t topk) {
+  return token_lds<F>(H) <= kLdsBytes - 1024u && (uint64_t)topk * token_lds<F>(I) <= kLdsBytes - 1024u;
+}
+
+template <class K>
+hipError_t allow_lds(K kernel, uint32_t lds) {
+  if (lds <= 64u << 10) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+}
+
+template <class F, int KW, int R>
+hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, const MoeArgs &m, MoeHead *head, uint16_t *h,
+                         uint32_t I, uint32_t lds, hipStream_t stream) {
+  auto kern = k_moe1_up<F, KW, 4, R>;
+  hipError_t e = allow_lds(kern, lds);
+  if (e != hipSuccess) return e;
+  const uint32_t cus = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW, most = cus * 16u / KW;
+  kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits, m.logits_bf16, m.E, m.topk, m.renorm,
+                                                           m.scale, head, h);
+  return hipGetLastError();
+}
+
+template <class F, int KW, int KS>
+hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead *head, const uint16_t *h, uint32_t H,
+                           uint32_t lds, hipStream_t stream) {
+  auto kern = k_moe1_down<F, KW, 4, KS>;
+  hipError_t e = allow_lds(kern, lds);
+  if (e != hipSuccess) return e;
+  const uint32_t cus = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
+  const uint32_t most = cus * 16u / KW;
+  kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(d, H, h, head, m.resid, m.y);
+  return hipGetLastError();
+}
+
+template <class F, int KW>
+hipError_t launch_one_up_r(const typename F::View &g, const typename F::View &u, const MoeArgs &m, MoeHead *head,
+                           uint16_t *h, uint32_t I, uint32_t lds, hipStream_t stream) {
+  return m.E <= 64u ? launch_one_up<F, KW, 1>(g, u, m, head, h, I, lds, stream)
+                    : m.E <= 128u ? launch_one_up<F, KW, 2>(g, u, m, head, h, I, lds, stream)
+                                  : launch_one_up<F, KW, 8>(g, u, m, head, h, I, lds, stream);
+}
+
+template <class F>
+hipError_t launch_one(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
+                      MoeHead *head, uint16_t *h, hipStream_t stream) {
+  const uint32_t I = g.N / m.E, H = d.N / m.E;
+  // two workgroups of 8 waves a CU where their LDS allows, else one of 16
+  const uint32_t lu = token_lds<F>(H), ld = m.topk * token_lds<F>(I), half = kLdsBytes / 2u - 1024u;
+  const hipError_t e = lu <= half ? launch_one_up_r<F, 8>(g, u, m, head, h, I, lu, stream)
+                                  : launch_one_up_r<F, 16>(g, u, m, head, h, I, lu, stream);
+  if (e != hipSuccess) return e;
+  const uint32_t pairs = (H + 1u) / 2u, waves = 16u * (uint32_t)device_cu_count();
+  if (ld > half) return launch_one_down<F, 16, 1>(d, m, head, h, H, ld, stream);
+  if (pairs * 4u <= waves) return launch_one_down<F, 8, 4>(d, m, head, h, H, ld, stream);
+  if (pairs * 2u <= waves) return launch_one_down<F, 8, 2>(d, m, head, h, H, ld, stream);
+  return launch_one_down<F, 8, 1>(d, m, head, h, H, ld, stream);
+}
+
 template <class F, int NX, bool ONE>
 hipError_t launch_pass(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
                        MoeHead *head, uint16_t *h, uint32_t T, uint32_t most, const uint16_t *x, const uint16_t *resid,
@@ -328,12 +585,13 @@ hipError_t launch_pass(const typename F::View &g, const typename F::View &u, con
   return hipGetLastError();
 }
 
-template <class F>
+template <class F, class One>
 hipError_t launch_layer(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
                         hipStream_t stream) {
   MoeHead *head = reinterpret_cast<MoeHead *>(m.ws);
   uint16_t *h = reinterpret_cast<uint16_t *>((uint8_t *)m.ws + kMoeHeadBytes);
   const size_t H = d.N / m.E;
+  if (m.tokens == 1u && one_token_fits<One>((uint32_t)H, g.N / m.E, m.topk)) return launch_one<One>(g, u, d, m, head, h, stream);
   for (uint32_t t0 = 0; t0 < m.tokens; t0 += kTok) {
     const uint32_t T = m.tokens - t0 < kTok ? m.tokens - t0 : kTok, slots = T * m.topk;
     const uint8_t *logits = (const uint8_t *)m.logits + (size_t)t0 * m.E * (m.logits_bf16 ? 2u : 4u);
@@ -359,11 +617,11 @@ hipError_t launch_layer(const typename F::View &g, const typename F::View &u, co
 
 hipError_t launch_moe_int8(const WeightView &g, const WeightView &u, const WeightView &d, const MoeArgs &m,
                            hipStream_t stream) {
-  return g.gs == 32u ? launch_layer<Int8Fmt<true>>(g, u, d, m, stream) : launch_layer<Int8Fmt<false>>(g, u, d, m, stream);
+  return g.gs == 32u ? launch_layer<Int8Fmt<true>, Int8Tok>(g, u, d, m, stream) : launch_layer<Int8Fmt<false>, Int8Tok>(g, u, d, m, stream);
 }
 
 hipError_t launch_moe_mx(const MxView &g, const MxView &u, const MxView &d, const MoeArgs &m, hipStream_t stream) {
-  return launch_layer<MxFmt>(g, u, d, m, stream);
+  return launch_layer<MxFmt, MxTok>(g, u, d, m, stream);
 }
 
 }  // namespace int8w

@@ -13,11 +13,120 @@
 #include <type_traits>
 
 #include "rows_stream.h"
+#include "token_stream.h"
 #include "launch.h"
 
 namespace int8w {
 
 namespace {
+
+// ---- one row ----------------------------------------------------------------------------------
+
+// Waves share the pairs of weight rows; KS neighbouring waves share a pair's segments
+// where there are few pairs.  LDS: x.
+template <int KW, int U, int KS>
+__global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *__restrict__ x, uint16_t *__restrict__ y) {
+  typedef MxTok F;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_gemv[];
+  __shared__ float red[KW][2];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = w.K, segs = token_segs<F>(K);
+  const uint32_t units = gridDim.x * (KW / KS), unit = blockIdx.x * (KW / KS) + wave / KS, ks = wave % KS;
+  const uint32_t pairs = (w.N + 1u) / 2u;
+  const uint32_t p0 = (uint32_t)((uint64_t)pairs * unit / units), p1 = (uint32_t)((uint64_t)pairs * (unit + 1u) / units);
+  const uint32_t s0 = segs * ks / KS, s1 = segs * (ks + 1u) / KS;  // the wave's segments of a pair
+  uint32_t lp = p0, ls = s0;                                       // the next load
+  F::Row ra, rb;
+  auto rows = [&]() {
+    const bool a = lp < p1, b = a && 2u * lp + 1u < w.N;
+    ra = F::row(w, a ? 2u * lp : 0u, a);
+    rb = F::row(w, b ? 2u * lp + 1u : 0u, b);
+  };
+  rows();
+  TokenPair<F> ring[U];
+  auto load = [&](TokenPair<F> &t) {
+    F::load(t.a, ra, w, ls, lane);
+    F::load(t.b, rb, w, ls, lane);
+    token_order();
+    if (++ls >= s1) {
+      ls = s0;
+      ++lp;
+      rows();
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(ring[u]);
+  stage_token<F>(lds_gemv, x, K, threadIdx.x, 64u * KW);
+  __syncthreads();
+  float a = 0.f, b = 0.f;
+  uint32_t cp = p0, cs = s0;
+  auto store = [&](uint32_t p, float va, float vb) {
+    const uint32_t r = 2u * p + lane;
+    if (lane < 2u && r < w.N) y[r] = to_bf16_bits(lane ? vb : va);
+  };
+  for (uint32_t i = 0, items = (p1 - p0) * (s1 - s0); i < items; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < items) {
+        u32x4 xv[F::kX];
+        float xsum;
+        get_token<F>(xv, xsum, lds_gemv, segs, cs, lane);
+        a = F::dot(a, ring[u].a, xv, xsum);
+        b = F::dot(b, ring[u].b, xv, xsum);
+        if (++cs == s1) {
+          cs = s0;
+          if constexpr (KS == 1) {
+            store(cp, token_sum(a), token_sum(b));
+            a = b = 0.f;
+          }
+          ++cp;
+        }
+      }
+      token_order();
+      load(ring[u]);
+    }
+  }
+  if constexpr (KS > 1) {
+    a = token_sum(a);
+    b = token_sum(b);
+    if (lane == 0) {
+      red[wave][0] = a;
+      red[wave][1] = b;
+    }
+    __syncthreads();
+    if (ks == 0 && p0 < p1) {
+      a = b = 0.f;
+#pragma unroll
+      for (uint32_t k = 0; k < (uint32_t)KS; ++k) {
+        a += red[wave + k][0];
+        b += red[wave + k][1];
+      }
+      store(p0, a, b);
+    }
+  }
+}
+
+template <int KW, int KS>
+hipError_t launch_gemv_one(const MxView &w, const uint16_t *x, uint16_t *y, hipStream_t stream) {
+  auto kern = k_mx_gemv<KW, 4, KS>;
+  const uint32_t lds = token_lds<MxTok>(w.K);
+  if (lds > 64u << 10) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  const uint32_t units = KW / KS, want = ((w.N + 1u) / 2u + units - 1u) / units;
+  const uint32_t most = (uint32_t)device_cu_count() * 16u / KW;
+  kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(w, x, y);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemv(const MxView &w, const uint16_t *x, uint16_t *y, hipStream_t stream) {
+  // two workgroups of 8 waves a CU where their LDS allows, else one of 16
+  if (token_lds<MxTok>(w.K) > (79u << 10)) return launch_gemv_one<16, 1>(w, x, y, stream);
+  const uint32_t pairs = (w.N + 1u) / 2u, waves = 16u * (uint32_t)device_cu_count(), segs = token_segs<MxTok>(w.K);
+  if (pairs * 4u <= waves && segs >= 4u) return launch_gemv_one<8, 4>(w, x, y, stream);
+  if (pairs * 2u <= waves && segs >= 2u) return launch_gemv_one<8, 2>(w, x, y, stream);
+  return launch_gemv_one<8, 1>(w, x, y, stream);
+}
 
 // ---- few rows ---------------------------------------------------------------------------------
 
@@ -450,6 +559,7 @@ hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxView &w, const uint16_t *x, uint16_t *y, uint32_t m, hipStream_t stream) {
+  if (m == 1u && token_lds<MxTok>(w.K) <= (159u << 10)) return launch_gemv(w, x, y, stream);
   return launch_any<false>(w, x, nullptr, m, y, stream);
 }
 
