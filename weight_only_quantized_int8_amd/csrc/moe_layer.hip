@@ -49,65 +49,84 @@ struct MoeHead {
 };
 static_assert(sizeof(MoeHead) <= kMoeHeadBytes, "workspace head");
 
+// Maximum over the wave, in every lane, by data-parallel moves (a shuffle through LDS costs
+// over a hundred cycles, and top-k takes six a choice).
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-  return v;
+#define INT8W_DPP_MAX(ctrl, rows)                                                                                  \
+  v = fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(v), (int)__float_as_uint(v), \
+                                                                      ctrl, rows, 0xF, false)))
+  INT8W_DPP_MAX(0x111, 0xF);  // row_shr:1
+  INT8W_DPP_MAX(0x112, 0xF);
+  INT8W_DPP_MAX(0x114, 0xF);
+  INT8W_DPP_MAX(0x118, 0xF);
+  INT8W_DPP_MAX(0x142, 0xA);  // row_bcast:15
+  INT8W_DPP_MAX(0x143, 0xC);  // row_bcast:31
+#undef INT8W_DPP_MAX
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-// One wave routes one token: lane j < topk gets choice j's expert (0xFFFF: none) and
-// weight.  Returns whether the logits hold a NaN or +inf (then nothing is chosen).
+// One wave routes one token.  Lane l holds the logits of experts l, l + 64, ...
 template <int R>  // ceil(E / 64) at most
-__device__ __forceinline__ bool route_token(const void *logits, bool bf16, uint32_t t, uint32_t E, uint32_t topk,
-                                            bool renorm, float scale, uint32_t lane, uint32_t &id, float &w) {
-  const float ninf = -__builtin_inff();
-  float v[R], top = ninf;
-  bool odd = false;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint32_t e = 64u * r + lane;
-    v[r] = ninf;
-    if (e < E) {
-      v[r] = bf16 ? bf16_bits_to_f32(((const uint16_t *)logits)[(size_t)t * E + e]) : ((const float *)logits)[(size_t)t * E + e];
-      odd |= !(v[r] < __builtin_inff());
-    }
-    top = fmaxf(top, v[r]);
-  }
-  id = 0xFFFFu;
-  w = 0.f;
-  if (__ballot(odd) != 0ull) return true;
-  top = wave_max(top);
-  if (!(top > ninf)) return false;  // every expert masked out
-  float total = 0.f, p = 0.f, best = top;
-  if (!renorm) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) total += v[r] > ninf ? expf(v[r] - top) : 0.f;
-    total = wave_sum(total);
-  }
-  for (uint32_t j = 0; j < topk && best > ninf; ++j) {  // the largest left, the lowest index among equals
-    uint32_t at = kMaxE;
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      const unsigned long long is = __ballot(v[r] == best);
-      if (is) at = 64u * r + (uint32_t)__builtin_ctzll(is);
-    }
-    float left = ninf;
+struct RouteToken {
+  float v[R];
+  uint32_t id;  // lane j < topk: choice j's expert (0xFFFF: none)
+  float w;      // ... and weight
+  __device__ __forceinline__ void load(const void *logits, bool bf16, uint32_t t, uint32_t E, uint32_t lane) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (64u * r + lane == at) v[r] = ninf;
-      left = fmaxf(left, v[r]);
+      const uint32_t e = 64u * r + lane;
+      v[r] = -__builtin_inff();
+      if (e < E)
+        v[r] = bf16 ? bf16_bits_to_f32(((const uint16_t *)logits)[(size_t)t * E + e]) : ((const float *)logits)[(size_t)t * E + e];
     }
-    if (lane == j) {
-      id = at;
-      p = expf(best - top);
-    }
-    if (j + 1u < topk) best = wave_max(left);
   }
-  if (renorm) total = wave_sum(p);
-  w = p > 0.f ? p / total * scale : 0.f;
-  if (w == 0.f) id = 0xFFFFu;  // underflow, or a scale of 0: the expert adds nothing and is not run
-  return false;
-}
+  // Returns whether the logits hold a NaN or +inf (then nothing is chosen).
+  __device__ __forceinline__ bool choose(uint32_t topk, bool renorm, float scale, uint32_t lane) {
+    const float ninf = -__builtin_inff();
+    float top = ninf;
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      odd |= !(v[r] < __builtin_inff());
+      top = fmaxf(top, v[r]);
+    }
+    id = 0xFFFFu;
+    w = 0.f;
+    if (__ballot(odd) != 0ull) return true;
+    top = wave_max(top);
+    if (!(top > ninf)) return false;  // every expert masked out
+    float total = 0.f, p = 0.f, best = top;
+    if (!renorm) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) total += v[r] > ninf ? expf(v[r] - top) : 0.f;
+      total = token_sum(total);
+    }
+    for (uint32_t j = 0; j < topk && best > ninf; ++j) {  // the largest left, the lowest index among equals
+      uint32_t at = kMaxE;
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) {
+        const unsigned long long is = __ballot(v[r] == best);
+        if (is) at = 64u * r + (uint32_t)__builtin_ctzll(is);
+      }
+      float left = ninf;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (64u * r + lane == at) v[r] = ninf;
+        left = fmaxf(left, v[r]);
+      }
+      if (lane == j) {
+        id = at;
+        p = best;
+      }
+      if (j + 1u < topk) best = wave_max(left);
+    }
+    p = id < kMaxE ? expf(p - top) : 0.f;
+    if (renorm) total = token_sum(p);
+    w = p > 0.f ? p / total * scale : 0.f;
+    if (w == 0.f) id = 0xFFFFu;  // underflow, or a scale of 0: the expert adds nothing and is not run
+    return false;
+  }
+};
 
 // 16 waves; wave w routes tokens w, w + 16, ...; segments of up to C tokens.
 template <int R>
@@ -122,13 +141,13 @@ __global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ log
   if (tid < 64u * R) takers[tid] = 0ull;
   __syncthreads();
   for (uint32_t t = wave; t < T; t += 16u) {
-    uint32_t id;
-    float w;
-    const bool is_nan = route_token<R>(logits, bf16, t, E, topk, renorm, scale, lane, id, w);
+    RouteToken<R> route;
+    route.load(logits, bf16, t, E, lane);
+    const bool is_nan = route.choose(topk, renorm, scale, lane);
     if (lane < topk) {
-      ids[t * topk + lane] = (uint16_t)id;
-      head->weight[t * topk + lane] = w;
-      if (id < kMaxE) atomicOr(&takers[id], 1ull << t);  // order-free
+      ids[t * topk + lane] = (uint16_t)route.id;
+      head->weight[t * topk + lane] = route.w;
+      if (route.id < kMaxE) atomicOr(&takers[route.id], 1ull << t);  // order-free
     }
     if (lane == 0) head->nan[t] = is_nan ? 1u : 0u;
   }
@@ -326,9 +345,13 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typena
                                                      MoeHead *__restrict__ head, uint16_t *__restrict__ h) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wg.K, segs = token_segs<F>(K);
-  uint32_t id;
-  float w;
-  const bool is_nan = route_token<R>(logits, bf16, 0, E, topk, renorm, scale, lane, id, w);
+  RouteToken<R> route;
+  route.load(logits, bf16, 0, E, lane);
+  TokenStage<F> stage(x, K, 1u, threadIdx.x, 64u * KW);
+  stage.load();
+  const bool is_nan = route.choose(topk, renorm, scale, lane);
+  const uint32_t id = route.id;
+  const float w = route.w;
   const uint32_t n = (uint32_t)__popcll(__ballot(id < kMaxE));  // choices 0 .. n-1: their weights fall
   if (blockIdx.x == 0 && wave == 0) {
     if (lane < topk) {
@@ -371,7 +394,7 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typena
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(ring[u]);
-  stage_token<F>(lds, x, K, threadIdx.x, 64u * KW);
+  stage.finish(lds);
   __syncthreads();
   uint32_t cp = p0, cs = 0;
   float g = 0.f, up = 0.f;
@@ -404,12 +427,15 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typena
 // segments where there are few pairs.  LDS: h of the chosen experts.
 template <class F, int KW, int U, int KS>
 __global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint32_t H, const uint16_t *__restrict__ h,
-                                                       const MoeHead *__restrict__ head,
+                                                       uint32_t topk, const MoeHead *__restrict__ head,
                                                        const uint16_t *__restrict__ resid, uint16_t *__restrict__ y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ float red[KW][2];
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wd.K, segs = token_segs<F>(K);
+  // the rows of h past the last chosen expert's hold nothing, and are not used
+  TokenStage<F> stage(h, K, topk, threadIdx.x, 64u * KW);
   const uint32_t n = uniform32(head->segments), ids = head->seg[lane < kMaxTopk ? lane : 0u].expert;
+  stage.load();
   const uint32_t units = gridDim.x * (KW / KS), unit = blockIdx.x * (KW / KS) + wave / KS, ks = wave % KS;
   const uint32_t pairs = (H + 1u) / 2u;
   const uint32_t p0 = (uint32_t)((uint64_t)pairs * unit / units), p1 = (uint32_t)((uint64_t)pairs * (unit + 1u) / units);
@@ -445,7 +471,7 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint
 #pragma unroll
   for (int u = 0; u < U; ++u) load(ring[u]);
   const uint32_t stride = token_lds<F>(K);
-  for (uint32_t j = 0; j < n; ++j) stage_token<F>(lds + j * stride, h + (size_t)j * K, K, threadIdx.x, 64u * KW);
+  stage.finish(lds);
   __syncthreads();
   float a = 0.f, b = 0.f;
   uint32_t cp = p0, cq = q0, cj = j0, cs = s0;
@@ -542,7 +568,7 @@ hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead 
   if (e != hipSuccess) return e;
   const uint32_t cus = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
   const uint32_t most = cus * 16u / KW;
-  kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(d, H, h, head, m.resid, m.y);
+  kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(d, H, h, m.topk, head, m.resid, m.y);
   return hipGetLastError();
 }
 

@@ -35,6 +35,8 @@ __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *_
   const uint32_t p0 = (uint32_t)((uint64_t)pairs * unit / units), p1 = (uint32_t)((uint64_t)pairs * (unit + 1u) / units);
   const uint32_t s0 = segs * ks / KS, s1 = segs * (ks + 1u) / KS;  // the wave's segments of a pair
   uint32_t lp = p0, ls = s0;                                       // the next load
+  TokenStage<F> stage(x, K, 1u, threadIdx.x, 64u * KW);
+  stage.load();
   F::Row ra, rb;
   auto rows = [&]() {
     const bool a = lp < p1, b = a && 2u * lp + 1u < w.N;
@@ -55,7 +57,7 @@ __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *_
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(ring[u]);
-  stage_token<F>(lds_gemv, x, K, threadIdx.x, 64u * KW);
+  stage.finish(lds_gemv);
   __syncthreads();
   float a = 0.f, b = 0.f;
   uint32_t cp = p0, cs = s0;

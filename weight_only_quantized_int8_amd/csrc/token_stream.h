@@ -35,6 +35,9 @@ __device__ __forceinline__ float token_sum(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
+// As keep_order() of rows_stream.h.
+__device__ __forceinline__ void token_order() { __builtin_amdgcn_sched_barrier(0); }
+
 struct MxTok {
   typedef MxView View;
   static constexpr uint32_t kSeg = 2048;  // k of a load
@@ -119,22 +122,58 @@ __host__ __device__ constexpr uint32_t token_lds(uint32_t K) {
   return token_segs<F>(K) * (1024u * F::kX + (F::kSums ? 256u : 0u));
 }
 
-// Staged by `threads` threads (a multiple of 64); zeros past K.
+// n rows of K values, back to back, staged one token_lds() after the other by `threads`
+// threads (a multiple of 64); zeros past K.  Four pieces a thread are in flight: with one,
+// each was a memory latency of its own.  The first four are loaded by load() and written by
+// finish(), with the weight's first loads in between: loads return in order, so the staging
+// then waits for the activations alone.
 template <class F>
-__device__ __forceinline__ void stage_token(uint8_t *lds, const uint16_t *x, uint32_t K, uint32_t tid, uint32_t threads) {
-  const uint32_t blocks = token_segs<F>(K) * 64u, plane = 16u * blocks;
-  for (uint32_t p = tid; p < blocks * F::kX; p += threads) {
-    const u32x4 v = 8u * p < K ? *reinterpret_cast<const u32x4 *>(x + 8u * p) : u32x4{0u, 0u, 0u, 0u};
-    *reinterpret_cast<u32x4 *>(lds + (p % F::kX) * plane + 16u * (p / F::kX)) = v;
-    if constexpr (F::kSums) {  // two neighbouring lanes hold a run of 16
-      float s = 0.f;
+struct TokenStage {
+  u32x4 v[4];
+  const uint16_t *x;
+  uint32_t K, n, row, plane, stride, tid, threads;
+  __device__ __forceinline__ TokenStage(const uint16_t *x_, uint32_t K_, uint32_t n_, uint32_t tid_, uint32_t threads_)
+      : x(x_), K(K_), n(n_), tid(tid_), threads(threads_) {
+    const uint32_t blocks = token_segs<F>(K) * 64u;
+    plane = 16u * blocks;
+    row = blocks * F::kX;
+    stride = token_lds<F>(K);
+  }
+  __device__ __forceinline__ void load(uint32_t p0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s += bf16_lo(v[i]) + bf16_hi(v[i]);
-      s += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(s), 0xB1, 0xF, 0xF, true));
-      if ((p & 1u) == 0) *reinterpret_cast<float *>(lds + F::kX * plane + 4u * (p >> 1)) = s;
+    for (uint32_t i = 0; i < 4u; ++i) {
+      const uint32_t p = p0 + i * threads, r = p / row, c = p - r * row;
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (r < n && 8u * c < K) v[i] = *reinterpret_cast<const u32x4 *>(x + (size_t)r * K + 8u * c);
+    }
+    token_order();
+  }
+  __device__ __forceinline__ void load() { load(tid); }
+  __device__ __forceinline__ void write(uint8_t *lds, uint32_t p0) const {
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; ++i) {
+      const uint32_t p = p0 + i * threads, r = p / row, c = p - r * row;
+      if (r < n) {  // whole waves: a row is a multiple of 64 pieces
+        uint8_t *at = lds + r * stride;
+        *reinterpret_cast<u32x4 *>(at + (c % F::kX) * plane + 16u * (c / F::kX)) = v[i];
+        if constexpr (F::kSums) {  // two neighbouring lanes hold a run of 16
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s += bf16_lo(v[i][k]) + bf16_hi(v[i][k]);
+          s += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(s), 0xB1, 0xF, 0xF, true));
+          if ((c & 1u) == 0) *reinterpret_cast<float *>(at + F::kX * plane + 4u * (c >> 1)) = s;
+        }
+      }
     }
   }
-}
+  __device__ __forceinline__ void finish(uint8_t *lds) {
+    write(lds, tid);
+    for (uint32_t p0 = tid + 4u * threads; p0 < n * row; p0 += 4u * threads) {
+      load(p0);
+      write(lds, p0);
+    }
+  }
+};
 
 template <class F>
 __device__ __forceinline__ void get_token(u32x4 (&x)[F::kX], float &sum, const uint8_t *lds, uint32_t segs, uint32_t seg,
@@ -149,8 +188,5 @@ template <class F>
 struct TokenPair {
   typename F::Frag a, b;
 };
-
-// As keep_order() of rows_stream.h.
-__device__ __forceinline__ void token_order() { __builtin_amdgcn_sched_barrier(0); }
 
 }  // namespace int8w
