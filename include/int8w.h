@@ -249,7 +249,7 @@ int int8w_mxfp4_gemm_mx(const int8w_mxfp4 *w, const int8w_mxfp4 *x, uint16_t *y,
  * else is fp32 until the one rounding of y.  Any number of tokens: they go in passes
  * of 64, each of which streams the weights of the experts that its tokens take.
  * workspace: device scratch, 256-byte aligned, of at least
- * int8w_moe_workspace_bytes(tokens, topk, inner) bytes; no initial value, none kept;
+ * int8w_moe_workspace_bytes(tokens, topk, inner, hidden) bytes; no initial value, none kept;
  * calls that share it must not overlap.  tokens = 0 is a no-op.
  * Errors: INT8W_ERR_NULL; INT8W_ERR_SHAPE (shapes that do not fit each other or
  * num_experts, num_experts above INT8W_MAX_MOE_EXPERTS, topk outside
@@ -271,7 +271,7 @@ typedef struct {
   float routed_scale;
 } int8w_moe_call;
 
-uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inner);
+uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inner, uint32_t hidden);
 int int8_moe_layer(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down, uint32_t num_experts,
                    const int8w_moe_call *call, void *workspace, uint64_t workspace_bytes, uint64_t stream);
 int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down,

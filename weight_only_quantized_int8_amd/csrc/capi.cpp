@@ -534,7 +534,7 @@ int check_moe(uint64_t gate_rows, uint32_t hidden, uint64_t up_rows, uint32_t up
   if (!aligned(c->logits, el)) return fail(INT8W_ERR_ALIGN, "logits is not %u-byte aligned", el);
   if (!aligned(c->y, 2) || !aligned(c->x_resid, 2)) return fail(INT8W_ERR_ALIGN, "y/x_resid are not 2-byte aligned");
   if (!aligned(ws, 256)) return fail(INT8W_ERR_ALIGN, "workspace is not 256-byte aligned");
-  const uint64_t need = int8w_moe_workspace_bytes(c->tokens, c->topk, inner);
+  const uint64_t need = int8w_moe_workspace_bytes(c->tokens, c->topk, inner, hidden);
   if (ws_bytes < need)
     return fail(INT8W_ERR_SHAPE, "workspace of %llu bytes, this call needs %llu", (unsigned long long)ws_bytes,
                 (unsigned long long)need);
@@ -637,10 +637,10 @@ int int8w_mxfp4_gemm_mx(const int8w_mxfp4 *w, const int8w_mxfp4 *x, uint16_t *y,
   return finish_launch(launch_mx_gemm_mx(view(w), view(x), y, as_stream(stream)), as_stream(stream));
 }
 
-uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inner) {
+uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inner, uint32_t hidden) {
   if (tokens == 0) return 0;
   const uint64_t slots = (uint64_t)(tokens < kMoePassTokens ? tokens : kMoePassTokens) * topk;
-  return kMoeHeadBytes + slots * inner * 2u;
+  return kMoeHeadBytes + slots * inner * 2u + slots * hidden * 4u;
 }
 
 int int8_moe_layer(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down, uint32_t num_experts,

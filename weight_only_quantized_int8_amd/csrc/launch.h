@@ -121,7 +121,7 @@ struct MoeArgs {
   float scale;
   const uint16_t *resid;  // [tokens, H] or nullptr
   uint16_t *y;            // [tokens, H]
-  void *ws;               // head, then h [min(tokens, kMoePassTokens) topk, I] BF16
+  void *ws;               // head, then for min(tokens, kMoePassTokens) topk slots h [I] BF16, shares [H] f32
 };
 hipError_t launch_moe_int8(const WeightView &gate, const WeightView &up, const WeightView &down, const MoeArgs &m,
                            hipStream_t stream);

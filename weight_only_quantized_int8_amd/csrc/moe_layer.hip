@@ -5,18 +5,19 @@
 //   r_j = p_j / sum of the chosen p (renormalized) or p_j, times routed_scale;
 //   y[t] = x_resid[t] + sum_j r_j  Wd_j ( silu(Wg_j x_t) * (Wu_j x_t) ).
 //
-// Three launches on one stream, up to 64 tokens a pass:
+// One token: two launches (k_moe1_up, k_moe1_down, token_stream.h).  More: four launches on
+// one stream, up to 64 tokens a pass:
 //  k_moe_route   one workgroup: each wave takes tokens.  Its result is a list of
-//                segments: an expert and up to C of the slots (t, j) that take it.
-//  k_moe_up      workgroup (segment, 16 inner rows): gate and up rows are streamed
-//                once for all the segment's tokens (rows_stream.h); the epilogue
-//                writes h[slot] = r * silu(g) * u.
-//  k_moe_down    workgroup (16 output rows): the segments' down rows one after the
-//                other, the waves sharing the list evenly; a wave adds a segment's
-//                products to its own fp32 sums by token, so the weighted sum over
-//                experts needs no atomics and no further pass.
-// Bound: HBM, each chosen expert's three matrices once.  An expert with more than C
-// tokens has several segments, whose further reads of its rows come from the caches.
+//                segments: an expert and up to 16 of the slots (t, j) that take it.
+//  k_moe_up      workgroup (segment, rows): gate and up rows are streamed once for all
+//                the segment's tokens (rows_stream.h); the epilogue writes
+//                h[slot] = r * silu(g) * u.
+//  k_moe_down    workgroup (segment, rows): the slot's share of its token's sum, fp32.
+//  k_moe_sum     the shares of a token in the order of its choices, and the residual:
+//                no atomics, so the same bits each time.
+// Bound: HBM, each chosen expert's three matrices once.  An expert with more than
+// 16 tokens has several segments, whose further reads of its rows come from the caches
+// where they run together.
 //
 // h is kept in BF16 (the matrix cores' operand type): its relative rounding of at
 // most 2^-9 a value averages out over the inner sum to about the output's own BF16
@@ -184,153 +185,73 @@ __global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ log
   }
 }
 
-// Sum of the waves' accumulators, in wave order: red[wave][tile][lane] f32x4.
-template <int KS>
-__device__ __forceinline__ float red_sum(const float *red, uint32_t tiles, uint32_t tile, uint32_t row, uint32_t tok) {
-  const uint32_t at = (tile * 64u + (tok >> 2) * 16u + row) * 4u + (tok & 3u);
-  float v = 0.f;
-#pragma unroll
-  for (int w = 0; w < KS; ++w) v += red[(uint32_t)w * tiles * 256u + at];
-  return v;
-}
-
-// grid (16-row tiles of I, segments at most).  NX: loads that a quarter's activations take.
-template <class F, int KS, int U, int NX, int AUX>
-__global__ __launch_bounds__(64 * KS) void k_moe_up(typename F::View wg, typename F::View wu, uint32_t I,
+// grid (row blocks of I) x (segments at most): a wave has 16 gate and the same 16 up rows.
+template <class F, int KW, int AUX>
+__global__ __launch_bounds__(64 * KW, 4) void k_moe_up(typename F::View wg, typename F::View wu, uint32_t I, uint32_t blocks,
                                                     const uint16_t *__restrict__ x, uint32_t T, uint32_t topk,
                                                     const MoeHead *__restrict__ head, uint16_t *__restrict__ h) {
-  typedef XBf16<F, NX> X;
-  constexpr uint32_t kWaveLds = stream_lds<X, 2>();
-  static_assert(KS * kWaveLds >= KS * 2048u, "the partial sums reuse the stream's LDS");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[KS * kWaveLds];
-  const MoeSegment *seg = &head->seg[blockIdx.y];
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wg.K, i0 = 16u * blockIdx.x;
+  typedef BlockStream<F, KW, 2> S;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
+  const MoeSegment *seg = &head->seg[blockIdx.x / blocks];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wg.K;
   const uint32_t n = uniform32(seg->n), e = uniform32(seg->expert);  // meaningless, and unused, past the last segment
-  if (blockIdx.y >= uniform32(head->segments)) return;
-  const typename F::Tile tg = F::tile(wg, (uint64_t)e * I, i0, I, lane), tu = F::tile(wu, (uint64_t)e * I, i0, I, lane);
-  const X xs(x, T * K * 2u, K, lane, [&](uint32_t i) { return i < n ? seg->slot[i] / topk * (K * 2u) : kOutOfRange; });
-  const uint32_t np = (K + F::kPiece - 1u) / F::kPiece;
-  Pieces<F, X, 2> r[U];
-  auto load = [&](Pieces<F, X, 2> &b, uint32_t c) {
-    xs.load(b.x, c, lane);
-    F::template load<AUX>(b.w[0], tg, wg, c, lane);
-    F::template load<AUX>(b.w[1], tu, wu, c, lane);
-    keep_order();
-  };
-  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  if (blockIdx.x / blocks >= uniform32(head->segments)) return;
+  const uint32_t i0 = 16u * (blockIdx.x % blocks * KW + wave);
+  S s(lds, x, T * K * 2u, K, lane, wave, [&](uint32_t i) { return i < n ? seg->slot[i] / topk * (K * 2u) : kOutOfRange; });
+  s.t[0] = F::tile(wg, (uint64_t)e * I, i0 < I ? i0 : I - 1u, I, lane);  // a wave past the last row repeats it
+  s.t[1] = F::tile(wu, (uint64_t)e * I, i0 < I ? i0 : I - 1u, I, lane);
+  const typename F::View *const v[2] = {&wg, &wu};
+  s.template run<AUX>(v, blockIdx.x);
+  // D[4 g + i][row]: token i of the segment, inner row
+  const uint32_t row = i0 + (lane & 15u);
+  if (row >= I) return;
 #pragma unroll
-  for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
-  for (uint32_t c = wave; c < np; c += KS * U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      stream_piece<F, X, 2>(acc, r[u], xs, lds + wave * kWaveLds, lane);
-      keep_order();
-      load(r[u], c + KS * (U + u));  // past the row's end: zeros, no traffic
-    }
-  }
-  __syncthreads();
-  float *red = reinterpret_cast<float *>(lds);
-  reinterpret_cast<f32x4 *>(red)[(wave * 2u) * 64u + lane] = acc[0];
-  reinterpret_cast<f32x4 *>(red)[(wave * 2u + 1u) * 64u + lane] = acc[1];
-  __syncthreads();
-  for (uint32_t o = threadIdx.x; o < 16u * n; o += 64u * KS) {
-    const uint32_t row = o & 15u, tok = o >> 4;
-    if (i0 + row < I) {
-      const float g = red_sum<KS>(red, 2u, 0, row, tok), u = red_sum<KS>(red, 2u, 1, row, tok);
-      const uint32_t p = seg->slot[tok];
-      h[(size_t)p * I + i0 + row] = to_bf16_bits(head->weight[p] * silu_mul(g, u));
+  for (uint32_t i = 0; i < 4u; ++i) {
+    const uint32_t k = 4u * (lane >> 4) + i;
+    if (k < n) {
+      const uint32_t p = seg->slot[k];
+      h[(size_t)p * I + row] = to_bf16_bits(head->weight[p] * silu_mul(s.acc[0][i], s.acc[1][i]));
     }
   }
 }
 
-// grid: 16-row tiles of H.  Dynamic LDS: the streams', then the waves' sums
-// [KS][tokens][16], then the segments.  ONE: a single token, whose sums stay in registers.
-template <class F, int KS, int U, int NX, bool ONE, int AUX>
-__global__ __launch_bounds__(64 * KS) void k_moe_down(typename F::View wd, uint32_t H, const uint16_t *__restrict__ h,
-                                                      uint32_t T, uint32_t topk, const MoeHead *__restrict__ head,
-                                                      const uint16_t *__restrict__ resid, uint16_t *__restrict__ y) {
-  typedef XBf16<F, NX> X;
-  constexpr uint32_t kWaveLds = stream_lds<X, 1>();
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  float *sums = reinterpret_cast<float *>(lds + KS * kWaveLds);  // [KS][T][16]
-  MoeSegment *segs = reinterpret_cast<MoeSegment *>(sums + KS * T * 16u);
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), n0 = 16u * blockIdx.x, K = wd.K;
-  const uint32_t count = uniform32(head->segments);
-  for (uint32_t i = threadIdx.x; i < count * (sizeof(MoeSegment) / 4u); i += 64u * KS)
-    reinterpret_cast<uint32_t *>(segs)[i] = reinterpret_cast<const uint32_t *>(head->seg)[i];
-  for (uint32_t i = threadIdx.x; i < KS * T * 16u; i += 64u * KS) sums[i] = 0.f;
-  __syncthreads();
-  const uint32_t np = (K + F::kPiece - 1u) / F::kPiece, items = count * np;
-  // this wave's items: neighbouring pieces of one segment after the other
-  const uint32_t i0 = (uint32_t)((uint64_t)items * wave / KS), i1 = (uint32_t)((uint64_t)items * (wave + 1u) / KS);
-  uint32_t ls = 0, lp = 0;  // segment and piece of the next load
-  typename F::Tile tile = {};
-  X xs(h, T * topk * K * 2u, K, lane, [&](uint32_t) { return kOutOfRange; });
-  auto segment = [&](uint32_t s) {
-    const MoeSegment &g = segs[s];
-    tile = F::tile(wd, (uint64_t)uniform32(g.expert) * H, n0, H, lane);
-    const uint32_t n = g.n;
-    xs = X(h, T * topk * K * 2u, K, lane, [&](uint32_t i) { return i < n ? g.slot[i] * (K * 2u) : kOutOfRange; });
-  };
-  if (i0 < i1) {
-    ls = i0 / np;
-    lp = i0 - ls * np;
-    segment(ls);
+// grid (row blocks of H) x (segments at most); out [slots, H]: the slot's share of its token's sum.
+template <class F, int KW, int AUX>
+__global__ __launch_bounds__(64 * KW, 4) void k_moe_down(typename F::View wd, uint32_t H, uint32_t blocks,
+                                                      const uint16_t *__restrict__ h, uint32_t slots,
+                                                      const MoeHead *__restrict__ head, float *__restrict__ out) {
+  typedef BlockStream<F, KW, 1> S;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
+  const MoeSegment *seg = &head->seg[blockIdx.x / blocks];
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wd.K;
+  const uint32_t n = uniform32(seg->n), e = uniform32(seg->expert);
+  if (blockIdx.x / blocks >= uniform32(head->segments)) return;
+  const uint32_t n0 = 16u * (blockIdx.x % blocks * KW + wave);
+  S s(lds, h, slots * K * 2u, K, lane, wave, [&](uint32_t i) { return i < n ? seg->slot[i] * (K * 2u) : kOutOfRange; });
+  s.t[0] = F::tile(wd, (uint64_t)e * H, n0 < H ? n0 : H - 1u, H, lane);
+  const typename F::View *const v[1] = {&wd};
+  s.template run<AUX>(v, blockIdx.x);
+  const uint32_t row = n0 + (lane & 15u);
+  if (row >= H) return;
+#pragma unroll
+  for (uint32_t i = 0; i < 4u; ++i) {
+    const uint32_t k = 4u * (lane >> 4) + i;
+    if (k < n) out[(size_t)seg->slot[k] * H + row] = s.acc[0][i];
   }
-  uint32_t cs = ls, cp = lp;  // ... of the next products
-  Pieces<F, X, 1> r[U];
-  uint32_t next = i0;
-  auto load = [&](Pieces<F, X, 1> &b) {
-    if (lp == np) {
-      lp = 0;
-      if (++ls < count) segment(ls);
-    }
-    const uint32_t p = next < i1 ? lp : np;  // piece np: past the row's end, zeros
-    xs.load(b.x, p, lane);
-    F::template load<AUX>(b.w[0], tile, wd, p, lane);
-    ++lp;
-    ++next;
-    keep_order();
-  };
-  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-  auto flush = [&](uint32_t s) {  // D[4 g + i][row]: token i of the segment, output row
-    const uint32_t n = segs[s].n;
-#pragma unroll
-    for (uint32_t i = 0; i < 4u; ++i) {
-      const uint32_t k = 4u * (lane >> 4) + i;
-      if (k < n) sums[(wave * T + segs[s].slot[k] / topk) * 16u + (lane & 15u)] += acc[0][i];
-    }
-    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u) load(r[u]);
-  for (uint32_t i = i0; i < i1;) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      stream_piece<F, X, 1>(acc, r[u], xs, lds + wave * kWaveLds, lane);
-      keep_order();
-      load(r[u]);
-      ++i;
-      if (!ONE && i <= i1 && (++cp == np || i == i1)) {
-        flush(cs);
-        cp = 0;
-        ++cs;
-      }
-    }
-  }
-  if (ONE && lane < 16u) sums[wave * 16u + lane] = acc[0][0];
-  __syncthreads();
-  for (uint32_t o = threadIdx.x; o < 16u * T; o += 64u * KS) {
-    const uint32_t row = o & 15u, tok = o >> 4, n = n0 + row;
-    if (n < H) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < KS; ++w) v += sums[((uint32_t)w * T + tok) * 16u + row];
-      if (head->nan[tok]) v = __builtin_nanf("");
-      if (resid) v += bf16_bits_to_f32(resid[(size_t)tok * H + n]);
-      y[(size_t)tok * H + n] = to_bf16_bits(v);
-    }
-  }
+}
+
+// y[t] = x_resid[t] + the sum of the token's slots in order (a slot of weight 0 was not run).
+__global__ __launch_bounds__(256) void k_moe_sum(const float *__restrict__ out, uint32_t H, uint32_t topk,
+                                                 const MoeHead *__restrict__ head, const uint16_t *__restrict__ resid,
+                                                 uint16_t *__restrict__ y) {
+  const uint32_t t = blockIdx.y, n = blockIdx.x * 256u + threadIdx.x;
+  if (n >= H) return;
+  float v = 0.f;
+  for (uint32_t j = 0; j < topk; ++j)
+    if (head->weight[t * topk + j] != 0.f) v += out[(size_t)(t * topk + j) * H + n];
+  if (head->nan[t]) v = __builtin_nanf("");
+  if (resid) v += bf16_bits_to_f32(resid[(size_t)t * H + n]);
+  y[(size_t)t * H + n] = to_bf16_bits(v);
 }
 
 // ---- one token --------------------------------------------------------------------------------
@@ -596,44 +517,28 @@ hipError_t launch_one(const typename F::View &g, const typename F::View &u, cons
   return launch_one_down<F, 8, 1>(d, m, head, h, H, ld, stream);
 }
 
-template <class F, int NX, bool ONE>
-hipError_t launch_pass(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
-                       MoeHead *head, uint16_t *h, uint32_t T, uint32_t most, const uint16_t *x, const uint16_t *resid,
-                       uint16_t *y, hipStream_t stream) {
-  const uint32_t I = g.N / m.E, H = d.N / m.E;
-  constexpr int KU = 4, KD = NX == 1 ? 16 : 8, U = NX == 1 ? 2 : 1, AUX = ONE ? kAuxNontemporal : 0;
-  k_moe_up<F, KU, U, NX, AUX><<<dim3((I + 15u) / 16u, most), 64 * KU, 0, stream>>>(g, u, I, x, T, m.topk, head, h);
-  const uint32_t lds = KD * (stream_lds<XBf16<F, NX>, 1>() + T * 64u) + most * (uint32_t)sizeof(MoeSegment);
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_moe_down<F, KD, U, NX, ONE, AUX>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (e != hipSuccess) return e;
-  k_moe_down<F, KD, U, NX, ONE, AUX><<<(H + 15u) / 16u, 64 * KD, lds, stream>>>(d, H, h, T, m.topk, head, resid, y);
-  return hipGetLastError();
-}
-
 template <class F, class One>
 hipError_t launch_layer(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
                         hipStream_t stream) {
   MoeHead *head = reinterpret_cast<MoeHead *>(m.ws);
   uint16_t *h = reinterpret_cast<uint16_t *>((uint8_t *)m.ws + kMoeHeadBytes);
-  const size_t H = d.N / m.E;
-  if (m.tokens == 1u && one_token_fits<One>((uint32_t)H, g.N / m.E, m.topk)) return launch_one<One>(g, u, d, m, head, h, stream);
+  const uint32_t I = g.N / m.E, H = d.N / m.E;
+  if (m.tokens == 1u && one_token_fits<One>(H, I, m.topk)) return launch_one<One>(g, u, d, m, head, h, stream);
+  float *out = reinterpret_cast<float *>(h + (size_t)(m.tokens < kTok ? m.tokens : kTok) * m.topk * I);
+  constexpr int KW = 8;
   for (uint32_t t0 = 0; t0 < m.tokens; t0 += kTok) {
     const uint32_t T = m.tokens - t0 < kTok ? m.tokens - t0 : kTok, slots = T * m.topk;
     const uint8_t *logits = (const uint8_t *)m.logits + (size_t)t0 * m.E * (m.logits_bf16 ? 2u : 4u);
-    // tokens a segment: the rows of one activation load where experts have few tokens
-    constexpr uint32_t kOne = 64u / F::kXChunks;
-    const bool few = T <= kOne || slots <= m.E * (kOne / 2u);
-    const uint32_t C = few ? kOne : kSegTokens;
-    // segments at most: one an expert taken, one more for each C further tokens
-    const uint32_t taken = slots < m.E ? slots : m.E, most = taken + (slots - taken) / C;
+    // segments at most: one an expert taken, one more for each kSegTokens further tokens
+    const uint32_t taken = slots < m.E ? slots : m.E, most = taken + (slots - taken) / kSegTokens;
     auto route = m.E <= 64u ? k_moe_route<1> : m.E <= 128u ? k_moe_route<2> : m.E <= 256u ? k_moe_route<4> : k_moe_route<8>;
-    route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, T, m.E, m.topk, m.renorm, m.scale, C, head);
-    const uint16_t *x = m.x + t0 * H, *resid = m.resid ? m.resid + t0 * H : nullptr;
-    uint16_t *y = m.y + t0 * H;
-    const hipError_t e = T == 1u ? launch_pass<F, 1, true>(g, u, d, m, head, h, T, most, x, resid, y, stream)
-                         : few   ? launch_pass<F, 1, false>(g, u, d, m, head, h, T, most, x, resid, y, stream)
-                                 : launch_pass<F, kSegTokens / kOne, false>(g, u, d, m, head, h, T, most, x, resid, y, stream);
+    route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, T, m.E, m.topk, m.renorm, m.scale, kSegTokens, head);
+    const size_t at = (size_t)t0 * H;
+    const uint32_t ub = (I + 16u * KW - 1u) / (16u * KW), db = (H + 16u * KW - 1u) / (16u * KW);
+    k_moe_up<F, KW, kAuxNontemporal><<<ub * most, 64 * KW, 0, stream>>>(g, u, I, ub, m.x + at, T, m.topk, head, h);
+    k_moe_down<F, KW, kAuxNontemporal><<<db * most, 64 * KW, 0, stream>>>(d, H, db, h, slots, head, out);
+    k_moe_sum<<<dim3((H + 255u) / 256u, T), 256, 0, stream>>>(out, H, m.topk, head, m.resid ? m.resid + at : nullptr, m.y + at);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -141,9 +141,11 @@ struct MxFmt {
 };
 
 // ---- 8-bit affine -----------------------------------------------------------------------------
-__device__ __forceinline__ u32x4 int8_codes_bf16(uint32_t a, uint32_t b) {  // eight codes as BF16 integers (exact)
-  return u32x4{pack_bf16x2(code_f32(a, 0), code_f32(a, 1)), pack_bf16x2(code_f32(a, 2), code_f32(a, 3)),
-               pack_bf16x2(code_f32(b, 0), code_f32(b, 1)), pack_bf16x2(code_f32(b, 2), code_f32(b, 3))};
+__device__ __forceinline__ uint32_t int8_pair_bf16(uint32_t w, int i) {  // codes 2i, 2i + 1 as BF16 integers (exact)
+  return __builtin_amdgcn_perm(__float_as_uint(code_f32(w, 2 * i + 1)), __float_as_uint(code_f32(w, 2 * i)), 0x07060302u);
+}
+__device__ __forceinline__ u32x4 int8_codes_bf16(uint32_t a, uint32_t b) {
+  return u32x4{int8_pair_bf16(a, 0), int8_pair_bf16(a, 1), int8_pair_bf16(b, 0), int8_pair_bf16(b, 1)};
 }
 
 template <bool G32>
@@ -315,5 +317,124 @@ __device__ __forceinline__ void stream_piece(f32x4 (&acc)[RT], const Pieces<F, X
     wave_fence();
   }
 }
+
+// ---- a workgroup's stream ---------------------------------------------------------------------
+// KW waves, each with RT tiles of 16 weight rows of its own, walk K together.  The
+// activations of a piece are shared in LDS, two buffers, one barrier a piece; weights go as
+// above.  Two pieces of weights are in flight a wave: a piece's activations are requested
+// before its weights, so waiting for the former (loads return in order) leaves the latter in
+// flight for the whole of the piece before.
+template <class F, int KW, int RT>
+struct BlockStream {
+  static constexpr uint32_t kQuarterLds = 256u * F::kXChunks;             // 16 rows of a quarter's activations
+  static constexpr uint32_t kXLds = 4u * kQuarterLds;
+  static constexpr uint32_t kWaveLds = 2u * 1024u * RT;
+  static constexpr uint32_t kLds = 2u * kXLds + KW * kWaveLds;
+  static constexpr uint32_t kRowChunks = 4u * F::kXChunks;                // 16-byte chunks of a row in a piece
+  static constexpr int NX = (int)(16u * kRowChunks / (64u * KW));         // activation loads a wave
+  static_assert(16u * kRowChunks % (64u * KW) == 0, "whole loads");
+
+  typename F::Tile t[RT];
+  __amdgpu_buffer_rsrc_t rx;
+  uint32_t K, lane, wave, xo[NX], xk[NX], xl[NX];
+  uint8_t *lds;
+  f32x4 acc[RT];
+
+  // row(i): byte offset of activation row i (i < 16), or kOutOfRange
+  template <class Row>
+  __device__ __forceinline__ BlockStream(uint8_t *lds_, const void *x, uint32_t xbytes, uint32_t K_, uint32_t lane_,
+                                         uint32_t wave_, Row row)
+      : K(K_), lane(lane_), wave(wave_), lds(lds_) {
+    rx = make_rsrc(x, xbytes);
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+      const uint32_t c = (wave * NX + j) * 64u + lane, r = c / kRowChunks, k = c % kRowChunks;
+      xk[j] = 16u * k;
+      xo[j] = row(r) + 16u * k;
+      xl[j] = k / F::kXChunks * kQuarterLds + XBf16<F, 1>::at(r, k % F::kXChunks);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void load_x(u32x4 (&v)[NX], uint32_t piece) const {
+    const uint32_t b = piece * (2u * F::kPiece);
+#pragma unroll
+    for (int j = 0; j < NX; ++j) v[j] = buf_load_b128(rx, b + xk[j] < 2u * K ? xo[j] + b : kOutOfRange);
+    keep_order();
+  }
+  __device__ __forceinline__ void put_x(const u32x4 (&v)[NX], uint32_t buf) const {
+#pragma unroll
+    for (int j = 0; j < NX; ++j) *reinterpret_cast<u32x4 *>(lds + buf * kXLds + xl[j]) = v[j];
+  }
+  template <int AUX, class View>
+  __device__ __forceinline__ void load_w(typename F::Piece (&w)[RT], const View *const *v, uint32_t piece) const {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) F::template load<AUX>(w[i], t[i], *v[i], piece, lane);
+    keep_order();
+  }
+  __device__ __forceinline__ void products(const typename F::Piece (&w)[RT], uint32_t buf) {
+    uint8_t *const own = lds + 2u * kXLds + wave * kWaveLds;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint8_t *at = own + (h & 1) * (1024u * RT);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) put_quarter(at + 1024u * i, w[i].q[h], lane);
+      wave_fence();
+      u32x4 x[F::kXFrags];
+#pragma unroll
+      for (int f = 0; f < F::kXFrags; ++f)
+        x[f] = *reinterpret_cast<const u32x4 *>(lds + buf * kXLds + h * kQuarterLds + XBf16<F, 1>::at(lane & 15u, F::x_chunk(f, lane >> 4)));
+      typename F::Sums S;
+      F::sums(S, x);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) F::mac(acc[i], weight_operand<F>(at + 1024u * i, lane), w[i], h, x, S, lane);
+      wave_fence();
+    }
+  }
+  // acc += A B^T over all of K, from piece `first` on and round.  Workgroups that start
+  // at the same piece walk the rows' same 256 bytes together, a row length apart: with row
+  // lengths of whole kilobytes that is one memory channel in sixteen at a time.
+  template <int AUX, class View>
+  __device__ __forceinline__ void run(const View *const *v, uint32_t first) {
+    const uint32_t np = (K + F::kPiece - 1u) / F::kPiece;
+    uint32_t next = first % np, left = np;  // the next piece to load
+    auto take = [&]() {
+      const uint32_t c = left ? next : np;  // past the end: zeros, no traffic
+      left -= left ? 1u : 0u;
+      next = next + 1u == np ? 0u : next + 1u;
+      return c;
+    };
+    uint32_t p = take();
+    typename F::Piece w0[RT], w1[RT];
+    u32x4 x[NX];
+    load_x(x, p);
+    load_w<AUX>(w0, v, p);
+    put_x(x, 0);
+    p = take();
+    load_x(x, p);
+    load_w<AUX>(w1, v, p);
+    __syncthreads();
+    for (uint32_t c = 0;;) {
+      products(w0, 0);
+      put_x(x, 1);
+      keep_order();
+      p = take();
+      load_x(x, p);
+      load_w<AUX>(w0, v, p);
+      block_barrier();
+      if (++c >= np) break;
+      products(w1, 1);
+      put_x(x, 0);
+      keep_order();
+      p = take();
+      load_x(x, p);
+      load_w<AUX>(w1, v, p);
+      block_barrier();
+      if (++c >= np) break;
+    }
+  }
+  // LDS only: the loads in flight go to registers of the wave that waits for them
+  static __device__ __forceinline__ void block_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+};
 
 }  // namespace int8w
