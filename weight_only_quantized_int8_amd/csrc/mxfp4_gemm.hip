@@ -133,43 +133,46 @@ hipError_t launch_gemv(const MxView &w, const uint16_t *x, uint16_t *y, hipStrea
 // ---- few rows ---------------------------------------------------------------------------------
 
 // Activations in MXFP4: another tile of rows.
+template <bool DW>
 struct XMx {
   static constexpr uint32_t kLds = 1024u;
-  typedef MxFmt::Piece Piece;
+  typedef typename MxFmt<DW>::Piece Piece;
   MxView v;
-  MxFmt::Tile t;
+  typename MxFmt<DW>::Tile t;
   __device__ __forceinline__ XMx(const void *x, const uint8_t *scales, uint32_t m0, uint32_t m, uint32_t K, uint32_t lane) {
     v = MxView{(const uint8_t *)x, scales, m, K};
-    t = MxFmt::tile(v, 0, m0, m, lane);
+    t = MxFmt<DW>::tile(v, 0, m0, m, lane);
   }
-  __device__ __forceinline__ void load(Piece &f, uint32_t piece, uint32_t lane) const { MxFmt::load<0>(f, t, v, piece, lane); }
+  __device__ __forceinline__ void load(Piece &f, uint32_t piece, uint32_t lane) const { MxFmt<DW>::template load<0>(f, t, v, piece, lane); }
 };
 
-__device__ __forceinline__ void stream_piece_mx(f32x4 &acc, const Pieces<MxFmt, XMx, 1> &p, uint8_t *lds, uint32_t lane) {
+template <bool DW>
+__device__ __forceinline__ void stream_piece_mx(f32x4 &acc, const Pieces<MxFmt<DW>, XMx<DW>, 1> &p, uint8_t *lds, uint32_t lane) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
-    uint8_t *at = lds + (h & 1) * (stream_lds<XMx, 1>() / 2u);
+    uint8_t *at = lds + (h & 1) * (stream_lds<XMx<DW>, 1>() / 2u);
     put_quarter(at, p.w[0].q[h], lane);
     put_quarter(at + 1024u, p.x.q[h], lane);
     wave_fence();
-    acc = mfma_mx(get_quarter(at + 1024u, lane), MxFmt::scale(p.x, h, lane), get_quarter(at, lane),
-                  MxFmt::scale(p.w[0], h, lane), acc);
+    acc = mfma_mx(get_quarter(at + 1024u, lane), MxFmt<DW>::scale(p.x, h, lane), get_quarter(at, lane),
+                  MxFmt<DW>::scale(p.w[0], h, lane), acc);
     wave_fence();
   }
 }
 
 // grid: (16-row weight tiles) x (groups of 16 rows of X), the groups of a tile side by side.
-template <bool XMX, int KS, int U, int NX, int AUX>
+template <bool XMX, bool DW, int KS, int U, int NX, int AUX>
 __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
                                                      const uint8_t *__restrict__ xs, uint32_t m, uint32_t groups,
                                                      uint16_t *__restrict__ y) {
-  typedef std::conditional_t<XMX, XMx, XBf16<MxFmt, NX>> X;
+  typedef MxFmt<DW> F;
+  typedef std::conditional_t<XMX, XMx<DW>, XBf16<F, NX>> X;
   constexpr uint32_t kWaveLds = stream_lds<X, 1>();
   __shared__ __attribute__((aligned(16))) uint8_t lds[KS * kWaveLds];
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = w.K;
   const uint32_t n0 = 16u * (blockIdx.x / groups), m0 = 16u * (blockIdx.x % groups);
   const uint32_t rows = m - m0 < 16u ? m - m0 : 16u;
-  const MxFmt::Tile t = MxFmt::tile(w, 0, n0, w.N, lane);
+  const typename F::Tile t = F::tile(w, 0, n0, w.N, lane);
   auto make = [&]() {
     if constexpr (XMX)
       return X(x, xs, m0, m, K, lane);
@@ -178,11 +181,11 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
                [&](uint32_t i) { return i < rows ? i * K * 2u : kOutOfRange; });
   };
   const X xr = make();
-  Pieces<MxFmt, X, 1> r[U];
-  const uint32_t np = (K + MxFmt::kPiece - 1u) / MxFmt::kPiece;
-  auto load = [&](Pieces<MxFmt, X, 1> &b, uint32_t c) {
+  Pieces<F, X, 1> r[U];
+  const uint32_t np = (K + F::kPiece - 1u) / F::kPiece;
+  auto load = [&](Pieces<F, X, 1> &b, uint32_t c) {
     xr.load(b.x, c, lane);
-    MxFmt::load<AUX>(b.w[0], t, w, c, lane);
+    F::template load<AUX>(b.w[0], t, w, c, lane);
     keep_order();
   };
   f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
@@ -192,9 +195,9 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if constexpr (XMX)
-        stream_piece_mx(acc[0], r[u], lds + wave * kWaveLds, lane);
+        stream_piece_mx<DW>(acc[0], r[u], lds + wave * kWaveLds, lane);
       else
-        stream_piece<MxFmt, X, 1>(acc, r[u], xr, lds + wave * kWaveLds, lane);
+        stream_piece<F, X, 1>(acc, r[u], xr, lds + wave * kWaveLds, lane);
       keep_order();
       load(r[u], c + KS * (U + u));  // past the row's end: zeros, no traffic
     }
@@ -506,17 +509,24 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_mx_tile(MxView w, const u
   }
 }
 
-template <bool XMX, int NX, int AUX>
-hipError_t launch_rows(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
-  const uint32_t groups = (m + 15u) / 16u, grid = (w.N + 15u) / 16u * groups, np = (w.K + MxFmt::kPiece - 1u) / MxFmt::kPiece;
+template <bool XMX, bool DW, int NX, int AUX>
+hipError_t launch_rows_dw(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  const uint32_t groups = (m + 15u) / 16u, grid = (w.N + 15u) / 16u * groups;
+  const uint32_t np = (w.K + MxFmt<DW>::kPiece - 1u) / MxFmt<DW>::kPiece;
   constexpr int U = NX <= 2 && !XMX ? 2 : 1, K16 = NX == 1 ? 16 : 8;
   if (np >= 16u && grid <= 512u)
-    k_mx_rows<XMX, K16, U, NX, AUX><<<grid, 64 * K16, 0, stream>>>(w, x, xs, m, groups, y);
+    k_mx_rows<XMX, DW, K16, U, NX, AUX><<<grid, 64 * K16, 0, stream>>>(w, x, xs, m, groups, y);
   else if (np >= 8u)
-    k_mx_rows<XMX, 8, U, NX, AUX><<<grid, 512, 0, stream>>>(w, x, xs, m, groups, y);
+    k_mx_rows<XMX, DW, 8, U, NX, AUX><<<grid, 512, 0, stream>>>(w, x, xs, m, groups, y);
   else
-    k_mx_rows<XMX, 4, U, NX, AUX><<<grid, 256, 0, stream>>>(w, x, xs, m, groups, y);
+    k_mx_rows<XMX, DW, 4, U, NX, AUX><<<grid, 256, 0, stream>>>(w, x, xs, m, groups, y);
   return hipGetLastError();
+}
+
+template <bool XMX, int NX, int AUX>
+hipError_t launch_rows(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  const bool dw = mx_dwords(w) && (!XMX || (reinterpret_cast<uintptr_t>(xs) & 3u) == 0);
+  return dw ? launch_rows_dw<XMX, true, NX, AUX>(w, x, xs, m, y, stream) : launch_rows_dw<XMX, false, NX, AUX>(w, x, xs, m, y, stream);
 }
 
 template <bool XMX, int BM, int BN, int WM, int WN, int CH, int KG = 1>

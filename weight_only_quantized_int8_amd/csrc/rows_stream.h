@@ -75,6 +75,14 @@ __device__ __forceinline__ u32x4 get_quarter(const uint8_t *lds, uint32_t lane) 
 }
 
 // ---- MXFP4 ------------------------------------------------------------------------------------
+// DW: scales can be loaded four at a time (K a multiple of 128, scales 4-byte aligned).  A
+// choice at run time would cost every wait of the loop: after a branch the compiler counts
+// on the path with fewer loads in flight.
+__host__ __device__ inline bool mx_dwords(const MxView &w) {
+  return w.K % 128u == 0 && (reinterpret_cast<uintptr_t>(w.scales) & 3u) == 0;
+}
+
+template <bool DW>
 struct MxFmt {
   typedef MxView View;
   static constexpr uint32_t kQuarter = 128;           // k a quarter
@@ -85,7 +93,6 @@ struct MxFmt {
   struct Tile {  // 16 weight rows
     __amdgpu_buffer_rsrc_t codes, scales;
     uint32_t oc, os;  // this lane's byte offsets at piece 0 (kOutOfRange for a row past the end)
-    bool dwords;      // scales can be loaded four at a time
   };
   struct Piece {
     u32x4 q[4];
@@ -102,7 +109,6 @@ struct MxFmt {
     t.scales = make_rsrc(sc, rows * (w.K / 32u));
     t.oc = r < rows ? r * (w.K / 2u) + 16u * p : kOutOfRange;
     t.os = r < rows ? r * (w.K / 32u) + 4u * p : kOutOfRange;
-    t.dwords = w.K % 128u == 0 && (reinterpret_cast<uintptr_t>(sc) & 3u) == 0;
     return t;
   }
   template <int AUX>
@@ -112,7 +118,7 @@ struct MxFmt {
     for (int h = 0; h < 4; ++h)
       f.q[h] = buf_load_b128<AUX>(t.codes, b0 + 64u * h + 16u * p < w.K / 2u ? t.oc + b0 + 64u * h : kOutOfRange);
     const uint32_t blk = 16u * piece + 4u * p;  // first block of quarter p
-    if (t.dwords) {
+    if constexpr (DW) {
       f.s = __builtin_amdgcn_raw_buffer_load_b32(t.scales, (int)(blk < w.K / 32u ? t.os + 16u * piece : kOutOfRange), 0, 0);
     } else {
       f.s = 0;
