@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * KW, 3) void k_moe_up(typename F::View wg, type
     const uint32_t k = 4u * (lane >> 4) + i;
     if (k < n) {
       const uint32_t p = seg->slot[k];
-      h[(size_t)p * I + row] = to_bf16_bits(head->weight[p] * silu_mul(s.acc[0][i], s.acc[1][i]));
+      h[(size_t)p * I + row] = to_bf16_bits(head->weight[p] * silu_mul(s.acc[0][0][i] + s.acc[0][1][i], s.acc[1][0][i] + s.acc[1][1][i]));
     }
   }
 }
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(64 * KW, 4) void k_moe_down(typename F::View wd, ui
 #pragma unroll
   for (uint32_t i = 0; i < 4u; ++i) {
     const uint32_t k = 4u * (lane >> 4) + i;
-    if (k < n) out[(size_t)seg->slot[k] * H + row] = s.acc[0][i];
+    if (k < n) out[(size_t)seg->slot[k] * H + row] = s.acc[0][0][i] + s.acc[0][1][i];
   }
 }
 
@@ -535,8 +535,8 @@ hipError_t launch_layer(const typename F::View &g, const typename F::View &u, co
     route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, T, m.E, m.topk, m.renorm, m.scale, kSegTokens, head);
     const size_t at = (size_t)t0 * H;
     const uint32_t ub = (I + 16u * KW - 1u) / (16u * KW), db = (H + 16u * KW - 1u) / (16u * KW);
-    k_moe_up<F, KW, kAuxNontemporal><<<ub * most, 64 * KW, 0, stream>>>(g, u, I, ub, m.x + at, T, m.topk, head, h);
-    k_moe_down<F, KW, kAuxNontemporal><<<db * most, 64 * KW, 0, stream>>>(d, H, db, h, slots, head, out);
+    k_moe_up<F, KW, 0><<<ub * most, 64 * KW, 0, stream>>>(g, u, I, ub, m.x + at, T, m.topk, head, h);
+    k_moe_down<F, KW, 0><<<db * most, 64 * KW, 0, stream>>>(d, H, db, h, slots, head, out);
     k_moe_sum<<<dim3((H + 255u) / 256u, T), 256, 0, stream>>>(out, H, m.topk, head, m.resid ? m.resid + at : nullptr, m.y + at);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -147,15 +147,16 @@ struct XMx {
 };
 
 template <bool DW>
-__device__ __forceinline__ void stream_piece_mx(f32x4 &acc, const Pieces<MxFmt<DW>, XMx<DW>, 1> &p, uint8_t *lds, uint32_t lane) {
+__device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<MxFmt<DW>, XMx<DW>, 1> &p, uint8_t *lds, uint32_t lane) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    uint8_t *at = lds + (h & 1) * (stream_lds<XMx<DW>, 1>() / 2u);
-    put_quarter(at, p.w[0].q[h], lane);
-    put_quarter(at + 1024u, p.x.q[h], lane);
+  for (int hp = 0; hp < 2; ++hp) {
+    put_lines(lds, p.w[0].q, hp, lane);
+    put_lines(lds + 2048u, p.x.q, hp, lane);
     wave_fence();
-    acc = mfma_mx(get_quarter(at + 1024u, lane), MxFmt<DW>::scale(p.x, h, lane), get_quarter(at, lane),
-                  MxFmt<DW>::scale(p.w[0], h, lane), acc);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      acc[i] = mfma_mx(get_quarter(lds + 2048u + 1024u * i, lane), MxFmt<DW>::scale(p.x, 2 * hp + i, lane),
+                       get_quarter(lds + 1024u * i, lane), MxFmt<DW>::scale(p.w[0], 2 * hp + i, lane), acc[i]);
     wave_fence();
   }
 }
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
     F::template load<AUX>(b.w[0], t, w, c, lane);
     keep_order();
   };
-  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+  f32x4 acc[1][2] = {{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}};
 #pragma unroll
   for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
   for (uint32_t c = wave; c < np; c += KS * U) {
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
   }
   __syncthreads();
   float *red = reinterpret_cast<float *>(lds);  // the partial sums reuse the streams' LDS
-  reinterpret_cast<f32x4 *>(red)[wave * 64u + lane] = acc[0];
+  reinterpret_cast<f32x4 *>(red)[wave * 64u + lane] = acc[0][0] + acc[0][1];
   __syncthreads();
   for (uint32_t o = threadIdx.x; o < 16u * rows; o += 64u * KS) {
     const uint32_t row = o & 15u, tok = o >> 4;

@@ -10,10 +10,11 @@
 // of 64 bytes a row.
 //  * In the operand layout neighbouring lanes belong to different rows, and a load in
 //    that layout costs the address unit a cycle a lane (measured: 64 a load, 2.4 TB/s
-//    over the whole GPU).  So all loads are made with neighbouring lanes on
-//    neighbouring bytes (lane l: row l/4, 16-byte chunk l%4 of a quarter) and a quarter
-//    changes lanes through 1 KB of LDS that only this wave uses: one ds_write_b128, one
-//    ds_read_b128, no barrier.  Chunks are XOR-swizzled by row against bank conflicts.
+//    over the whole GPU).  So a load takes 128 bytes, a whole cache line, of each of 8
+//    rows, eight lanes side by side (with 64 bytes of 16 rows the same stream without its
+//    products took 204 us instead of 177), and the two quarters of a line change lanes
+//    through 2 KB of LDS that only this wave uses, with no barrier.  16-byte chunks are
+//    XOR-swizzled by row against bank conflicts.
 //  * Activations of a quarter take the same way (rows of 256 or 128 bytes).
 //  * Scales: one load a piece, lane l: row l/4, quarter l%4; a lane fetches its row's by
 //    a lane permute.
@@ -67,11 +68,35 @@ __device__ __forceinline__ uint32_t lane_get(uint32_t v, uint32_t from) {
 
 // A quarter of a tile of 16 rows x 64 bytes in LDS: chunk p of row r at 64 r + 16 (p ^ (r/2 % 4)).
 __device__ __forceinline__ uint32_t quarter_at(uint32_t r, uint32_t p) { return 64u * r + 16u * (p ^ ((r >> 1) & 3u)); }
-__device__ __forceinline__ void put_quarter(uint8_t *lds, u32x4 v, uint32_t lane) {
-  *reinterpret_cast<u32x4 *>(lds + quarter_at(lane >> 2, lane & 3u)) = v;
-}
 __device__ __forceinline__ u32x4 get_quarter(const uint8_t *lds, uint32_t lane) {  // chunk l/16 of row l%16
   return *reinterpret_cast<const u32x4 *>(lds + quarter_at(lane & 15u, lane >> 4));
+}
+
+// The loads of a tile's piece: load j takes rows 8 (j & 1) + l/8, bytes 128 (j >> 1) + 16 (l % 8).
+struct LineOffsets {
+  uint32_t o[2];  // this lane's byte offset at piece 0 in the upper and the lower eight rows
+  __device__ __forceinline__ LineOffsets() {}
+  __device__ __forceinline__ LineOffsets(uint32_t rows, uint32_t row_bytes, uint32_t lane) {
+    const uint32_t r = lane >> 3;
+    o[0] = r < rows ? r * row_bytes + 16u * (lane & 7u) : kOutOfRange;
+    o[1] = r + 8u < rows ? (r + 8u) * row_bytes + 16u * (lane & 7u) : kOutOfRange;
+  }
+};
+template <int AUX>
+__device__ __forceinline__ void load_lines(u32x4 (&q)[4], __amdgpu_buffer_rsrc_t rsrc, const LineOffsets &l, uint32_t row_bytes,
+                                           uint32_t piece, uint32_t lane) {
+  const uint32_t b0 = kPieceBytes * piece, c = 16u * (lane & 7u);
+#pragma unroll
+  for (uint32_t j = 0; j < 4u; ++j) {
+    const uint32_t b = b0 + 128u * (j >> 1);
+    q[j] = buf_load_b128<AUX>(rsrc, b + c < row_bytes ? l.o[j & 1u] + b : kOutOfRange);
+  }
+}
+// Quarters 2 hp and 2 hp + 1 of a piece to lds and lds + 1024.
+__device__ __forceinline__ void put_lines(uint8_t *lds, const u32x4 (&q)[4], int hp, uint32_t lane) {
+  uint8_t *const at = lds + 1024u * ((lane >> 2) & 1u);
+  *reinterpret_cast<u32x4 *>(at + quarter_at(lane >> 3, lane & 3u)) = q[2 * hp];
+  *reinterpret_cast<u32x4 *>(at + quarter_at(8u + (lane >> 3), lane & 3u)) = q[2 * hp + 1];
 }
 
 // ---- MXFP4 ------------------------------------------------------------------------------------
@@ -92,7 +117,8 @@ struct MxFmt {
   static constexpr int kRuns = 1;
   struct Tile {  // 16 weight rows
     __amdgpu_buffer_rsrc_t codes, scales;
-    uint32_t oc, os;  // this lane's byte offsets at piece 0 (kOutOfRange for a row past the end)
+    LineOffsets l;
+    uint32_t os;  // this lane's byte offset at piece 0 (kOutOfRange for a row past the end)
   };
   struct Piece {
     u32x4 q[4];
@@ -107,16 +133,14 @@ struct MxFmt {
     const uint8_t *sc = w.scales + row0 * (w.K / 32u);
     t.codes = make_rsrc(w.codes + row0 * (w.K / 2u), rows * (w.K / 2u));
     t.scales = make_rsrc(sc, rows * (w.K / 32u));
-    t.oc = r < rows ? r * (w.K / 2u) + 16u * p : kOutOfRange;
+    t.l = LineOffsets(rows, w.K / 2u, lane);
     t.os = r < rows ? r * (w.K / 32u) + 4u * p : kOutOfRange;
     return t;
   }
   template <int AUX>
   static __device__ __forceinline__ void load(Piece &f, const Tile &t, const MxView &w, uint32_t piece, uint32_t lane) {
-    const uint32_t p = lane & 3u, b0 = kPieceBytes * piece;
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      f.q[h] = buf_load_b128<AUX>(t.codes, b0 + 64u * h + 16u * p < w.K / 2u ? t.oc + b0 + 64u * h : kOutOfRange);
+    const uint32_t p = lane & 3u;
+    load_lines<AUX>(f.q, t.codes, t.l, w.K / 2u, piece, lane);
     const uint32_t blk = 16u * piece + 4u * p;  // first block of quarter p
     if constexpr (DW) {
       f.s = __builtin_amdgcn_raw_buffer_load_b32(t.scales, (int)(blk < w.K / 32u ? t.os + 16u * piece : kOutOfRange), 0, 0);
@@ -164,7 +188,8 @@ struct Int8Fmt {
   static constexpr int kRuns = G32 ? 2 : 1;  // runs of one group in a quarter
   struct Tile {
     __amdgpu_buffer_rsrc_t codes, scales, biases;
-    uint32_t oc, os;
+    LineOffsets l;
+    uint32_t os;
   };
   struct Piece {
     u32x4 q[4];
@@ -173,21 +198,19 @@ struct Int8Fmt {
 
   static __device__ __forceinline__ Tile tile(const WeightView &w, uint64_t base, uint32_t n0, uint32_t N, uint32_t lane) {
     Tile t;
-    const uint32_t rows = N - n0 < 16u ? N - n0 : 16u, r = lane >> 2, p = lane & 3u, G = w.K / w.gs;
+    const uint32_t rows = N - n0 < 16u ? N - n0 : 16u, r = lane >> 2, G = w.K / w.gs;
     const uint64_t row0 = base + n0;
     t.codes = make_rsrc((const uint8_t *)w.packed + row0 * w.K, rows * w.K);
     t.scales = make_rsrc(w.scales + row0 * G, rows * G * 2u);
     t.biases = make_rsrc(w.biases + row0 * G, rows * G * 2u);
-    t.oc = r < rows ? r * w.K + 16u * p : kOutOfRange;
+    t.l = LineOffsets(rows, w.K, lane);
     t.os = r < rows ? r * G * 2u : kOutOfRange;
     return t;
   }
   template <int AUX>
   static __device__ __forceinline__ void load(Piece &f, const Tile &t, const WeightView &w, uint32_t piece, uint32_t lane) {
     const uint32_t p = lane & 3u, b0 = kPieceBytes * piece;
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      f.q[h] = buf_load_b128<AUX>(t.codes, b0 + 64u * h + 16u * p < w.K ? t.oc + b0 + 64u * h : kOutOfRange);
+    load_lines<AUX>(f.q, t.codes, t.l, w.K, piece, lane);
     const uint32_t gl = 31u - (uint32_t)__builtin_clz(w.gs);
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
@@ -290,7 +313,7 @@ struct XBf16 {
   }
 };
 
-// LDS bytes of one wave: two quarters (one is written while the other is read) of RT tiles and the activations.
+// LDS bytes of one wave: two quarters of RT tiles and of the activations.
 template <class X, int RT>
 constexpr uint32_t stream_lds() {
   return 2u * (1024u * RT + X::kLds);
@@ -302,24 +325,29 @@ struct Pieces {
   typename X::Piece x;
 };
 
-// acc[t] += A B^T of one piece.
+// acc[t][0] + acc[t][1] += A B^T of one piece: the two quarters of a line have sums of their
+// own, so that neither waits for the other's products.
 template <class F, class X, int RT>
-__device__ __forceinline__ void stream_piece(f32x4 (&acc)[RT], const Pieces<F, X, RT> &p, const X &X_, uint8_t *lds,
+__device__ __forceinline__ void stream_piece(f32x4 (&acc)[RT][2], const Pieces<F, X, RT> &p, const X &X_, uint8_t *lds,
                                              uint32_t lane) {
-  constexpr uint32_t kHalf = stream_lds<X, RT>() / 2u;
+  uint8_t *const xl = lds + 2048u * RT;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    uint8_t *at = lds + (h & 1) * kHalf;
+  for (int hp = 0; hp < 2; ++hp) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t) put_quarter(at + 1024u * t, p.w[t].q[h], lane);
-    X_.put(at + 1024u * RT, p.x, h, lane);
+    for (int t = 0; t < RT; ++t) put_lines(lds + 2048u * t, p.w[t].q, hp, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) X_.put(xl + i * X::kLds, p.x, 2 * hp + i, lane);
     wave_fence();
-    u32x4 x[F::kXFrags];
-    X::get(x, at + 1024u * RT, lane);
-    typename F::Sums S;
-    F::sums(S, x);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) F::mac(acc[t], weight_operand<F>(at + 1024u * t, lane), p.w[t], h, x, S, lane);
+    for (int i = 0; i < 2; ++i) {
+      u32x4 x[F::kXFrags];
+      X::get(x, xl + i * X::kLds, lane);
+      typename F::Sums S;
+      F::sums(S, x);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        F::mac(acc[t][i], weight_operand<F>(lds + 2048u * t + 1024u * i, lane), p.w[t], 2 * hp + i, x, S, lane);
+    }
     wave_fence();
   }
 }
@@ -344,7 +372,7 @@ struct BlockStream {
   __amdgpu_buffer_rsrc_t rx;
   uint32_t K, lane, wave, xo[NX], xk[NX], xl[NX];
   uint8_t *lds;
-  f32x4 acc[RT];
+  f32x4 acc[RT][2];  // to be added
 
   // row(i): byte offset of activation row i (i < 16), or kOutOfRange
   template <class Row>
@@ -360,7 +388,7 @@ struct BlockStream {
       xl[j] = k / F::kXChunks * kQuarterLds + XBf16<F, 1>::at(r, k % F::kXChunks);
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   __device__ __forceinline__ void load_x(u32x4 (&v)[NX], uint32_t piece) const {
     const uint32_t b = piece * (2u * F::kPiece);
@@ -381,19 +409,22 @@ struct BlockStream {
   __device__ __forceinline__ void products(const typename F::Piece (&w)[RT], uint32_t buf) {
     uint8_t *const own = lds + 2u * kXLds + wave * kWaveLds;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint8_t *at = own + (h & 1) * (1024u * RT);
+    for (int hp = 0; hp < 2; ++hp) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) put_quarter(at + 1024u * i, w[i].q[h], lane);
+      for (int t = 0; t < RT; ++t) put_lines(own + 2048u * t, w[t].q, hp, lane);
       wave_fence();
-      u32x4 x[F::kXFrags];
 #pragma unroll
-      for (int f = 0; f < F::kXFrags; ++f)
-        x[f] = *reinterpret_cast<const u32x4 *>(lds + buf * kXLds + h * kQuarterLds + XBf16<F, 1>::at(lane & 15u, F::x_chunk(f, lane >> 4)));
-      typename F::Sums S;
-      F::sums(S, x);
+      for (int i = 0; i < 2; ++i) {
+        const int h = 2 * hp + i;
+        u32x4 x[F::kXFrags];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) F::mac(acc[i], weight_operand<F>(at + 1024u * i, lane), w[i], h, x, S, lane);
+        for (int f = 0; f < F::kXFrags; ++f)
+          x[f] = *reinterpret_cast<const u32x4 *>(lds + buf * kXLds + h * kQuarterLds + XBf16<F, 1>::at(lane & 15u, F::x_chunk(f, lane >> 4)));
+        typename F::Sums S;
+        F::sums(S, x);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) F::mac(acc[t][i], weight_operand<F>(own + 2048u * t + 1024u * i, lane), w[t], h, x, S, lane);
+      }
       wave_fence();
     }
   }
