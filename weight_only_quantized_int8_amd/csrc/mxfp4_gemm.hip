@@ -514,13 +514,14 @@ template <bool XMX, bool DW, int NX, int AUX>
 hipError_t launch_rows_dw(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
   const uint32_t groups = (m + 15u) / 16u, grid = (w.N + 15u) / 16u * groups;
   const uint32_t np = (w.K + MxFmt<DW>::kPiece - 1u) / MxFmt<DW>::kPiece;
-  constexpr int U = NX <= 2 && !XMX ? 2 : 1, K16 = NX == 1 ? 16 : 8;
-  if (np >= 16u && grid <= 512u)
-    k_mx_rows<XMX, DW, K16, U, NX, AUX><<<grid, 64 * K16, 0, stream>>>(w, x, xs, m, groups, y);
-  else if (np >= 8u)
-    k_mx_rows<XMX, DW, 8, U, NX, AUX><<<grid, 512, 0, stream>>>(w, x, xs, m, groups, y);
+  // Four waves share a tile's K, eight where there is at most a tile a CU and K is long
+  // (us with four / eight: m = 2 8192x28672 25 / 27, m = 8 14336x4096 12.6 / 22,
+  // m = 16 4096x14336 14.5 / 13.6).
+  constexpr int U4 = !XMX && NX <= 2 ? 2 : 1;
+  if (grid <= (uint32_t)device_cu_count() && np >= 16u)
+    k_mx_rows<XMX, DW, 8, 1, NX, AUX><<<grid, 512, 0, stream>>>(w, x, xs, m, groups, y);
   else
-    k_mx_rows<XMX, DW, 4, U, NX, AUX><<<grid, 256, 0, stream>>>(w, x, xs, m, groups, y);
+    k_mx_rows<XMX, DW, 4, U4, NX, AUX><<<grid, 256, 0, stream>>>(w, x, xs, m, groups, y);
   return hipGetLastError();
 }
 

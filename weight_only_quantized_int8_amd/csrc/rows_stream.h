@@ -115,6 +115,7 @@ struct MxFmt {
   static constexpr uint32_t kXChunks = 16;            // 16-byte chunks of an activation row in a quarter
   static constexpr int kXFrags = 4;                   // A operands of a quarter
   static constexpr int kRuns = 1;
+  static __host__ __device__ constexpr uint32_t row_bytes(uint32_t K) { return K / 2u; }
   struct Tile {  // 16 weight rows
     __amdgpu_buffer_rsrc_t codes, scales;
     LineOffsets l;
@@ -186,6 +187,7 @@ struct Int8Fmt {
   static constexpr uint32_t kXChunks = 8;
   static constexpr int kXFrags = 2;
   static constexpr int kRuns = G32 ? 2 : 1;  // runs of one group in a quarter
+  static __host__ __device__ constexpr uint32_t row_bytes(uint32_t K) { return K; }
   struct Tile {
     __amdgpu_buffer_rsrc_t codes, scales, biases;
     LineOffsets l;
