@@ -571,10 +571,7 @@ class Mxfp4Weight:
             raise ValueError("codes and scales must be contiguous")
         if codes.device != scales.device or codes.device.type != "cuda":
             raise ValueError("codes and scales must be on one GPU")
-        self.codes, self.scales = codes, scales
-        self.rows, self.k = rows, k
-        self.device = codes.device
-        self.desc = Mxfp4Desc(codes.data_ptr(), scales.data_ptr(), rows, k)
+        self._set(codes, scales, rows, k, codes.device)
 
     @classmethod
     def quantize(cls, x: torch.Tensor) -> "Mxfp4Weight":
@@ -589,7 +586,13 @@ class Mxfp4Weight:
         scales = torch.empty((rows, k // 32), dtype=torch.uint8, device=x.device)
         _check(int8w_mxfp4_quantize(x.data_ptr(), VALUES_F32 if x.dtype == torch.float32 else VALUES_BF16, rows, k,
                                     codes.data_ptr(), scales.data_ptr(), _stream_of(x.device)))
-        return cls(codes, scales)
+        q = cls.__new__(cls)  # the tensors are as __init__ wants them
+        q._set(codes, scales, rows, k, x.device)
+        return q
+
+    def _set(self, codes, scales, rows, k, device) -> None:
+        self.codes, self.scales, self.rows, self.k, self.device = codes, scales, rows, k, device
+        self.desc = Mxfp4Desc(codes.data_ptr(), scales.data_ptr(), rows, k)
 
     def dequantize_to(self, out: torch.Tensor | None = None) -> torch.Tensor:
         if out is None:

@@ -355,8 +355,9 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wd.K, segs = token_segs<F>(K);
   // the rows of h past the last chosen expert's hold nothing, and are not used
   TokenStage<F> stage(h, K, topk, threadIdx.x, 64u * KW);
-  const uint32_t n = uniform32(head->segments), ids = head->seg[lane < kMaxTopk ? lane : 0u].expert;
+  const uint32_t count = head->segments, ids = head->seg[lane < kMaxTopk ? lane : 0u].expert;
   stage.load();
+  const uint32_t n = uniform32(count);
   const uint32_t units = gridDim.x * (KW / KS), unit = blockIdx.x * (KW / KS) + wave / KS, ks = wave % KS;
   const uint32_t pairs = (H + 1u) / 2u;
   const uint32_t p0 = (uint32_t)((uint64_t)pairs * unit / units), p1 = (uint32_t)((uint64_t)pairs * (unit + 1u) / units);
@@ -463,17 +464,22 @@ bool one_token_fits(uint32_t H, uint32_t I, uint32_t topk) {
   return token_lds<F>(H) <= kLdsBytes - 1024u && (uint64_t)topk * token_lds<F>(I) <= kLdsBytes - 1024u;
 }
 
+// Dynamic LDS above 64 KiB has to be allowed once a kernel.
 template <class K>
-hipError_t allow_lds(K kernel, uint32_t lds) {
-  if (lds <= 64u << 10) return hipSuccess;
-  return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+hipError_t allow_lds(K kernel, uint32_t lds, bool &allowed) {
+  if (allowed || lds <= 64u << 10) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)kLdsBytes - 1024);
+  allowed = e == hipSuccess;
+  return e;
 }
 
 template <class F, int KW, int R>
 hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, const MoeArgs &m, MoeHead *head, uint16_t *h,
                          uint32_t I, uint32_t lds, hipStream_t stream) {
   auto kern = k_moe1_up<F, KW, 4, R>;
-  hipError_t e = allow_lds(kern, lds);
+  static bool allowed = false;
+  hipError_t e = allow_lds(kern, lds, allowed);
   if (e != hipSuccess) return e;
   const uint32_t cus = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW, most = cus * 16u / KW;
   kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits, m.logits_bf16, m.E, m.topk, m.renorm,
@@ -485,7 +491,8 @@ template <class F, int KW, int KS>
 hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead *head, const uint16_t *h, uint32_t H,
                            uint32_t lds, hipStream_t stream) {
   auto kern = k_moe1_down<F, KW, 4, KS>;
-  hipError_t e = allow_lds(kern, lds);
+  static bool allowed = false;
+  hipError_t e = allow_lds(kern, lds, allowed);
   if (e != hipSuccess) return e;
   const uint32_t cus = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
   const uint32_t most = cus * 16u / KW;
