@@ -11,6 +11,7 @@
 //   (both MXFP4: 16 x 16 x 128 products with a scale per 32 k in the
 //   instruction).
 #include <type_traits>
+#include <utility>
 
 #include "rows_stream.h"
 #include "token_stream.h"
@@ -259,6 +260,11 @@ __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t c) {
   return c ^ ((row >> 1) & 3u);
 }
 
+template <int... N, class Body>
+__device__ __forceinline__ void for_each(std::integer_sequence<int, N...>, Body &body) {
+  (body(std::integral_constant<int, N>{}), ...);
+}
+
 template <int C>
 __device__ __forceinline__ f32x4 mfma_mx_sel(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
   const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
@@ -317,20 +323,24 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_mx_tile(MxView w, const u
     pw[j] = 16u * swz<S::WB / 16u>(row, slot % (S::WB / 16u));
     vw[j] = row < nrows ? row * wrow + pw[j] : kOutOfRange;
   }
-  auto dma = [&](uint32_t step, uint8_t *base) {
-#pragma unroll
-    for (int j = 0; j < S::NX; ++j) {
+  // Load j of the wave's NX + NW of a step.
+  constexpr int kLoads = S::NX + S::NW;
+  auto dma_one = [&](int j, uint32_t step, uint8_t *base) {
+    if (j < S::NX) {
       const bool in = step * S::XB + px[j] < xrow;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (__attribute__((address_space(3))) void *)(base + (wave * S::NX + j) * 1024u),
                                                16, (int)(in ? vx[j] + step * S::XB : kOutOfRange), 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < S::NW; ++j) {
-      const bool in = step * S::WB + pw[j] < wrow;
+    } else {
+      const int i = j - S::NX;
+      const bool in = step * S::WB + pw[i] < wrow;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (__attribute__((address_space(3))) void *)(base + S::X_BYTES + (wave * S::NW + j) * 1024u), 16,
-          (int)(in ? vw[j] + step * S::WB : kOutOfRange), 0, 0, 0);
+          rw, (__attribute__((address_space(3))) void *)(base + S::X_BYTES + (wave * S::NW + i) * 1024u), 16,
+          (int)(in ? vw[i] + step * S::WB : kOutOfRange), 0, 0, 0);
     }
+  };
+  auto dma = [&](uint32_t step, uint8_t *base) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) dma_one(j, step, base);
   };
   auto load_scales = [&](u32x4 (&v)[S::NS], uint32_t group) {
 #pragma unroll
@@ -390,38 +400,66 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_mx_tile(MxView w, const u
 #pragma unroll
     for (int j = 0; j < S::TM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // chunk C of the group, the step's chunk c
-  auto chunk = [&](auto tag, int c, const uint8_t *base) {
-    constexpr int C = decltype(tag)::value;
+  // The products of a step (chunks C0 .. C0 + CH - 1 of the group).  The weight operands are
+  // read kAhead products of a row ahead: with the one that the compiler left by itself, four
+  // products did not cover an LDS read.
+  // With both operands in MXFP4 the next step's loads go out between the first half of the
+  // products: issued together after the barrier, the waves' loads queue for the address unit
+  // before any product starts (m = 2048 14336x4096 82 us instead of 86 with both changes).
+  // BF16 products take four times as long and the compiler's own order is 3 % faster there.
+  auto step_products = [&](auto tag, const uint8_t *base, uint32_t next, uint8_t *next_base) {
+    constexpr int C0 = decltype(tag)::value;
+    constexpr int kHalf = (CH * S::TN + 1) / 2, kPer = (kLoads + kHalf - 1) / kHalf;
+    auto issue = [&](int n) {
+#pragma unroll
+      for (int j = n * kPer; j < (n + 1) * kPer && j < kLoads; ++j) dma_one(j, next, next_base);
+    };
     const uint8_t *xb = base, *wb = base + S::X_BYTES;
+    auto wread = [&](int n) {  // weight operand n of the step
+      const uint32_t row = (wn * S::TN + (uint32_t)(n % S::TN)) * 16u + lr;
+      return *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * (uint32_t)(n / S::TN) + g));
+    };
+    constexpr int kAhead = 3, kSteps = CH * S::TN;
+    u32x4 wq[kAhead];
     if constexpr (XMX) {
-      u32x4 b[S::TM];
+      u32x4 b[2][S::TM];
+      auto xread = [&](int c) {
 #pragma unroll
-      for (int j = 0; j < S::TM; ++j) {
-        const uint32_t row = (wm * S::TM + j) * 16u + lr;
-        b[j] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 4u * c + g));
-      }
+        for (int j = 0; j < S::TM; ++j) {
+          const uint32_t row = (wm * S::TM + j) * 16u + lr;
+          b[c & 1][j] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 4u * c + g));
+        }
+      };
+      xread(0);
 #pragma unroll
-      for (int i = 0; i < S::TN; ++i) {
-        const uint32_t row = (wn * S::TN + i) * 16u + lr;
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
+      for (int n = 0; n < kAhead && n < kSteps; ++n) wq[n] = wread(n);
+      keep_order();
+      auto row_products = [&](auto ntag) {
+        constexpr int n = decltype(ntag)::value, c = n / S::TN, i = n % S::TN;
+        const u32x4 q = wq[n % kAhead];
+        if (CH > 1 && c + 1 < CH && i == S::TN / 2) xread(c + 1);
+        if (n + kAhead < kSteps) wq[n % kAhead] = wread(n + kAhead);
 #pragma unroll
-        for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma_mx_sel<C>(a, sw[i], b[j], sx[j], acc[i][j]);
-      }
+        for (int j = 0; j < S::TM; ++j) acc[i][j] = mfma_mx_sel<C0 + c>(q, sw[i], b[c & 1][j], sx[j], acc[i][j]);
+        issue(n);
+        keep_order();
+      };
+      for_each(std::make_integer_sequence<int, kSteps>{}, row_products);
     } else {
+      static_assert(CH == 1, "one chunk a step");
+      dma(next, next_base);
       u32x4 b[S::TM][4];
 #pragma unroll
       for (int j = 0; j < S::TM; ++j) {
         const uint32_t row = (wm * S::TM + j) * 16u + lr;
 #pragma unroll
         for (int f = 0; f < 4; ++f)
-          b[j][f] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 16u * c + 4u * g + f));
+          b[j][f] = *reinterpret_cast<const u32x4 *>(xb + row * S::XB + 16u * swz<S::XB / 16u>(row, 4u * g + f));
       }
 #pragma unroll
       for (int i = 0; i < S::TN; ++i) {
-        const uint32_t row = (wn * S::TN + i) * 16u + lr;
-        const u32x4 q = *reinterpret_cast<const u32x4 *>(wb + row * S::WB + 16u * swz<S::WB / 16u>(row, 4u * c + g));
-        const float sc = mx_scale_f32((sw[i] >> (8 * C)) & 0xFFu);
+        const u32x4 q = wread(i);
+        const float sc = mx_scale_f32((sw[i] >> (8 * C0)) & 0xFFu);
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const uint4 a = mx_to_bf16x8(q[f], sc);
@@ -451,29 +489,21 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_mx_tile(MxView w, const u
     const uint32_t q = part + KG * i;
     get_scales(i & 1u);
     if constexpr (CH == 2) {
-      dma(2u * q + 1u, st1);
       load_scales(sv, q + KG);
-      chunk(std::integral_constant<int, 0>{}, 0, st0);
-      chunk(std::integral_constant<int, 1>{}, 1, st0);
+      step_products(std::integral_constant<int, 0>{}, st0, 2u * q + 1u, st1);
       sync();
-      dma(2u * (q + KG), st0);
-      chunk(std::integral_constant<int, 2>{}, 0, st1);
-      chunk(std::integral_constant<int, 3>{}, 1, st1);
+      step_products(std::integral_constant<int, 2>{}, st1, 2u * (q + KG), st0);
       put_scales(sv, (i + 1u) & 1u);
       sync();
     } else {
-      dma(4u * q + 1u, st1);
       load_scales(sv, q + KG);
-      chunk(std::integral_constant<int, 0>{}, 0, st0);
+      step_products(std::integral_constant<int, 0>{}, st0, 4u * q + 1u, st1);
       sync();
-      dma(4u * q + 2u, st0);
-      chunk(std::integral_constant<int, 1>{}, 0, st1);
+      step_products(std::integral_constant<int, 1>{}, st1, 4u * q + 2u, st0);
       sync();
-      dma(4u * q + 3u, st1);
-      chunk(std::integral_constant<int, 2>{}, 0, st0);
+      step_products(std::integral_constant<int, 2>{}, st0, 4u * q + 3u, st1);
       sync();
-      dma(4u * (q + KG), st0);
-      chunk(std::integral_constant<int, 3>{}, 0, st1);
+      step_products(std::integral_constant<int, 3>{}, st1, 4u * (q + KG), st0);
       put_scales(sv, (i + 1u) & 1u);
       sync();
     }
