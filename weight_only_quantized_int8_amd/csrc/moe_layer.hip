@@ -477,11 +477,11 @@ hipError_t allow_lds(K kernel, uint32_t lds, bool &allowed) {
 template <class F, int KW, int R>
 hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, const MoeArgs &m, MoeHead *head, uint16_t *h,
                          uint32_t I, uint32_t lds, hipStream_t stream) {
-  auto kern = k_moe1_up<F, KW, 4, R>;
+  auto kern = k_moe1_up<F, KW, 2, R>;
   static bool allowed = false;
   hipError_t e = allow_lds(kern, lds, allowed);
   if (e != hipSuccess) return e;
-  const uint32_t cus = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW, most = cus * 16u / KW;
+  const uint32_t most = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW;
   kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits, m.logits_bf16, m.E, m.topk, m.renorm,
                                                            m.scale, head, h);
   return hipGetLastError();
@@ -490,12 +490,11 @@ hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, c
 template <class F, int KW, int KS>
 hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead *head, const uint16_t *h, uint32_t H,
                            uint32_t lds, hipStream_t stream) {
-  auto kern = k_moe1_down<F, KW, 4, KS>;
+  auto kern = k_moe1_down<F, KW, 2, KS>;
   static bool allowed = false;
   hipError_t e = allow_lds(kern, lds, allowed);
   if (e != hipSuccess) return e;
-  const uint32_t cus = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
-  const uint32_t most = cus * 16u / KW;
+  const uint32_t most = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
   kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(d, H, h, m.topk, head, m.resid, m.y);
   return hipGetLastError();
 }
@@ -512,16 +511,18 @@ template <class F>
 hipError_t launch_one(const typename F::View &g, const typename F::View &u, const typename F::View &d, const MoeArgs &m,
                       MoeHead *head, uint16_t *h, hipStream_t stream) {
   const uint32_t I = g.N / m.E, H = d.N / m.E;
-  // two workgroups of 8 waves a CU where their LDS allows, else one of 16
-  const uint32_t lu = token_lds<F>(H), ld = m.topk * token_lds<F>(I), half = kLdsBytes / 2u - 1024u;
-  const hipError_t e = lu <= half ? launch_one_up_r<F, 8>(g, u, m, head, h, I, lu, stream)
-                                  : launch_one_up_r<F, 16>(g, u, m, head, h, I, lu, stream);
+  // One workgroup of 8 waves a CU with two segments of a pair in flight each: more waves cost
+  // more to start, and a longer ring more instructions to fetch, than they bring (us with
+  // 8 / 16 waves a CU: the smallest layers 15 / 18.5 and 13 / 17.6, 8x14336x4096 64 / 64; with
+  // 2 / 4 / 8 segments 14.8 / 14.7 / 18.2, 12.4 / 13.0 / 15.9, 64 / 66 / 68).
+  constexpr int KW = 8;
+  const uint32_t lu = token_lds<F>(H), ld = m.topk * token_lds<F>(I);
+  const hipError_t e = launch_one_up_r<F, KW>(g, u, m, head, h, I, lu, stream);
   if (e != hipSuccess) return e;
-  const uint32_t pairs = (H + 1u) / 2u, waves = 16u * (uint32_t)device_cu_count();
-  if (ld > half) return launch_one_down<F, 16, 1>(d, m, head, h, H, ld, stream);
-  if (pairs * 4u <= waves) return launch_one_down<F, 8, 4>(d, m, head, h, H, ld, stream);
-  if (pairs * 2u <= waves) return launch_one_down<F, 8, 2>(d, m, head, h, H, ld, stream);
-  return launch_one_down<F, 8, 1>(d, m, head, h, H, ld, stream);
+  const uint32_t pairs = (H + 1u) / 2u, waves = KW * (uint32_t)device_cu_count();
+  if (pairs * 4u <= waves) return launch_one_down<F, KW, 4>(d, m, head, h, H, ld, stream);
+  if (pairs * 2u <= waves) return launch_one_down<F, KW, 2>(d, m, head, h, H, ld, stream);
+  return launch_one_down<F, KW, 1>(d, m, head, h, H, ld, stream);
 }
 
 template <class F, class One>

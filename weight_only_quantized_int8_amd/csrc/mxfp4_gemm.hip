@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *_
 
 template <int KW, int KS>
 hipError_t launch_gemv_one(const MxView &w, const uint16_t *x, uint16_t *y, hipStream_t stream) {
-  auto kern = k_mx_gemv<KW, 4, KS>;
+  auto kern = k_mx_gemv<KW, 2, KS>;
   const uint32_t lds = token_lds<MxTok>(w.K);
   static bool allowed = false;  // dynamic LDS above 64 KiB, once a kernel
   if (!allowed && lds > 64u << 10) {
@@ -119,15 +119,17 @@ hipError_t launch_gemv_one(const MxView &w, const uint16_t *x, uint16_t *y, hipS
     allowed = true;
   }
   const uint32_t units = KW / KS, want = ((w.N + 1u) / 2u + units - 1u) / units;
-  const uint32_t most = (uint32_t)device_cu_count() * 16u / KW;
+  const uint32_t most = (uint32_t)device_cu_count();
   kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(w, x, y);
   return hipGetLastError();
 }
 
 hipError_t launch_gemv(const MxView &w, const uint16_t *x, uint16_t *y, hipStream_t stream) {
-  // two workgroups of 8 waves a CU where their LDS allows, else one of 16
-  if (token_lds<MxTok>(w.K) > (79u << 10)) return launch_gemv_one<16, 1>(w, x, y, stream);
-  const uint32_t pairs = (w.N + 1u) / 2u, waves = 16u * (uint32_t)device_cu_count(), segs = token_segs<MxTok>(w.K);
+  // one workgroup of 8 waves a CU, two segments of a pair in flight: more waves cost more to
+  // start, and a longer ring more instructions to fetch, than they bring (us with 8 / 16 waves
+  // a CU: 4096x4096 4.9 / 6.5, 4096x14336 8.0 / 9.0, 8192x28672 22.5 / 22.5; with 2 / 4 / 8
+  // segments 4.1 / 4.7 / 5.9, 7.8 / 7.9 / 9.5, 22.6 / 22.6 / 23.9)
+  const uint32_t pairs = (w.N + 1u) / 2u, waves = 8u * (uint32_t)device_cu_count(), segs = token_segs<MxTok>(w.K);
   if (pairs * 4u <= waves && segs >= 4u) return launch_gemv_one<8, 4>(w, x, y, stream);
   if (pairs * 2u <= waves && segs >= 2u) return launch_gemv_one<8, 2>(w, x, y, stream);
   return launch_gemv_one<8, 1>(w, x, y, stream);
