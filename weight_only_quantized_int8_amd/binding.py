@@ -571,7 +571,7 @@ class Mxfp4Weight:
             raise ValueError("codes and scales must be contiguous")
         if codes.device != scales.device or codes.device.type != "cuda":
             raise ValueError("codes and scales must be on one GPU")
-        self._set(codes, scales, rows, k, codes.device)
+        self._set(codes, scales, rows, k, codes.device, codes.data_ptr(), scales.data_ptr())
 
     @classmethod
     def quantize(cls, x: torch.Tensor) -> "Mxfp4Weight":
@@ -582,23 +582,25 @@ class Mxfp4Weight:
         rows, k = x.shape
         if k == 0 or k % 32:
             raise ValueError(f"k {k} must be a positive multiple of 32")
-        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((rows, k // 32), dtype=torch.uint8, device=x.device)
-        _check(int8w_mxfp4_quantize(x.data_ptr(), VALUES_F32 if x.dtype == torch.float32 else VALUES_BF16, rows, k,
-                                    codes.data_ptr(), scales.data_ptr(), _stream_of(x.device)))
+        codes = x.new_empty((rows, k // 2), dtype=torch.uint8)
+        scales = x.new_empty((rows, k // 32), dtype=torch.uint8)
+        c, s, device = codes.data_ptr(), scales.data_ptr(), x.device
+        _check(load_library().int8w_mxfp4_quantize(x.data_ptr(), VALUES_F32 if x.dtype == torch.float32 else VALUES_BF16,
+                                                   rows, k, c, s, _stream_of(device)))
         q = cls.__new__(cls)  # the tensors are as __init__ wants them
-        q._set(codes, scales, rows, k, x.device)
+        q._set(codes, scales, rows, k, device, c, s)
         return q
 
-    def _set(self, codes, scales, rows, k, device) -> None:
+    def _set(self, codes, scales, rows, k, device, codes_ptr, scales_ptr) -> None:
         self.codes, self.scales, self.rows, self.k, self.device = codes, scales, rows, k, device
-        self.desc = Mxfp4Desc(codes.data_ptr(), scales.data_ptr(), rows, k)
+        self.desc = Mxfp4Desc(codes_ptr, scales_ptr, rows, k)
 
     def dequantize_to(self, out: torch.Tensor | None = None) -> torch.Tensor:
         if out is None:
             out = torch.empty((self.rows, self.k), dtype=torch.bfloat16, device=self.device)
-        _need_bf16(out, "out", self.rows * self.k, self.device)
-        _check(int8w_mxfp4_dequantize_to(self.desc, out.data_ptr(), _stream_of(self.device)))
+        else:
+            _need_bf16(out, "out", self.rows * self.k, self.device)
+        _check(load_library().int8w_mxfp4_dequantize_to(self.desc, out.data_ptr(), _stream_of(self.device)))
         return out
 
     def gemm(self, x: torch.Tensor, y: torch.Tensor | None = None) -> torch.Tensor:
@@ -608,9 +610,10 @@ class Mxfp4Weight:
         m = x.shape[0]
         _need_bf16(x, "X", m * self.k, self.device)
         if y is None:
-            y = torch.empty((m, self.rows), dtype=torch.bfloat16, device=self.device)
-        _need_bf16(y, "Y", m * self.rows, self.device)
-        _check(int8w_mxfp4_gemm(self.desc, x.data_ptr(), y.data_ptr(), m, _stream_of(self.device)))
+            y = x.new_empty((m, self.rows))
+        else:
+            _need_bf16(y, "Y", m * self.rows, self.device)
+        _check(load_library().int8w_mxfp4_gemm(self.desc, x.data_ptr(), y.data_ptr(), m, _stream_of(self.device)))
         return y
 
     def gemm_mx(self, x: "Mxfp4Weight", y: torch.Tensor | None = None) -> torch.Tensor:
@@ -621,8 +624,9 @@ class Mxfp4Weight:
             raise ValueError(f"X is on {x.device}, weight on {self.device}")
         if y is None:
             y = torch.empty((x.rows, self.rows), dtype=torch.bfloat16, device=self.device)
-        _need_bf16(y, "Y", x.rows * self.rows, self.device)
-        _check(int8w_mxfp4_gemm_mx(self.desc, x.desc, y.data_ptr(), _stream_of(self.device)))
+        else:
+            _need_bf16(y, "Y", x.rows * self.rows, self.device)
+        _check(load_library().int8w_mxfp4_gemm_mx(self.desc, x.desc, y.data_ptr(), _stream_of(self.device)))
         return y
 
 
