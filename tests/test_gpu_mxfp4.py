@@ -126,7 +126,9 @@ def test_outputs_stay_inside_their_buffers():
 SHAPES = [(1, 1, 32), (1, 77, 64), (1, 4096, 4096), (1, 1025, 4128), (1, 300, 28672), (1, 33, 36896), (1, 8, 90016),
           (2, 50, 96), (4, 1024, 4096), (5, 130, 544), (8, 4096, 1024), (9, 77, 2080), (16, 513, 4096), (16, 40, 14336),
           (17, 100, 1056), (32, 260, 4096), (64, 1000, 608), (33, 7, 8192), (65, 70, 96), (96, 300, 2080), (128, 1024, 1024),
-          (130, 259, 4128), (300, 1024, 512), (513, 129, 672), (700, 2304, 256)]
+          (130, 259, 4128), (300, 1024, 512), (513, 129, 672), (700, 2304, 256),
+          # 64 x 32 tiles, and 64 x 64 / 64 x 128, with every edge ragged: K off 128 and off 512, one to nine groups
+          (130, 1501, 4128), (100, 1790, 608), (513, 513, 2080), (70, 2501, 32), (700, 2301, 1056)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -219,6 +221,30 @@ def test_scales_of_any_alignment(m):
         xs.copy_(q.scales)
         a, b = w.gemm_mx(q), w.gemm_mx(Mxfp4Weight(q.codes, xs))
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("off", [0, 1, 2])
+@pytest.mark.parametrize("m,n", [(130, 1501), (700, 2301), (1000, 2700)])
+def test_tiles_with_nan_scales_of_any_alignment(m, n, off):
+    # 64 x 32, 64 x 64 (64 x 128) and large tiles; K = 736: 23 scale bytes a row, so every row's start differs
+    log(f"tiles m={m} n={n} offset {off}")
+    k = 736
+    codes, scales = matrix(31, n, k)
+    scales[n // 3, 5] = 255
+    scales[n - 2, 22] = 255  # the last block of a row
+    s = torch.zeros(scales.size + 3, dtype=torch.uint8, device="cuda")[off:off + scales.size].view(n, k // 32)
+    s.copy_(torch.from_numpy(scales))
+    w = Mxfp4Weight(torch.from_numpy(codes).cuda(), s)
+    W = R.decode(codes, scales)
+    xb = bits_of(np.random.default_rng(32).standard_normal((m, k)))
+    ref, lim = R.product(R.bf16_values(xb), W)
+    check(w.gemm(bits_to_dev(xb)), ref, lim, "gemm")
+    xc, xsc = matrix(33, m, k)
+    xsc[m // 2, 3] = 255
+    xs = torch.zeros(xsc.size + 3, dtype=torch.uint8, device="cuda")[off:off + xsc.size].view(m, k // 32)
+    xs.copy_(torch.from_numpy(xsc))
+    ref, lim = R.product(R.decode(xc, xsc), W)
+    check(w.gemm_mx(Mxfp4Weight(torch.from_numpy(xc).cuda(), xs)), ref, lim, "gemm_mx")
 
 
 def test_no_rows():

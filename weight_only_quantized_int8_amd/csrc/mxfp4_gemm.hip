@@ -370,11 +370,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_mx_tile(MxView w, const u
         }
         return o;
       };
-      // a wave's 64 rows are all the weight's or all X's (BN is a multiple of 64)
-      if (!XMX || uniform32(row) < BN)
+      const uint32_t first = uniform32(row);  // of the wave's 64
+      if (!XMX || first + 63u < BN)
         v[j] = one(rws, have);
-      else
+      else if (first >= BN)
         v[j] = one(rxs, have);
+      else
+        v[j] = one(rws, have && isw) | one(rxs, have && !isw);
     }
   };
   uint8_t *const sbase = lds_mx + 2u * S::STAGE;
@@ -590,24 +592,26 @@ hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_
   if (m <= 4u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
   if (m <= 8u) return launch_rows<XMX, 2, kAuxNontemporal>(w, x, xs, m, y, stream);
   if (m <= 16u) return launch_rows<XMX, 4, kAuxNontemporal>(w, x, xs, m, y, stream);
-  // 17..64 rows: one workgroup per group of 16 rows and tile, as long as that is a few
-  // workgroups a CU (m = 64, us against the tiled kernel: 4096x14336 40 / 46, X MXFP4 20 / 23,
-  // but 14336x4096 59 / 18 and 25 / 12).
+  // More rows on small weights: a workgroup per group of 16 rows and tile, as long as that is
+  // at most three workgroups a CU (us, here / 64 x 32 tiles below, X BF16 and X MXFP4:
+  // two a CU, m = 256 512x14336 18.4 / 35.4 and 10.2 / 17.0; three, m = 48 4096x14336
+  // 28.0 / 33.1 and 17.8 / 19.9; four, m = 128 2048x8192 23.2 / 18.4 and 13.1 / 11.6).
   const uint32_t cus = (uint32_t)device_cu_count();
-  if (m <= 64u && (m + 15u) / 16u * ((w.N + 15u) / 16u) <= 4u * cus) return launch_rows<XMX, XMX ? 1 : 4, 0>(w, x, xs, m, y, stream);
-  // Tiles of 64 x 64 where the large ones would leave half the GPU idle.  Such a launch is
-  // bound by the latency of a step, so K is dealt to parts of the workgroup, the more the
-  // fewer tiles there are (4096x14336, one part / several, us: X BF16 m = 128 66 / 47,
-  // m = 512 77 / 71 as 64 x 128; X MXFP4 m = 128 40 / 27 with 4 parts, m = 512 44 / 36 with 2).
+  if ((m + 15u) / 16u * ((w.N + 15u) / 16u) <= 3u * cus) return launch_rows<XMX, XMX ? 1 : 4, 0>(w, x, xs, m, y, stream);
+  // Small tiles where the large ones would leave half the GPU idle.  Such a launch is bound by
+  // the latency of a step, so K is dealt to parts of the workgroup, and where even 64 x 64
+  // tiles are no more than the CUs they are halved to 64 x 32 with four parts (us, 64 x 64 /
+  // 64 x 32: X BF16 m = 128 4096x14336 46.2 / 39.6, m = 128 4096x4096 14.1 / 11.9; X MXFP4
+  // 25.5 / 20.4 and 9.8 / 8.2; five parts 21.0 and 9.1).
   const uint32_t big = ((m + (XMX ? 255u : 127u)) / (XMX ? 256u : 128u)) * ((w.N + 255u) / 256u);
   const bool few = (m + 63u) / 64u * ((w.N + 63u) / 64u) <= cus;
   if constexpr (XMX) {
     if (big >= cus / 2u) return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
-    if (few) return launch_tile<true, 64, 64, 2, 2, 2, 4>(w, x, xs, m, y, stream);
+    if (few) return launch_tile<true, 64, 32, 2, 1, 2, 4>(w, x, xs, m, y, stream);
     return launch_tile<true, 64, 64, 2, 2, 2, 2>(w, x, xs, m, y, stream);
   } else {
     if (big >= cus / 2u) return launch_tile<false, 128, 256, 2, 4, 1>(w, x, xs, m, y, stream);
-    if (few) return launch_tile<false, 64, 64, 2, 2, 1, 2>(w, x, xs, m, y, stream);
+    if (few) return launch_tile<false, 64, 32, 2, 1, 1, 4>(w, x, xs, m, y, stream);
     return launch_tile<false, 64, 128, 2, 2, 1, 2>(w, x, xs, m, y, stream);
   }
 }
