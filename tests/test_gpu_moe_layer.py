@@ -267,6 +267,53 @@ def test_workspace_that_must_grow_during_capture(monkeypatch):
         assert torch.equal(y.view(torch.int16), want.view(torch.int16))
 
 
+def test_graph_keeps_its_scratch_when_later_calls_need_more():
+    log("a graph, then larger calls, then replays")
+    E, I, H = 6, 256, 256
+    L = Layer(32, "mxfp4", E, I, H)
+    xb, ld, _ = inputs(1, 20, H, E)
+    x = bits_to_dev(xb)
+    want = L.run(x, ld, 2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            y = L.run(x, ld, 2)
+    torch.cuda.synchronize()
+    big = Layer(33, "mxfp4", 16, 8192, 128)
+    xb2, ld2, _ = inputs(2, 64, 128, 16)
+    keep = []
+    for _ in range(3):
+        keep.append(big.run(bits_to_dev(xb2), ld2, 16))
+        keep.append(torch.full((40 << 20,), 7, dtype=torch.uint8, device="cuda"))
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+        assert all((k == 7).all() for k in keep[1::2])
+        assert torch.equal(keep[0].view(torch.int16), keep[-2].view(torch.int16))
+
+
+def test_calls_that_overlap_on_streams():
+    log("two streams at a time")
+    E, I, H = 6, 512, 512
+    layers = [Layer(34 + i, "mxfp4", E, I, H) for i in range(2)]
+    data = [inputs(40 + i, 48, H, E) for i in range(2)]
+    xs = [bits_to_dev(d[0]) for d in data]
+    want = [L.run(x, d[1], 3) for L, x, d in zip(layers, xs, data)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(layers[i].run(xs[i], data[i][1], 3))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y.view(torch.int16), want[i].view(torch.int16)) for y in got[i])
+
+
 def test_outputs_stay_inside_their_buffer_and_no_tokens():
     log("extent")
     E, I, H, T = 4, 128, 160, 3

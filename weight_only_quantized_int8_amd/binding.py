@@ -640,7 +640,7 @@ def moe_layer(gate, up, down, num_experts: int, x: torch.Tensor, logits: torch.T
     x:        bfloat16 [tokens, hidden]
     logits:   float32 or bfloat16 [tokens, num_experts], the router's scores before the softmax
     returns   bfloat16 [tokens, hidden]: x_resid + the weighted sum over the topk experts of each token.
-    Scratch comes from the device's cached workspace: calls that overlap on several streams would race.
+    Scratch is allocated for the call on the current stream, so calls may overlap on several streams.
     """
     mx = isinstance(gate, Mxfp4Weight)
     kind = Mxfp4Weight if mx else Int8Weight
@@ -663,9 +663,9 @@ def moe_layer(gate, up, down, num_experts: int, x: torch.Tensor, logits: torch.T
         y = torch.empty((T, hidden), dtype=torch.bfloat16, device=dev)
     _need_bf16(y, "y", T * hidden, dev)
     need = int8w_moe_workspace_bytes(T, topk, inner, hidden)
-    ws = _workspace(dev, need)
-    if ws is None:  # under graph capture: scratch of the graph's own
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    # A call's own: one kept for the device would be shared by streams, and freed when it grows
+    # under a graph that still writes to it.
+    ws = x.new_empty(need, dtype=torch.uint8)
     call = MoeCall(x.data_ptr(), logits.data_ptr(), x_resid.data_ptr() if x_resid is not None else None, y.data_ptr(),
                    T, topk, VALUES_F32 if logits.dtype == torch.float32 else VALUES_BF16, int(bool(renormalize)),
                    float(routed_scale))
