@@ -1,15 +1,16 @@
 // mxfp4_gemm.hip -- Y[m, N] = X[m, K] W^T with W in MXFP4 (mxfp4.h) and X in
 // BF16 (weight-only) or in MXFP4 too.  fp32 accumulation, one rounding to BF16.
 //
-// m <= 64: HBM-bound, the weight is streamed once for all rows
-//   (k_mx_rows): a workgroup owns 16 weight rows, its waves split K chunk by
-//   chunk and load weight codes, scales and the matching activations straight
-//   into matrix-core operands (rows_stream.h); no staging, no barrier until the
-//   waves' partial sums meet in LDS in wave order.
-// more rows: a tiled kernel (k_mx_tile) on bf16 MFMA (X BF16: codes are
-//   converted with their scale in registers, exactly) or on the scaled fp4 MFMA
-//   (both MXFP4: 16 x 16 x 128 products with a scale per 32 k in the
-//   instruction).
+// Three kernels, chosen by launch_any() below:
+//  k_mx_gemv  one row of BF16: vector ALUs, weight rows streamed along K (token_stream.h).
+//  k_mx_rows  few rows, or many on a small weight: a workgroup owns 16 weight rows and up
+//             to 16 rows of X, its waves share K piece by piece (rows_stream.h) and meet in
+//             LDS in wave order.
+//  k_mx_tile  more: LDS-tiled, on bf16 MFMA (X BF16: codes are converted with their scale
+//             in registers, exactly) or on the scaled fp4 MFMA (both MXFP4: 16 x 16 x 128
+//             products with a scale per 32 k in the instruction).
+// The first two are bound by HBM, once the weight is large enough to hide a launch; the
+// last by the matrix cores and by the LDS and conversions that feed them.
 #include <type_traits>
 #include <utility>
 
@@ -23,8 +24,9 @@ namespace {
 
 // ---- one row ----------------------------------------------------------------------------------
 
-// Waves share the pairs of weight rows; KS neighbouring waves share a pair's segments
-// where there are few pairs.  LDS: x.
+// y[n] = sum_k W[n, k] x[k].  Waves share the pairs of weight rows; KS neighbouring waves
+// share a pair's segments where there are few pairs.  LDS: x.  HBM-bound: 8192x28672, 125 MB
+// in 20.3 us, 6.2 TB/s; 4096x4096 3.9 us, of which an empty launch is the larger part.
 template <int KW, int U, int KS>
 __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *__restrict__ x, uint16_t *__restrict__ y) {
   typedef MxTok F;
@@ -167,6 +169,9 @@ __device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<Mx
 }
 
 // grid: (16-row weight tiles) x (groups of 16 rows of X), the groups of a tile side by side.
+// HBM-bound in what it moves, but a row of 14336 is 28 pieces, three or four a wave: the first
+// loads' latency and the waves' last sum are a large part of a call.  4096x14336, 31.8 MB: m = 16
+// 12.4 us; m = 8 with X in MXFP4 8.6 us.
 template <bool XMX, bool DW, int KS, int U, int NX, int AUX>
 __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
                                                      const uint8_t *__restrict__ xs, uint32_t m, uint32_t groups,
@@ -233,6 +238,9 @@ constexpr uint32_t kGroup = 4 * kChunk;  // k of one scale load: 16 scale bytes 
 // operands are copied to LDS by DMA, two stages; 16-byte pieces of a row are
 // XOR-swizzled so that the rows of an operand read fall into distinct banks.  A =
 // weight rows, B = X rows: a lane's four results are neighbours in Y.
+// 14336x4096: m = 512 X BF16 52 us, 1.16 PFLOP/s (the bf16 MFMA alone reaches 1.66); m = 2048
+// both MXFP4 80 us, 3.0 PFLOP/s (the fp4 MFMA alone 6.1): each product needs its operands
+// from LDS once per 16 x 16 x 128, and the loads of a step share the address unit.
 // Scales: loaded a group ahead, a lane per row and 16 bytes (block g of chunk c at
 // byte 4c + g), transposed to bytes 4g + c and put in LDS, so that a lane gets its
 // row's scales of block g for all four chunks as one dword whose byte c the scaled

