@@ -26,7 +26,7 @@ namespace {
 
 // y[n] = sum_k W[n, k] x[k].  Waves share the pairs of weight rows; KS neighbouring waves
 // share a pair's segments where there are few pairs.  LDS: x.  HBM-bound: 8192x28672, 125 MB
-// in 20.3 us, 6.2 TB/s; 4096x4096 3.9 us, of which an empty launch is the larger part.
+// in 21.3 us, 5.9 TB/s; 4096x4096, 8.9 MB, 4.1 us, mostly the start and end of a launch.
 template <int KW, int U, int KS>
 __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *__restrict__ x, uint16_t *__restrict__ y) {
   typedef MxTok F;
