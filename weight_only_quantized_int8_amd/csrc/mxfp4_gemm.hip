@@ -162,8 +162,8 @@ __device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<Mx
     wave_fence();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      acc[i] = mfma_mx(get_quarter(lds + 2048u + 1024u * i, lane), MxFmt<DW>::scale(p.x, 2 * hp + i, lane),
-                       get_quarter(lds + 1024u * i, lane), MxFmt<DW>::scale(p.w[0], 2 * hp + i, lane), acc[i]);
+      acc[i] = mfma_mx(get_quarter(lds + 2048u, i, lane), MxFmt<DW>::scale(p.x, 2 * hp + i, lane),
+                       get_quarter(lds, i, lane), MxFmt<DW>::scale(p.w[0], 2 * hp + i, lane), acc[i]);
     wave_fence();
   }
 }
@@ -265,7 +265,7 @@ struct MxTile {
 // piece index -> swizzled piece, rows of P 16-byte pieces
 template <uint32_t P>
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t c) {
-  if constexpr (P >= 16u) return c ^ (row & 15u);
+  if constexpr (P == 16u) return row_swizzle<16>(row, c);
   if constexpr (P == 8u) return c ^ (row & 7u);
   return c ^ ((row >> 1) & 3u);
 }
