@@ -18,10 +18,10 @@
 // Bound: HBM, each chosen expert's three matrices once.  An expert with more than
 // 16 tokens has several segments, whose further reads of its rows come from the caches
 // where they run together.  Measured, up / down: 13 tokens, 64 experts of 1024x2048 in 8 bits,
-// 6 each: 37.8 us (191 MB fetched, 5.1 TB/s) / 22.1 us (96 MB, 4.4 TB/s); 37 tokens, 8 experts of
-// 14336x4096 in MXFP4, 2 each: 101 us (503 MB, 5.0 TB/s) / 49 us (276 MB, 5.6 TB/s); one token,
-// 8 experts of 14336x4096 in 8 bits, 2 taken: 41.1 us (250 MB, 6.1 TB/s) / 23.2 us (125 MB,
-// 5.4 TB/s).  Route and sum take 4.6 to 5.3 us each, mostly the start and end of a launch.
+// 6 each: 38.8 us (191 MB fetched, 4.9 TB/s) / 22.2 us (96 MB, 4.3 TB/s); 37 tokens, 8 experts of
+// 14336x4096 in MXFP4, 2 each: 100 us (503 MB, 5.0 TB/s) / 49 us (276 MB, 5.7 TB/s); one token,
+// 8 experts of 14336x4096 in 8 bits, 2 taken: 41.2 us (250 MB, 6.1 TB/s) / 23.2 us (125 MB,
+// 5.4 TB/s).  Route and sum take 4.7 to 5.5 us each, mostly the start and end of a launch.
 //
 // h is kept in BF16 (the matrix cores' operand type): its relative rounding of at
 // most 2^-9 a value averages out over the inner sum to about the output's own BF16

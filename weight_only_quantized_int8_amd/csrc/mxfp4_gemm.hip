@@ -26,7 +26,7 @@ namespace {
 
 // y[n] = sum_k W[n, k] x[k].  Waves share the pairs of weight rows; KS neighbouring waves
 // share a pair's segments where there are few pairs.  LDS: x.  HBM-bound: 8192x28672, 125 MB
-// in 21.3 us, 5.9 TB/s; 4096x4096, 8.9 MB, 4.1 us, mostly the start and end of a launch.
+// in 21.0 us, 5.9 TB/s; 4096x4096, 8.9 MB, 4.1 us, mostly the start and end of a launch.
 template <int KW, int U, int KS>
 __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *__restrict__ x, uint16_t *__restrict__ y) {
   typedef MxTok F;
@@ -171,7 +171,7 @@ __device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<Mx
 // grid: (16-row weight tiles) x (groups of 16 rows of X), the groups of a tile side by side.
 // HBM-bound in what it moves, but a row of 14336 is 28 pieces, three or four a wave: the first
 // loads' latency and the waves' last sum are a large part of a call.  4096x14336, 31.8 MB: m = 16
-// 12.4 us; m = 8 with X in MXFP4 8.6 us.
+// 12.4 us; m = 8 with X in MXFP4 8.4 us.
 template <bool XMX, bool DW, int KS, int U, int NX, int AUX>
 __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
                                                      const uint8_t *__restrict__ xs, uint32_t m, uint32_t groups,
@@ -238,7 +238,7 @@ constexpr uint32_t kGroup = 4 * kChunk;  // k of one scale load: 16 scale bytes 
 // operands are copied to LDS by DMA, two stages; 16-byte pieces of a row are
 // XOR-swizzled so that the rows of an operand read fall into distinct banks.  A =
 // weight rows, B = X rows: a lane's four results are neighbours in Y.
-// 14336x4096: m = 512 X BF16 52 us, 1.16 PFLOP/s (the bf16 MFMA alone reaches 1.66); m = 2048
+// 14336x4096: m = 512 X BF16 51 us, 1.18 PFLOP/s (the bf16 MFMA alone reaches 1.66); m = 2048
 // both MXFP4 80 us, 3.0 PFLOP/s (the fp4 MFMA alone 6.1): each product needs its operands
 // from LDS once per 16 x 16 x 128, and the loads of a step share the address unit.
 // Scales: loaded a group ahead, a lane per row and 16 bytes (block g of chunk c at
