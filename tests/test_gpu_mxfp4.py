@@ -276,6 +276,28 @@ def test_offsets_past_32_bits():
     check(w.gemm_mx(weight(xc, xs))[:, -50:], ref, lim, "gemm_mx")
 
 
+def test_rows_past_the_threads_of_a_launch():
+    # 2^28 + 48 rows: 16 threads a row are more than a launch counts in 32 bits
+    log("longest weights")
+    n, k = (1 << 28) + 48, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(115, 125, (n, 1), generator=g, device="cuda", dtype=torch.uint8)
+    w = Mxfp4Weight(codes, scales)
+    for m in (1, 2, 5, 9):
+        xb = bits_of(np.random.default_rng(m).standard_normal((m, k)))
+        xc, xs = matrix(m, m, k)
+        for what, x, run in (("gemm", R.bf16_values(xb), lambda: w.gemm(bits_to_dev(xb))),
+                             ("gemm_mx", R.decode(xc, xs), lambda: w.gemm_mx(weight(xc, xs)))):
+            log(f"  m={m} {what}")
+            y = run()
+            for a in (0, n // 2, n - 50):  # the first rows, some in the middle, the last
+                ref, lim = R.product(x, R.decode(codes[a:a + 50].cpu().numpy(), scales[a:a + 50].cpu().numpy()))
+                check(y[:, a:a + 50], ref, lim, f"{what} m={m} rows from {a}")
+            del y
+
+
 def test_another_stream_and_a_graph():
     log("stream and graph")
     n, k, m = 512, 2048, 5

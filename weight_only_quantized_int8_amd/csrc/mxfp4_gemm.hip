@@ -594,8 +594,22 @@ hipError_t launch_tile(const MxView &w, const void *x, const uint8_t *xs, uint32
   return hipGetLastError();
 }
 
+// 256x256 tiles with both operands in MXFP4, 128x256 with X in BF16.
+template <bool XMX>
+hipError_t launch_large_tile(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  if constexpr (XMX)
+    return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
+  else
+    return launch_tile<false, 128, 256, 2, 4, 1>(w, x, xs, m, y, stream);
+}
+
+// A launch counts its threads in 32 bits and wraps without an error: the few-row form, 256 threads
+// for 16 weight rows, would leave out the rows of a weight beyond 2^28.
+bool rows_form_fits(uint32_t N) { return ((uint64_t)N + 15u) / 16u * 256u <= 0xFFFFFFFFull; }
+
 template <bool XMX>
 hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  if (!rows_form_fits(w.N)) return launch_large_tile<XMX>(w, x, xs, m, y, stream);
   if (XMX && m <= 16u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
   if (m <= 4u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
   if (m <= 8u) return launch_rows<XMX, 2, kAuxNontemporal>(w, x, xs, m, y, stream);
@@ -613,12 +627,11 @@ hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_
   // 25.5 / 20.4 and 9.8 / 8.2; five parts 21.0 and 9.1).
   const uint32_t big = ((m + (XMX ? 255u : 127u)) / (XMX ? 256u : 128u)) * ((w.N + 255u) / 256u);
   const bool few = (m + 63u) / 64u * ((w.N + 63u) / 64u) <= cus;
+  if (big >= cus / 2u) return launch_large_tile<XMX>(w, x, xs, m, y, stream);
   if constexpr (XMX) {
-    if (big >= cus / 2u) return launch_tile<true, 256, 256, 4, 2, 2>(w, x, xs, m, y, stream);
     if (few) return launch_tile<true, 64, 32, 2, 1, 2, 4>(w, x, xs, m, y, stream);
     return launch_tile<true, 64, 64, 2, 2, 2, 2>(w, x, xs, m, y, stream);
   } else {
-    if (big >= cus / 2u) return launch_tile<false, 128, 256, 2, 4, 1>(w, x, xs, m, y, stream);
     if (few) return launch_tile<false, 64, 32, 2, 1, 1, 4>(w, x, xs, m, y, stream);
     return launch_tile<false, 64, 128, 2, 2, 1, 2>(w, x, xs, m, y, stream);
   }
