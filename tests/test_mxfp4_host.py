@@ -151,3 +151,20 @@ def test_python_checks():
             Mxfp4Weight.quantize(bad)
     with pytest.raises(TypeError, match="three Int8Weight or three Mxfp4Weight"):
         moe_layer(None, None, None, 4, torch.zeros(1, 64, dtype=bf), torch.zeros(1, 4), 2)
+
+
+def host_matrix(rows, k):
+    """An Mxfp4Weight on the CPU: enough for the checks that come before a launch."""
+    codes, scales = torch.zeros(rows, k // 2, dtype=torch.uint8), torch.zeros(rows, k // 32, dtype=torch.uint8)
+    w = Mxfp4Weight.__new__(Mxfp4Weight)
+    w._set(codes, scales, rows, k, codes.device, codes.data_ptr(), scales.data_ptr())
+    return w
+
+
+@pytest.mark.parametrize("topk", [-(1 << 31), -1, 0, 5, 17, 1 << 20, (1 << 32) + 1])
+def test_a_wrong_topk_is_refused_before_it_sizes_the_scratch(topk, monkeypatch):
+    monkeypatch.setattr(B, "int8w_moe_workspace_bytes", lambda *a: pytest.fail(f"scratch sized for topk {topk}"))
+    gate, up, down = host_matrix(E * I, H), host_matrix(E * I, H), host_matrix(E * H, I)
+    with pytest.raises(B.Int8wError, match="topk") as e:
+        moe_layer(gate, up, down, E, torch.zeros(3, H, dtype=torch.bfloat16), torch.zeros(3, E), topk)
+    assert e.value.code == B.INT8W_ERR_SHAPE

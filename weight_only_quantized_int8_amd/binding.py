@@ -659,6 +659,8 @@ def moe_layer(gate, up, down, num_experts: int, x: torch.Tensor, logits: torch.T
         raise ValueError(f"logits must be a contiguous float32 or bfloat16 [{T}, {E}] tensor on the weights' GPU")
     if x_resid is not None:
         _need_bf16(x_resid, "x_resid", T * hidden, dev)
+    if not 1 <= topk <= min(E, MAX_MOE_TOPK):  # before it sizes the scratch
+        raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk} outside 1..min({E} experts, {MAX_MOE_TOPK})")
     if y is None:
         y = torch.empty((T, hidden), dtype=torch.bfloat16, device=dev)
     _need_bf16(y, "y", T * hidden, dev)
