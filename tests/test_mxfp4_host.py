@@ -168,3 +168,13 @@ def test_a_wrong_topk_is_refused_before_it_sizes_the_scratch(topk, monkeypatch):
     with pytest.raises(B.Int8wError, match="topk") as e:
         moe_layer(gate, up, down, E, torch.zeros(3, H, dtype=torch.bfloat16), torch.zeros(3, E), topk)
     assert e.value.code == B.INT8W_ERR_SHAPE
+
+
+def test_dequantizing_no_rows_gives_no_rows():
+    q = host_matrix(0, 64)
+    y = q.dequantize_to()
+    assert y.shape == (0, 64) and y.dtype == torch.bfloat16
+    out = torch.ones(5, dtype=torch.bfloat16)
+    assert q.dequantize_to(out) is out and (out == 1).all()
+    with pytest.raises(TypeError, match="bfloat16"):
+        q.dequantize_to(torch.ones(5))

@@ -600,6 +600,8 @@ class Mxfp4Weight:
             out = torch.empty((self.rows, self.k), dtype=torch.bfloat16, device=self.device)
         else:
             _need_bf16(out, "out", self.rows * self.k, self.device)
+        if self.rows == 0:  # as from quantize() on no rows; the C entry wants a matrix
+            return out
         _check(load_library().int8w_mxfp4_dequantize_to(self.desc, out.data_ptr(), _stream_of(self.device)))
         return out
 
