@@ -178,3 +178,14 @@ def test_dequantizing_no_rows_gives_no_rows():
     assert q.dequantize_to(out) is out and (out == 1).all()
     with pytest.raises(TypeError, match="bfloat16"):
         q.dequantize_to(torch.ones(5))
+
+
+def test_streams_without_the_private_torch_function(monkeypatch):
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: Stream(1000 + index))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    assert B._stream_of(torch.device("cuda", 1)) == 1001
+    assert B._stream_of(torch.device("cuda")) == 1003

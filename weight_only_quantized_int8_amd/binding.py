@@ -302,9 +302,13 @@ def int8_gemv_multi(descs, x: int, ys, stream: int) -> int:
 # ---- tensor-level wrapper -----------------------------------------------------------------------
 
 def _stream_of(device: torch.device) -> int:
-    # the handle alone: building a torch.cuda.Stream object took 1.8 us of an 8 us call
+    # The handle alone: building a torch.cuda.Stream object took 1.8 us of an 8 us call.  The
+    # function is not a public one, so a torch without it takes the public way.
     index = device.index if device.index is not None else torch.cuda.current_device()
-    return torch._C._cuda_getCurrentRawStream(index)
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _need_bf16(t: torch.Tensor, name: str, numel: int, device: torch.device) -> None:
