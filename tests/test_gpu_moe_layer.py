@@ -189,6 +189,17 @@ def test_long_rows_fall_back_from_the_one_token_form():
     check(L.run(bits_to_dev(xb), ld, 8), ref, lim, "layer")
 
 
+@pytest.mark.parametrize("I", [2048, 2080, 4096, 4128])
+@pytest.mark.parametrize("H", [96, 2048])
+def test_one_token_about_64_kib_of_lds(I, H):
+    # the chosen experts' inner products take 32, 64, 64 and 96 KiB, and the kernel has an array of its own
+    log(f"one token I={I} H={H}")
+    L = Layer(22, "mxfp4", 8, I, H)
+    xb, ld, l = inputs(3, 1, H, 8)
+    ref, lim = L.want(R.bf16_values(xb), l, 8)
+    check(L.run(bits_to_dev(xb), ld, 8), ref, lim, "layer")
+
+
 def test_experts_past_32_bits():
     # gate of 40 experts x 16384 x 8192: 5.4 GB of codes; the last experts are the ones taken
     log("large experts")

@@ -276,6 +276,17 @@ def test_offsets_past_32_bits():
     check(w.gemm_mx(weight(xc, xs))[:, -50:], ref, lim, "gemm_mx")
 
 
+@pytest.mark.parametrize("k", [30720, 30752, 32768, 32800])
+@pytest.mark.parametrize("n", [9, 1500, 2100])
+def test_one_row_about_64_kib_of_lds(n, k):
+    # X takes 60, 64, 64 and 68 KiB; the kernel's own array makes the second and third more than 64
+    log(f"one row n={n} k={k}")
+    codes, scales = matrix(n + k, n, k)
+    xb = bits_of(np.random.default_rng(k).standard_normal((1, k)))
+    ref, lim = R.product(R.bf16_values(xb), R.decode(codes, scales))
+    check(weight(codes, scales).gemm(bits_to_dev(xb)), ref, lim, f"{n}x{k}")
+
+
 def test_rows_past_the_threads_of_a_launch():
     # 2^28 + 48 rows: 16 threads a row are more than a launch counts in 32 bits
     log("longest weights")

@@ -29,6 +29,7 @@
 #include "rows_stream.h"
 #include "token_stream.h"
 #include "launch.h"
+#include "lds_allowance.h"
 
 namespace int8w {
 
@@ -468,10 +469,10 @@ bool one_token_fits(uint32_t H, uint32_t I, uint32_t topk) {
   return token_lds<F>(H) <= kLdsBytes - 1024u && (uint64_t)topk * token_lds<F>(I) <= kLdsBytes - 1024u;
 }
 
-// Dynamic LDS above 64 KiB has to be allowed once a kernel.
+// Once a kernel, for its `lds` dynamic bytes and `own` static ones.
 template <class K>
-hipError_t allow_lds(K kernel, uint32_t lds, bool &allowed) {
-  if (allowed || lds <= 64u << 10) return hipSuccess;
+hipError_t allow_lds(K kernel, uint32_t lds, uint32_t own, bool &allowed) {
+  if (allowed || !needs_lds_allowance(lds, own)) return hipSuccess;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)kLdsBytes - 1024);
   allowed = e == hipSuccess;
@@ -483,7 +484,7 @@ hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, c
                          uint32_t I, uint32_t lds, hipStream_t stream) {
   auto kern = k_moe1_up<F, KW, 2, R>;
   static bool allowed = false;
-  hipError_t e = allow_lds(kern, lds, allowed);
+  hipError_t e = allow_lds(kern, lds, 0, allowed);
   if (e != hipSuccess) return e;
   const uint32_t most = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW;
   kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits, m.logits_bf16, m.E, m.topk, m.renorm,
@@ -496,7 +497,7 @@ hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead 
                            uint32_t lds, hipStream_t stream) {
   auto kern = k_moe1_down<F, KW, 2, KS>;
   static bool allowed = false;
-  hipError_t e = allow_lds(kern, lds, allowed);
+  hipError_t e = allow_lds(kern, lds, sizeof(float[KW][2]), allowed);
   if (e != hipSuccess) return e;
   const uint32_t most = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
   kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(d, H, h, m.topk, head, m.resid, m.y);

@@ -17,6 +17,7 @@
 #include "rows_stream.h"
 #include "token_stream.h"
 #include "launch.h"
+#include "lds_allowance.h"
 
 namespace int8w {
 
@@ -114,8 +115,8 @@ template <int KW, int KS>
 hipError_t launch_gemv_one(const MxView &w, const uint16_t *x, uint16_t *y, hipStream_t stream) {
   auto kern = k_mx_gemv<KW, 2, KS>;
   const uint32_t lds = token_lds<MxTok>(w.K);
-  static bool allowed = false;  // dynamic LDS above 64 KiB, once a kernel
-  if (!allowed && lds > 64u << 10) {
+  static bool allowed = false;  // once a kernel
+  if (!allowed && needs_lds_allowance(lds, sizeof(float[KW][2]))) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, 159 << 10);
     if (e != hipSuccess) return e;
     allowed = true;
