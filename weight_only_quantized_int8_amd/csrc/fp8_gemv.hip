@@ -415,21 +415,12 @@ hipError_t launch_fp8_rx(const Fp8Cfg &c, const uint8_t *codes, const void *scal
   return hipGetLastError();
 }
 
-template <typename Kern>
-hipError_t lds_cap(Kern kern, bool &configured) {
-  if (configured) return hipSuccess;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-  if (e == hipSuccess) configured = true;
-  return e;
-}
-
 template <int SF, int W, int RP, bool TAIL>
 hipError_t launch_fp8_cfg(const Fp8Cfg &c, const uint8_t *codes, const void *scale, float single, uint32_t bs_log2,
                           const uint16_t *x, uint16_t *y, uint32_t N, uint32_t K, hipStream_t stream) {
-  static bool configured = false;
+  static LdsAllowance allowance;
   auto kern = k_fp8_gemv<SF, W, RP, kFp8LoadsPerBlock / RP, TAIL>;
-  hipError_t e = lds_cap(kern, configured);
+  hipError_t e = allow_lds(allowance, kern, 160 * 1024);
   if (e != hipSuccess) return e;
   const size_t lds = fp8_lds_bytes(c);
   hipLaunchKernelGGL(kern, dim3(c.blocks), dim3(64 * W), lds, stream, codes, scale, single, x, y, N, K, bs_log2,

@@ -845,13 +845,9 @@ template <int BM, int BN, int WGM, int WGN, int NP>
 hipError_t launch_tile_dma(const WeightView &w, const uint16_t *X, uint16_t *Y, uint32_t m, hipStream_t stream,
                            uint32_t parts = 1, void *ws = nullptr, bool tail = false) {
   auto kern = k_gemm_prefill_dma<BM, BN, WGM, WGN, NP>;
-  static bool configured = false;
-  if (!configured) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (e != hipSuccess) return e;
-    configured = true;
-  }
+  static LdsAllowance allowance;
+  const hipError_t e = allow_lds(allowance, kern, 160 * 1024);
+  if (e != hipSuccess) return e;
   const uint32_t mtiles = (m + BM - 1) / BM;
   const uint32_t ntiles = (w.N + BN - 1) / BN;
   const size_t lds = 3u * (BM + BN) * BK * 2u + BN * 16u * 2u * 2u;
@@ -902,13 +898,9 @@ hipError_t launch_tile_dma(const WeightView &w, const uint16_t *X, uint16_t *Y, 
 template <int BM, int BN, int WGM, int WGN, int NP>
 hipError_t launch_tile_ws(const WeightView &w, const uint16_t *X, uint16_t *Y, uint32_t m, hipStream_t stream) {
   auto kern = k_gemm_prefill_ws<BM, BN, WGM, WGN, NP>;
-  static bool configured = false;
-  if (!configured) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (e != hipSuccess) return e;
-    configured = true;
-  }
+  static LdsAllowance allowance;
+  const hipError_t e = allow_lds(allowance, kern, 160 * 1024);
+  if (e != hipSuccess) return e;
   const uint32_t mtiles = (m + BM - 1) / BM;
   const uint32_t ntiles = (w.N + BN - 1) / BN;
   const uint32_t nwork = mtiles * ntiles;
@@ -922,13 +914,9 @@ hipError_t launch_tile_ws(const WeightView &w, const uint16_t *X, uint16_t *Y, u
 template <int BM, int BN, int WGM, int WGN>
 hipError_t launch_tile(const WeightView &w, const uint16_t *X, uint16_t *Y, uint32_t m, hipStream_t stream) {
   auto kern = k_gemm_prefill<BM, BN, WGM, WGN>;
-  static bool configured = false;
-  if (!configured) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (e != hipSuccess) return e;
-    configured = true;
-  }
+  static LdsAllowance allowance;
+  const hipError_t e = allow_lds(allowance, kern, 160 * 1024);
+  if (e != hipSuccess) return e;
   const uint32_t mtiles = (m + BM - 1) / BM;
   const uint32_t ntiles = (w.N + BN - 1) / BN;
   const uint32_t nwork = mtiles * ntiles;

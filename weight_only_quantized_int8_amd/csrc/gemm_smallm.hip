@@ -378,13 +378,9 @@ size_t smallm_lds_bytes(uint32_t K, uint32_t gs) {
 template <int KS, int RT, int SPW, int NS, bool G32, int MT = 1, int XR = 16>
 hipError_t launch_sm(const WeightView &w, const uint16_t *X, uint16_t *Y, uint32_t m, hipStream_t stream) {
   auto kern = k_gemm_smallm<KS, RT, SPW, NS, G32, MT, XR>;
-  static bool configured = false;
-  if (!configured) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (e != hipSuccess) return e;
-    configured = true;
-  }
+  static LdsAllowance allowance;
+  const hipError_t e = allow_lds(allowance, kern, 160 * 1024);
+  if (e != hipSuccess) return e;
   const uint32_t blocks = (w.N + 16u * RT - 1u) / (16u * RT);
   const size_t lds = smallm_lds_bytes<KS, RT, SPW, NS, MT, XR>(w.K, w.gs);
   hipLaunchKernelGGL(kern, dim3(blocks), dim3(64 * KS), lds, stream,

@@ -1101,31 +1101,22 @@ __global__ __launch_bounds__(512) void k_moe_grouped(const uint8_t *__restrict__
   }
 }
 
-template <typename Kern>
-hipError_t raise_lds_cap(Kern kern, bool &configured, int bytes = 160 * 1024) {
-  if (configured) return hipSuccess;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) configured = true;
-  return e;
-}
-
 template <int EPI, int W, int RP, bool TAIL, int NS = 0, bool SBI = false>
 hipError_t launch_cfg(const GemvCfg &cfg, const GemvTargets &t, uint32_t K, uint32_t gs, const uint16_t *xg,
                       const uint16_t *up, const uint16_t *resid, hipStream_t stream) {
-  static bool configured = false;  // raise the dynamic-LDS cap once per instantiation
+  static LdsAllowance allowance;  // one per instantiation
   const uint32_t gs_log2 = (uint32_t)__builtin_ctz(gs);
   const size_t lds = NS ? 0u : lds_bytes(cfg, gs);  // the register-resident form uses no LDS
   if (t.count == 1) {
     auto kern = k_gemv<NS, EPI, W, RP, kLoadsPerBlock / RP, TAIL, SBI>;
-    hipError_t e = raise_lds_cap(kern, configured);
+    hipError_t e = allow_lds(allowance, kern, 160 * 1024);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(cfg.blocks), dim3(64 * W), lds, stream, t.codes[0], t.scales[0], t.biases[0], xg,
                        up, resid, t.y[0], t.n[0], K, gs_log2, cfg.ct, cfg.max_rows);
   } else {
-    static bool configured_multi = false;
+    static LdsAllowance allowance_multi;
     auto kern = k_gemv_multi<NS, W, RP, kLoadsPerBlock / RP, TAIL, SBI>;
-    hipError_t e = raise_lds_cap(kern, configured_multi);
+    hipError_t e = allow_lds(allowance_multi, kern, 160 * 1024);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(cfg.blocks), dim3(64 * W), lds, stream, t, xg, K, gs_log2, cfg.ct, cfg.max_rows);
   }
@@ -1292,9 +1283,9 @@ hipError_t launch_gemv_list(const WeightView *w, uint16_t *const *y, uint32_t co
 template <int W, int RP, bool TAIL, int NS = 0, bool SBI = false>
 hipError_t launch_moe_cfg(const GemvCfg &cfg, const WeightView &w, uint32_t E, const uint16_t *x, uint32_t x_rows,
                           const uint32_t *ids, uint32_t topk, uint32_t slots, uint16_t *y, hipStream_t stream) {
-  static bool configured = false;
+  static LdsAllowance allowance;
   auto kern = k_moe_gemv<NS, W, RP, kLoadsPerBlock / RP, TAIL, SBI>;
-  hipError_t e = raise_lds_cap(kern, configured);
+  hipError_t e = allow_lds(allowance, kern, 160 * 1024);
   if (e != hipSuccess) return e;
   const uint32_t gs_log2 = (uint32_t)__builtin_ctz(w.gs);
   const size_t lds = NS ? 0u : lds_bytes(cfg, w.gs);
@@ -1387,9 +1378,9 @@ namespace {
 
 template <int MR>
 hipError_t launch_rows_lds_cfg(const WeightView &w, const uint16_t *X, uint16_t *Y, hipStream_t stream) {
-  static bool configured = false;
+  static LdsAllowance allowance;
   auto kern = k_gemv_rows_lds<MR>;
-  hipError_t e = raise_lds_cap(kern, configured);
+  hipError_t e = allow_lds(allowance, kern, 160 * 1024);
   if (e != hipSuccess) return e;
   uint32_t blocks = (uint32_t)device_cu_count();
   const uint32_t need = (w.N + 15u) / 16u;  // no workgroup without rows
@@ -1418,11 +1409,11 @@ namespace {
 template <int NS>
 hipError_t launch_moe_grouped(const WeightView &w, uint32_t E, const uint16_t *x, uint32_t x_rows,
                               const uint32_t *ids, uint32_t topk, uint32_t slots, uint16_t *y, hipStream_t stream) {
-  static bool configured = false;
+  static LdsAllowance allowance;
   auto kern = k_moe_grouped<NS>;
   const size_t lds = (size_t)kGrpC * NS * (256u * 16u + 64u * 4u);
   // the kernel also holds a few KiB of static LDS: ask for the dynamic part only
-  hipError_t e = raise_lds_cap(kern, configured, (int)lds);
+  hipError_t e = allow_lds(allowance, kern, (int)lds);
   if (e != hipSuccess) return e;
   const uint32_t blocks = 2u * (uint32_t)device_cu_count();  // two 8-wave workgroups per CU
   hipLaunchKernelGGL(kern, dim3(blocks), dim3(512), lds, stream, reinterpret_cast<const uint8_t *>(w.packed),

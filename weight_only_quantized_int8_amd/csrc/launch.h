@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "int8w.h"
+#include "lds_allowance.h"
 
 namespace int8w {
 
@@ -19,6 +20,17 @@ struct WeightView {
 
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
+
+// Lets `kernel` take `bytes` of dynamic LDS on the current device, once on each.
+template <class Kern>
+hipError_t allow_lds(LdsAllowance &allowance, Kern kernel, int bytes) {
+  int device = 0;
+  const hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  return allowance.once(device, hipSuccess, [&] {
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
 
 hipError_t launch_dequant(const WeightView &w, uint16_t *out, hipStream_t stream);
 

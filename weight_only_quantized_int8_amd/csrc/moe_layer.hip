@@ -29,7 +29,6 @@
 #include "rows_stream.h"
 #include "token_stream.h"
 #include "launch.h"
-#include "lds_allowance.h"
 
 namespace int8w {
 
@@ -469,23 +468,15 @@ bool one_token_fits(uint32_t H, uint32_t I, uint32_t topk) {
   return token_lds<F>(H) <= kLdsBytes - 1024u && (uint64_t)topk * token_lds<F>(I) <= kLdsBytes - 1024u;
 }
 
-// Once a kernel, for its `lds` dynamic bytes and `own` static ones.
-template <class K>
-hipError_t allow_lds(K kernel, uint32_t lds, uint32_t own, bool &allowed) {
-  if (allowed || !needs_lds_allowance(lds, own)) return hipSuccess;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)kLdsBytes - 1024);
-  allowed = e == hipSuccess;
-  return e;
-}
-
 template <class F, int KW, int R>
 hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, const MoeArgs &m, MoeHead *head, uint16_t *h,
                          uint32_t I, uint32_t lds, hipStream_t stream) {
   auto kern = k_moe1_up<F, KW, 2, R>;
-  static bool allowed = false;
-  hipError_t e = allow_lds(kern, lds, 0, allowed);
-  if (e != hipSuccess) return e;
+  static LdsAllowance allowance;
+  if (needs_lds_allowance(lds, 0)) {
+    const hipError_t e = allow_lds(allowance, kern, (int)kLdsBytes - 1024);
+    if (e != hipSuccess) return e;
+  }
   const uint32_t most = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW;
   kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits, m.logits_bf16, m.E, m.topk, m.renorm,
                                                            m.scale, head, h);
@@ -496,9 +487,11 @@ template <class F, int KW, int KS>
 hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead *head, const uint16_t *h, uint32_t H,
                            uint32_t lds, hipStream_t stream) {
   auto kern = k_moe1_down<F, KW, 2, KS>;
-  static bool allowed = false;
-  hipError_t e = allow_lds(kern, lds, sizeof(float[KW][2]), allowed);
-  if (e != hipSuccess) return e;
+  static LdsAllowance allowance;
+  if (needs_lds_allowance(lds, sizeof(float[KW][2]))) {
+    const hipError_t e = allow_lds(allowance, kern, (int)kLdsBytes - 1024);
+    if (e != hipSuccess) return e;
+  }
   const uint32_t most = (uint32_t)device_cu_count(), units = KW / KS, want = ((H + 1u) / 2u + units - 1u) / units;
   kern<<<KS > 1 || want < most ? want : most, 64 * KW, lds, stream>>>(d, H, h, m.topk, head, m.resid, m.y);
   return hipGetLastError();

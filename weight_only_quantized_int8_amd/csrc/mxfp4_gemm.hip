@@ -17,7 +17,6 @@
 #include "rows_stream.h"
 #include "token_stream.h"
 #include "launch.h"
-#include "lds_allowance.h"
 
 namespace int8w {
 
@@ -115,11 +114,10 @@ template <int KW, int KS>
 hipError_t launch_gemv_one(const MxView &w, const uint16_t *x, uint16_t *y, hipStream_t stream) {
   auto kern = k_mx_gemv<KW, 2, KS>;
   const uint32_t lds = token_lds<MxTok>(w.K);
-  static bool allowed = false;  // once a kernel
-  if (!allowed && needs_lds_allowance(lds, sizeof(float[KW][2]))) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, 159 << 10);
+  static LdsAllowance allowance;
+  if (needs_lds_allowance(lds, sizeof(float[KW][2]))) {
+    const hipError_t e = allow_lds(allowance, kern, 159 << 10);
     if (e != hipSuccess) return e;
-    allowed = true;
   }
   const uint32_t units = KW / KS, want = ((w.N + 1u) / 2u + units - 1u) / units;
   const uint32_t most = (uint32_t)device_cu_count();
@@ -584,13 +582,9 @@ template <bool XMX, int BM, int BN, int WM, int WN, int CH, int KG = 1>
 hipError_t launch_tile(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
   using S = MxTile<XMX, BM, BN, WM, WN, CH, KG>;
   const uint32_t mt = (m + BM - 1u) / BM, nt = (w.N + BN - 1u) / BN;
-  static bool allowed = false;
-  if (!allowed) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<XMX, BM, BN, WM, WN, CH, KG>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS);
-    if (e != hipSuccess) return e;
-    allowed = true;
-  }
+  static LdsAllowance allowance;
+  const hipError_t e = allow_lds(allowance, &k_mx_tile<XMX, BM, BN, WM, WN, CH, KG>, (int)S::LDS);
+  if (e != hipSuccess) return e;
   k_mx_tile<XMX, BM, BN, WM, WN, CH, KG><<<mt * nt, S::kThreads * KG, S::LDS, stream>>>(w, (const uint8_t *)x, xs, m, y, mt);
   return hipGetLastError();
 }
