@@ -220,14 +220,18 @@ int int8w_mxfp4_quantize(const void *x, uint32_t x_format, uint32_t rows, uint32
 int int8w_mxfp4_dequantize_to(const int8w_mxfp4 *w, uint16_t *out, uint64_t stream);
 
 /* mxfp4_gemm: Y = X W^T with BF16 X [m, k] and Y [m, rows], row-major:
- * Y[i,n] = RNE_bf16(sum_j w[n,j] X[i,j]), exact products, accumulated in fp32.  Any
- * m (m = 1: decode); m = 0 is a no-op.  The sum's order depends on m alone for a
+ * Y[i,n] = RNE_bf16(sum_j w[n,j] X[i,j]), exact products, accumulated in fp32.  w[n,j]
+ * enters as the BF16 value that mxfp4_dequantize_to gives: values at or above 2^128
+ * (scale byte 253 with magnitudes 4 and 6, 254 with 2 and up) are infinities, also
+ * against an X so small that the product would be finite, and NaN against an X of 0.
+ * Any m (m = 1: decode); m = 0 is a no-op.  The sum's order depends on m alone for a
  * given weight shape: results are deterministic.  INT8W_ERR_SHAPE also when
  * m * k or m * rows exceeds 2^32 - 1. */
 int int8w_mxfp4_gemm(const int8w_mxfp4 *w, const uint16_t *x, uint16_t *y, uint32_t m, uint64_t stream);
 
 /* mxfp4_gemm_mx: the same with X in MXFP4 as well (x->k == w->k; x->rows is m),
- * e.g. from mxfp4_quantize: the products run on the 4-bit matrix cores. */
+ * e.g. from mxfp4_quantize: the products run on the 4-bit matrix cores, which apply the
+ * scales to the products, so scale bytes 253 and 254 make no infinities here. */
 int int8w_mxfp4_gemm_mx(const int8w_mxfp4 *w, const int8w_mxfp4 *x, uint16_t *y, uint64_t stream);
 
 /* ---- A whole mixture-of-experts layer for a few tokens.  For token t with router
@@ -238,7 +242,8 @@ int int8w_mxfp4_gemm_mx(const int8w_mxfp4 *w, const int8w_mxfp4 *x, uint16_t *y,
  *   r_j = routed_scale * p_j, or routed_scale * p_j / (sum of the taken p) with
  *   renormalize; an expert whose r_j is zero is not run;
  *   y[t] = RNE_bf16( x_resid[t] + sum_j r_j Wd_j (silu(Wg_j x_t) * (Wu_j x_t)) ).
- * A token whose logits hold a NaN or +inf gets NaN outputs.
+ * A token whose logits hold a NaN or +inf gets NaN outputs.  MXFP4 experts' values at
+ * or above 2^128 are infinities, as in mxfp4_gemm.
  *   gate, up  [num_experts * inner, hidden], down [num_experts * hidden, inner]:
  *             experts stacked along rows, expert e first row e * inner (e * hidden);
  *   x         BF16 [tokens, hidden], 16-byte aligned;

@@ -189,6 +189,40 @@ def test_long_rows_fall_back_from_the_one_token_form():
     check(L.run(bits_to_dev(xb), ld, 8), ref, lim, "layer")
 
 
+@pytest.mark.parametrize("T", [1, 5, 24])
+def test_expert_values_about_2_to_the_128(T):
+    # the first block of every row under scale byte 254, against activations of about 2^-130: finite below 2^128;
+    # expert 2's up projection has a value of 2^128 there, which is an infinity
+    log(f"largest scales T={T}")
+    E, I, H = 4, 128, 128
+    rng = np.random.default_rng(50)
+    gpu, ref = [], []
+    for n, k, big in ((E * I, H, True), (E * I, H, True), (E * H, I, False)):
+        q = rng.integers(0, 16, (n, k))
+        scales = rng.integers(117, 122, (n, k // 32)).astype(np.uint8)
+        if big:
+            q[:, :32] = (q[:, :32] & 8) | rng.integers(1, 4, (n, 32))  # 0.5, 1, 1.5: up to 1.5 * 2^127
+            scales[:, 0] = 254
+        if len(gpu) == 1:
+            q[2 * I + 5, 7] = 4  # 2 * 2^127
+        codes = (q[:, 0::2] | q[:, 1::2] << 4).astype(np.uint8)
+        gpu.append(Mxfp4Weight(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()))
+        ref.append(R.decode(codes, scales).reshape(E, n // E, k))
+    x = rng.standard_normal((T, H))
+    x[:, :32] *= 2.0 ** -130
+    xb = bits_of(x)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[:, 2] = -np.inf
+    for infinite in ([], [T // 2]):
+        l[infinite, 2] = 9.0
+        y = moe_layer(*gpu, E, bits_to_dev(xb), torch.from_numpy(l).cuda(), 2)
+        want, lim = R.moe(R.bf16_values(xb), *ref, [np.abs(w) for w in ref], l.astype(np.float64), 2)
+        y = R.bf16_values(dev_to_bits(y))
+        keep = np.array([t not in infinite for t in range(T)])
+        assert (np.abs(y - want)[keep] <= lim[keep]).all()
+        assert not np.isfinite(y[~keep]).any()
+
+
 @pytest.mark.parametrize("I", [2048, 2080, 4096, 4128])
 @pytest.mark.parametrize("H", [96, 2048])
 def test_one_token_about_64_kib_of_lds(I, H):

@@ -203,6 +203,45 @@ def test_extreme_scales_and_activations(m):
     check(weight(codes, scales).gemm(bits_to_dev(xb)), ref, lim, "large scales")
 
 
+def largest_scales(seed, n, k):
+    """Scale bytes 253 and 254 with magnitudes below 2^128 in the even rows, any in the odd ones."""
+    rng = np.random.default_rng(seed)
+    scales = rng.integers(253, 255, (n, k // 32)).astype(np.uint8)
+    q = rng.integers(0, 8, (n, k))
+    most = np.where(np.repeat(scales, 32, 1) == 253, 6, 4)  # codes of 4 and of 2: the first that are not below
+    q = np.where((np.arange(n) % 2 == 0)[:, None], q % most, q) + 8 * rng.integers(0, 2, (n, k))
+    return (q[:, 0::2] | q[:, 1::2] << 4).astype(np.uint8), scales
+
+
+@pytest.mark.parametrize("m", [1, 2, 7, 16, 30, 100, 600])
+def test_values_about_2_to_the_128(m):
+    # with X in BF16 a value from 2^128 on is infinity, as fp32 and dequantize_to have it; with X in MXFP4 it is exact
+    log(f"largest scales m={m}")
+    n, k = 120, 320
+    codes, scales = largest_scales(41, n, k)
+    w, exact = weight(codes, scales), R.decode(codes, scales)
+    W = np.where(np.abs(exact) >= 2.0 ** 128, np.copysign(np.inf, exact), exact)
+    assert np.isfinite(W[::2]).all() and np.isinf(W[1::2]).any(1).all()
+    assert np.array_equal(R.bf16_values(dev_to_bits(w.dequantize_to())), W)
+    x = np.random.default_rng(m).standard_normal((m, k)) * 2.0 ** -40
+    x[m // 2, ::3] = 0.0  # 0 times infinity
+    x[0] = np.abs(x[0]) * np.where(exact[1] < 0, -1, 1)  # row 1: infinities of one sign
+    xb = bits_of(x)
+    X = R.bf16_values(xb)
+    with np.errstate(invalid="ignore"):
+        inf = np.array([[np.sum(a * b) for b in W] for a in X])
+    ref, lim = R.product(X, np.where(np.isinf(W), 0.0, W))
+    y = R.bf16_values(dev_to_bits(w.gemm(bits_to_dev(xb))))
+    assert np.array_equal(np.isnan(y), np.isnan(inf)) and np.array_equal(np.isinf(y), np.isinf(inf))
+    assert np.array_equal(np.sign(y[np.isinf(y)]), np.sign(inf[np.isinf(inf)]))
+    ok = np.isfinite(inf)
+    assert ok[:, ::2].all() and np.isnan(inf).any() and (m == 1 or np.isinf(inf).any())
+    assert (np.abs(y - ref)[ok] <= lim[ok]).all()
+    xc, xs = matrix(42, m, k, 80, 90)
+    ref, lim = R.product(R.decode(xc, xs), exact)
+    check(w.gemm_mx(weight(xc, xs)), ref, lim, "gemm_mx")
+
+
 @pytest.mark.parametrize("m", [1, 2, 12, 30, 100])
 def test_scales_of_any_alignment(m):
     log(f"unaligned scales m={m}")

@@ -19,7 +19,9 @@ constexpr uint32_t kMxBlock = 32;  // values a scale
 __device__ __forceinline__ float mx_scale_f32(uint32_t s) { return __uint_as_float(s << 23); }
 
 // Eight codes (one dword, element 0 in the low half of byte 0) -> eight BF16
-// values with the scale applied.  Exact: a magnitude has two significant bits.
+// values with the scale applied.  Exact below 2^128, since a magnitude has two significant
+// bits; at and above it (scale byte 253 with magnitudes 4 and 6, 254 with 2 and up), where
+// fp32 ends too, infinity.
 __device__ __forceinline__ uint4 mx_to_bf16x8(uint32_t q, float s) {
   const bf16x2 a = __builtin_bit_cast(bf16x2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
   const bf16x2 b = __builtin_bit_cast(bf16x2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));

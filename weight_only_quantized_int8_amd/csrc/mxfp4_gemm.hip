@@ -7,7 +7,7 @@
 //             to 16 rows of X, its waves share K piece by piece (rows_stream.h) and meet in
 //             LDS in wave order.
 //  k_mx_tile  more: LDS-tiled, on bf16 MFMA (X BF16: codes are converted with their scale
-//             in registers, exactly) or on the scaled fp4 MFMA (both MXFP4: 16 x 16 x 128
+//             in registers, exactly below 2^128) or on the scaled fp4 MFMA (both MXFP4: 16 x 16 x 128
 //             products with a scale per 32 k in the instruction).
 // The first two are bound by HBM, once the weight is large enough to hide a launch; the
 // last by the matrix cores and by the LDS and conversions that feed them.

@@ -20,7 +20,7 @@
 //    a lane permute.
 //  * MXFP4: lane group g = l/16 takes block g of the quarter's four (32 codes, 16
 //    bytes, one scale); MFMA f of four takes its codes 8f .. 8f+7, converted to BF16
-//    with the scale applied (exact).
+//    with the scale applied (exact below 2^128).
 //  * 8-bit affine: sum_k (q s + b) x = s sum q x + b sum x per run of one group: codes
 //    enter the MFMA as exact BF16 integers, sum x comes from an MFMA against ones
 //    (shared by the tiles), s and b are applied to the fp32 results.  Group size 64 and

@@ -6,7 +6,7 @@
 // run, and a ring of segments stays in flight across rows.  The matrix-core form
 // (rows_stream.h) would compute 16 columns to use one and change lanes through LDS for
 // each 64 bytes; here a code costs a fraction of a conversion and of a two-way dot product:
-//  * MXFP4: half a v_cvt_scalef32_pk_bf16_fp4 (scale applied, exact) and half a v_dot2.
+//  * MXFP4: half a v_cvt_scalef32_pk_bf16_fp4 (scale applied, exact below 2^128) and half a v_dot2.
 //  * 8-bit affine: codes to BF16 integers (exact), half a v_dot2; the run's
 //    s * sum q x + b * sum x once, sum x from LDS.
 // The activations sit in LDS as BF16, their 16-byte pieces in planes so that a wave's
