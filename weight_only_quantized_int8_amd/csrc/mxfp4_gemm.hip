@@ -572,8 +572,10 @@ hipError_t launch_rows_dw(const MxView &w, const void *x, const uint8_t *xs, uin
   return hipGetLastError();
 }
 
+// NX: loads that 4 NX rows of BF16 take.
 template <bool XMX, int NX, int AUX>
 hipError_t launch_rows(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
+  static_assert(!XMX || NX == 1, "16 rows in MXFP4 are one tile");
   const bool dw = mx_dwords(w) && (!XMX || (reinterpret_cast<uintptr_t>(xs) & 3u) == 0);
   return dw ? launch_rows_dw<XMX, true, NX, AUX>(w, x, xs, m, y, stream) : launch_rows_dw<XMX, false, NX, AUX>(w, x, xs, m, y, stream);
 }
@@ -605,10 +607,13 @@ bool rows_form_fits(uint32_t N) { return ((uint64_t)N + 15u) / 16u * 256u <= 0xF
 template <bool XMX>
 hipError_t launch_any(const MxView &w, const void *x, const uint8_t *xs, uint32_t m, uint16_t *y, hipStream_t stream) {
   if (!rows_form_fits(w.N)) return launch_large_tile<XMX>(w, x, xs, m, y, stream);
-  if (XMX && m <= 16u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
-  if (m <= 4u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
-  if (m <= 8u) return launch_rows<XMX, 2, kAuxNontemporal>(w, x, xs, m, y, stream);
-  if (m <= 16u) return launch_rows<XMX, 4, kAuxNontemporal>(w, x, xs, m, y, stream);
+  if constexpr (XMX) {
+    if (m <= 16u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
+  } else {
+    if (m <= 4u) return launch_rows<XMX, 1, kAuxNontemporal>(w, x, xs, m, y, stream);
+    if (m <= 8u) return launch_rows<XMX, 2, kAuxNontemporal>(w, x, xs, m, y, stream);
+    if (m <= 16u) return launch_rows<XMX, 4, kAuxNontemporal>(w, x, xs, m, y, stream);
+  }
   // More rows on small weights: a workgroup per group of 16 rows and tile, as long as that is
   // at most three workgroups a CU (us, here / 64 x 32 tiles below, X BF16 and X MXFP4:
   // two a CU, m = 256 512x14336 18.4 / 35.4 and 10.2 / 17.0; three, m = 48 4096x14336
