@@ -153,16 +153,16 @@ struct XMx {
 };
 
 template <bool DW>
-__device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<MxFmt<DW>, XMx<DW>, 1> &p, uint8_t *lds, uint32_t lane) {
+__device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<MxFmt<DW>, XMx<DW>> &p, uint8_t *lds, uint32_t lane) {
 #pragma unroll
   for (int hp = 0; hp < 2; ++hp) {
-    put_lines(lds, p.w[0].q, hp, lane);
+    put_lines(lds, p.w.q, hp, lane);
     put_lines(lds + 2048u, p.x.q, hp, lane);
     wave_fence();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       acc[i] = mfma_mx(get_quarter(lds + 2048u, i, lane), MxFmt<DW>::scale(p.x, 2 * hp + i, lane),
-                       get_quarter(lds, i, lane), MxFmt<DW>::scale(p.w[0], 2 * hp + i, lane), acc[i]);
+                       get_quarter(lds, i, lane), MxFmt<DW>::scale(p.w, 2 * hp + i, lane), acc[i]);
     wave_fence();
   }
 }
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
                                                      uint16_t *__restrict__ y) {
   typedef MxFmt<DW> F;
   typedef std::conditional_t<XMX, XMx<DW>, XBf16<F, NX>> X;
-  constexpr uint32_t kWaveLds = stream_lds<X, 1>();
+  constexpr uint32_t kWaveLds = stream_lds<X>();
   __shared__ __attribute__((aligned(16))) uint8_t lds[KS * kWaveLds];
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = w.K;
   const uint32_t n0 = 16u * (blockIdx.x / groups), m0 = 16u * (blockIdx.x % groups);
@@ -191,30 +191,30 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__res
                [&](uint32_t i) { return i < rows ? i * K * 2u : kOutOfRange; });
   };
   const X xr = make();
-  Pieces<F, X, 1> r[U];
+  Pieces<F, X> r[U];
   const uint32_t np = (K + F::kPiece - 1u) / F::kPiece;
-  auto load = [&](Pieces<F, X, 1> &b, uint32_t c) {
+  auto load = [&](Pieces<F, X> &b, uint32_t c) {
     xr.load(b.x, c, lane);
-    F::template load<AUX>(b.w[0], t, w, c, lane);
+    F::template load<AUX>(b.w, t, w, c, lane);
     keep_order();
   };
-  f32x4 acc[1][2] = {{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}};
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
   for (int u = 0; u < U; ++u) load(r[u], wave + KS * u);
   for (uint32_t c = wave; c < np; c += KS * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if constexpr (XMX)
-        stream_piece_mx<DW>(acc[0], r[u], lds + wave * kWaveLds, lane);
+        stream_piece_mx<DW>(acc, r[u], lds + wave * kWaveLds, lane);
       else
-        stream_piece<F, X, 1>(acc, r[u], xr, lds + wave * kWaveLds, lane);
+        stream_piece<F, X>(acc, r[u], xr, lds + wave * kWaveLds, lane);
       keep_order();
       load(r[u], c + KS * (U + u));  // past the row's end: zeros, no traffic
     }
   }
   __syncthreads();
   float *red = reinterpret_cast<float *>(lds);  // the partial sums reuse the streams' LDS
-  reinterpret_cast<f32x4 *>(red)[wave * 64u + lane] = acc[0][0] + acc[0][1];
+  reinterpret_cast<f32x4 *>(red)[wave * 64u + lane] = acc[0] + acc[1];
   __syncthreads();
   for (uint32_t o = threadIdx.x; o < 16u * rows; o += 64u * KS) {
     const uint32_t row = o & 15u, tok = o >> 4;

@@ -338,28 +338,27 @@ struct XBf16 {
   }
 };
 
-// LDS bytes of one wave: two quarters of RT tiles and of the activations.
-template <class X, int RT>
+// LDS bytes of one wave: two quarters of its tile and of the activations.
+template <class X>
 constexpr uint32_t stream_lds() {
-  return 2u * (1024u * RT + X::kLds);
+  return 2u * (1024u + X::kLds);
 }
 
-template <class F, class X, int RT>
+template <class F, class X>
 struct Pieces {
-  typename F::Piece w[RT];
+  typename F::Piece w;
   typename X::Piece x;
 };
 
-// acc[t][0] + acc[t][1] += A B^T of one piece: the two quarters of a line have sums of their
-// own, so that neither waits for the other's products.
-template <class F, class X, int RT>
-__device__ __forceinline__ void stream_piece(f32x4 (&acc)[RT][2], const Pieces<F, X, RT> &p, const X &X_, uint8_t *lds,
+// acc[0] + acc[1] += A B^T of one piece: the two quarters of a line have sums of their own, so
+// that neither waits for the other's products.
+template <class F, class X>
+__device__ __forceinline__ void stream_piece(f32x4 (&acc)[2], const Pieces<F, X> &p, const X &X_, uint8_t *lds,
                                              uint32_t lane) {
-  uint8_t *const xl = lds + 2048u * RT;
+  uint8_t *const xl = lds + 2048u;
 #pragma unroll
   for (int hp = 0; hp < 2; ++hp) {
-#pragma unroll
-    for (int t = 0; t < RT; ++t) put_lines(lds + 2048u * t, p.w[t].q, hp, lane);
+    put_lines(lds, p.w.q, hp, lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) X_.put(xl + i * X::kLds, p.x, 2 * hp + i, lane);
     wave_fence();
@@ -369,9 +368,7 @@ __device__ __forceinline__ void stream_piece(f32x4 (&acc)[RT][2], const Pieces<F
       X::get(x, xl + i * X::kLds, lane);
       typename F::Sums S;
       F::sums(S, x);
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        F::mac(acc[t][i], weight_operand<F>(lds + 2048u * t, i, lane), p.w[t], 2 * hp + i, x, S, lane);
+      F::mac(acc[i], weight_operand<F>(lds, i, lane), p.w, 2 * hp + i, x, S, lane);
     }
     wave_fence();
   }
