@@ -38,6 +38,11 @@ __device__ __forceinline__ float code_f32(uint32_t word, int b) {
   return (float)((word >> (8 * b)) & 0xFFu);
 }
 
+// Codes 2i and 2i + 1 of a code word as a pair of BF16 integers (exact).
+__device__ __forceinline__ uint32_t int8_pair_bf16(uint32_t word, int i) {
+  return __builtin_amdgcn_perm(__float_as_uint(code_f32(word, 2 * i + 1)), __float_as_uint(code_f32(word, 2 * i)), 0x07060302u);
+}
+
 // silu(g) * u in fp32; silu(g) = g / (1 + e^-g), with the hardware
 // reciprocal of 1 + e^-g (within 1 ulp) instead of an IEEE division, whose
 // scale-and-fixup sequence cost about nine more operations per value.  For
@@ -71,6 +76,10 @@ __device__ __forceinline__ void store_nt(uint4 v, uint4 *p) {
   u32x4 t = {v.x, v.y, v.z, v.w};
   __builtin_nontemporal_store(t, reinterpret_cast<u32x4 *>(p));
 }
+
+// Loads are waited for in the order of their issue, so a ring of pieces in flight only
+// works if the compiler keeps each piece's loads together and behind the ones before.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---- buffer loads.  A raw buffer resource bounds every access: a load whose
 // byte offset (plus its size) exceeds num_records returns zero and touches no

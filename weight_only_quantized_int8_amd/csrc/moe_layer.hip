@@ -304,7 +304,7 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typena
     const uint32_t s = left ? ls : segs;  // segment segs: past the row's end, zeros
     F::load(t.a, rg, wg, s, lane);
     F::load(t.b, ru, wu, s, lane);
-    token_order();
+    keep_order();
     if (left) {
       --left;
       if (++ls == segs) {
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typena
           ++cp;
         }
       }
-      token_order();
+      keep_order();
       load(ring[u]);
     }
   }
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint
   auto load = [&](TokenPair<F> &t) {
     F::load(t.a, ra, wd, ls, lane);
     F::load(t.b, rb, wd, ls, lane);
-    token_order();
+    keep_order();
     ++lq;
     if (++ls == segs || lq == q1) {
       ls = 0;
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint
           ++cp;
         }
       }
-      token_order();
+      keep_order();
       load(ring[u]);
     }
   }

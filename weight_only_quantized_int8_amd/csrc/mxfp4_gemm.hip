@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *_
   auto load = [&](TokenPair<F> &t) {
     F::load(t.a, ra, w, ls, lane);
     F::load(t.b, rb, w, ls, lane);
-    token_order();
+    keep_order();
     if (++ls >= s1) {
       ls = s0;
       ++lp;
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *_
           ++cp;
         }
       }
-      token_order();
+      keep_order();
       load(ring[u]);
     }
   }

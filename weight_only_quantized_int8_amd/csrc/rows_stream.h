@@ -50,10 +50,6 @@ __device__ __forceinline__ f32x4 mfma_mx(u32x4 a, uint32_t sa, u32x4 b, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// Loads are waited for in the order of their issue, so a ring of pieces in flight only
-// works if the compiler keeps each piece's loads together and behind the ones before.
-__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
 // LDS writes of this wave's lanes before reads by its other lanes: LDS instructions of a
 // wave execute in order, so only the compiler has to keep it.
 __device__ __forceinline__ void wave_fence() {
@@ -193,9 +189,6 @@ struct MxFmt {
 };
 
 // ---- 8-bit affine -----------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t int8_pair_bf16(uint32_t w, int i) {  // codes 2i, 2i + 1 as BF16 integers (exact)
-  return __builtin_amdgcn_perm(__float_as_uint(code_f32(w, 2 * i + 1)), __float_as_uint(code_f32(w, 2 * i)), 0x07060302u);
-}
 __device__ __forceinline__ u32x4 int8_codes_bf16(uint32_t a, uint32_t b) {
   return u32x4{int8_pair_bf16(a, 0), int8_pair_bf16(a, 1), int8_pair_bf16(b, 0), int8_pair_bf16(b, 1)};
 }

@@ -35,9 +35,6 @@ __device__ __forceinline__ float token_sum(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-// As keep_order() of rows_stream.h.
-__device__ __forceinline__ void token_order() { __builtin_amdgcn_sched_barrier(0); }
-
 struct MxTok {
   typedef MxView View;
   static constexpr uint32_t kSeg = 2048;  // k of a load
@@ -94,17 +91,14 @@ struct Int8Tok {
     f.s = buf_load_b16(r.scales, o);
     f.b = buf_load_b16(r.biases, o);
   }
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {  // codes 2i, 2i + 1 as BF16 (exact)
-    return __builtin_amdgcn_perm(__float_as_uint(code_f32(w, 2 * i + 1)), __float_as_uint(code_f32(w, 2 * i)), 0x07060302u);
-  }
   static __device__ __forceinline__ float dot(float acc, const Frag &f, const u32x4 (&x)[kX], float sum) {
     float p = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      p = dot2(pair(f.q[2 * h], 0), x[h].x, p);
-      p = dot2(pair(f.q[2 * h], 1), x[h].y, p);
-      p = dot2(pair(f.q[2 * h + 1], 0), x[h].z, p);
-      p = dot2(pair(f.q[2 * h + 1], 1), x[h].w, p);
+      p = dot2(int8_pair_bf16(f.q[2 * h], 0), x[h].x, p);
+      p = dot2(int8_pair_bf16(f.q[2 * h], 1), x[h].y, p);
+      p = dot2(int8_pair_bf16(f.q[2 * h + 1], 0), x[h].z, p);
+      p = dot2(int8_pair_bf16(f.q[2 * h + 1], 1), x[h].w, p);
     }
     return __builtin_fmaf(bf16_bits_to_f32(f.s), p, __builtin_fmaf(bf16_bits_to_f32(f.b), sum, acc));
   }
@@ -146,7 +140,7 @@ struct TokenStage {
       v[i] = u32x4{0u, 0u, 0u, 0u};
       if (r < n && 8u * c < K) v[i] = *reinterpret_cast<const u32x4 *>(x + (size_t)r * K + 8u * c);
     }
-    token_order();
+    keep_order();
   }
   __device__ __forceinline__ void load() { load(tid); }
   __device__ __forceinline__ void write(uint8_t *lds, uint32_t p0) const {
