@@ -18,13 +18,15 @@
 // Bound: HBM, each chosen expert's three matrices once.  An expert with more than
 // 16 tokens has several segments, whose further reads of its rows come from the caches
 // where they run together.  Measured, up / down: 13 tokens, 64 experts of 1024x2048 in 8 bits,
-// 6 each: 38.8 us (191 MB fetched, 4.9 TB/s) / 22.2 us (96 MB, 4.3 TB/s); 37 tokens, 8 experts of
-// 14336x4096 in MXFP4, 2 each: 100 us (503 MB, 5.0 TB/s) / 49 us (276 MB, 5.7 TB/s); one token,
-// 8 experts of 14336x4096 in 8 bits, 2 taken: 41.2 us (250 MB, 6.1 TB/s) / 23.2 us (125 MB,
-// 5.4 TB/s).  Route and sum take 4.7 to 5.5 us each, mostly the start and end of a launch.
+// 6 each: 38.2 us (191 MB fetched, 5.0 TB/s) / 21.9 us (96 MB, 4.4 TB/s), in groups of 32 52.7 / 23.6;
+// 37 tokens, 8 experts of 14336x4096 in MXFP4, 2 each: 102 us (503 MB, 4.9 TB/s) / 50 us (276 MB,
+// 5.5 TB/s); one token, 8 experts of 14336x4096 in 8 bits, 2 taken: 40.0 us (250 MB, 6.2 TB/s) /
+// 22.4 us (125 MB, 5.6 TB/s).  Route and sum take 4.6 to 6.3 us each, mostly the start and end of a
+// launch.  Each pass of 64 tokens streams its experts again: on a prompt the weights are read
+// tokens/64 times (512 tokens, 8 experts of 14336x4096 in MXFP4: 1.69 ms).
 //
 // h is kept in BF16 (the matrix cores' operand type): its relative rounding of at
-// most 2^-9 a value averages out over the inner sum to about the output's own BF16
+// most 2^-8 a value, 2^-9 rms, averages out over the inner sum to about the output's own BF16
 // rounding.  All sums, the softmax and the routing weights are fp32.
 #include "rows_stream.h"
 #include "token_stream.h"
@@ -462,7 +464,9 @@ __global__ __launch_bounds__(64 * KW) void k_moe1_down(typename F::View wd, uint
 
 constexpr uint32_t kLdsBytes = 160u << 10;
 
-// Whether the one-token kernels' activations fit the LDS.
+// Whether the one-token kernels' activations fit the LDS.  Beyond it a token takes the form for
+// several, with one of 16 rows of the matrix products in use: 8 of 16 experts of 8192x4096 take
+// 81 us in MXFP4 and 151 in 8 bits, of 8224x4096 151 and 246.
 template <class F>
 bool one_token_fits(uint32_t H, uint32_t I, uint32_t topk) {
   return token_lds<F>(H) <= kLdsBytes - 1024u && (uint64_t)topk * token_lds<F>(I) <= kLdsBytes - 1024u;
@@ -543,8 +547,10 @@ hipError_t launch_layer(const typename F::View &g, const typename F::View &u, co
     const size_t at = (size_t)t0 * H;
     const uint32_t ub = (I + 16u * KW - 1u) / (16u * KW), db = (H + 16u * KW - 1u) / (16u * KW);
     // streamed past the caches where a row is whole cache lines (else neighbouring pieces share
-    // one) and experts hardly have a second segment (37 tokens, 8 experts: 166 against 177 us;
-    // 64 tokens, 4 experts: 56 against 51, rows of 992 bytes: 233 against 217)
+    // one) and experts hardly have a second segment (us past the caches / through them, in MXFP4,
+    // 2 experts a token: 8 experts of 14336x4096, 16 tokens 141 / 157, 37 149 / 164, 48 163 / 175, 64
+    // 218 / 215; of 4096x4096, 64 tokens, 16 experts 96 / 106, 4 73 / 66; 16 tokens, 8 of 992x1984 35 / 30;
+    // in 8 bits: 8 of 14336x4096, 16 tokens 298 / 348, 48 354 / 390, 64 441 / 448)
     const bool nt = F::row_bytes(g.K) % 128u == 0 && F::row_bytes(d.K) % 128u == 0 && (T <= kSegTokens || slots <= 12u * m.E);
     if (nt) {
       k_moe_up<F, KW, kAuxNontemporal><<<ub * most, 64 * KW, 0, stream>>>(g, u, I, ub, m.x + at, T, m.topk, head, h);

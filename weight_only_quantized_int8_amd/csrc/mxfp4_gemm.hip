@@ -9,8 +9,9 @@
 //  k_mx_tile  more: LDS-tiled, on bf16 MFMA (X BF16: codes are converted with their scale
 //             in registers, exactly below 2^128) or on the scaled fp4 MFMA (both MXFP4: 16 x 16 x 128
 //             products with a scale per 32 k in the instruction).
-// The first two are bound by HBM, once the weight is large enough to hide a launch; the
-// last by the matrix cores and by the LDS and conversions that feed them.
+// The first is bound by HBM, once the weight is large enough to hide a launch; the second by the
+// re-reading of X through the L2s and by latency; the third, with several hundred rows of X, by
+// the matrix cores and by the LDS and conversions that feed them, with fewer again by re-reading.
 #include <type_traits>
 #include <utility>
 
@@ -26,7 +27,7 @@ namespace {
 
 // y[n] = sum_k W[n, k] x[k].  Waves share the pairs of weight rows; KS neighbouring waves
 // share a pair's segments where there are few pairs.  LDS: x.  HBM-bound: 8192x28672, 125 MB
-// in 21.0 us, 5.9 TB/s; 4096x4096, 8.9 MB, 4.1 us, mostly the start and end of a launch.
+// in 21.2 us, 5.9 TB/s; 4096x4096, 8.9 MB, 4.1 us, mostly the start and end of a launch.
 template <int KW, int U, int KS>
 __global__ __launch_bounds__(64 * KW) void k_mx_gemv(MxView w, const uint16_t *__restrict__ x, uint16_t *__restrict__ y) {
   typedef MxTok F;
@@ -168,9 +169,12 @@ __device__ __forceinline__ void stream_piece_mx(f32x4 (&acc)[2], const Pieces<Mx
 }
 
 // grid: (16-row weight tiles) x (groups of 16 rows of X), the groups of a tile side by side.
-// HBM-bound in what it moves, but a row of 14336 is 28 pieces, three or four a wave: the first
-// loads' latency and the waves' last sum are a large part of a call.  4096x14336, 31.8 MB: m = 16
-// 12.4 us; m = 8 with X in MXFP4 8.4 us.
+// Every workgroup reads its rows of X itself: in BF16 with m = 16, 32 bytes of X for each 8.5 of
+// weight.  And a row of 14336 is 28 pieces, three or four a wave, so the first loads' latency and
+// the waves' last sum are a large part of a call.  4096x14336 (31.8 MB at m = 16, floor 4.6 us):
+// m = 16 12.4 us with 152 MB requested from the L2s; m = 48, three groups, 27.3 us with 463 MB
+// requested and 107 MB from HBM (the groups do not find each other's weights); X in MXFP4 m = 8
+// 8.5 us, m = 32 12.6 us with 116 MB requested.
 template <bool XMX, bool DW, int KS, int U, int NX, int AUX>
 __global__ __launch_bounds__(64 * KS) void k_mx_rows(MxView w, const void *__restrict__ x,
                                                      const uint8_t *__restrict__ xs, uint32_t m, uint32_t groups,
@@ -237,9 +241,13 @@ constexpr uint32_t kGroup = 4 * kChunk;  // k of one scale load: 16 scale bytes 
 // operands are copied to LDS by DMA, two stages; 16-byte pieces of a row are
 // XOR-swizzled so that the rows of an operand read fall into distinct banks.  A =
 // weight rows, B = X rows: a lane's four results are neighbours in Y.
-// 14336x4096: m = 512 X BF16 51 us, 1.18 PFLOP/s (the bf16 MFMA alone reaches 1.66); m = 2048
-// both MXFP4 80 us, 3.0 PFLOP/s (the fp4 MFMA alone 6.1): each product needs its operands
-// from LDS once per 16 x 16 x 128, and the loads of a step share the address unit.
+// 14336x4096: m = 512 X BF16 51.7 us in calls without a pause, 1.16 PFLOP/s (the bf16 MFMA alone
+// reaches 1.66; a call on an idle GPU takes 55 to 61 us, the kernel under the tracer 60); m = 2048
+// both MXFP4 83.3 us, 2.9 PFLOP/s (the fp4 MFMA alone 6.1): each product needs its operands
+// from LDS once per 16 x 16 x 128, the loads of a step share the address unit, and 448 tiles are
+// 1.75 rounds of the CUs.
+// The narrow tiles read X once for each 32, 64 or 128 weight rows: m = 128 4096x14336 40.0 us
+// (floor 11.6) with 602 MB requested from the L2s for 36, both MXFP4 20.5 us (floor 4.8) with 206.
 // Scales: loaded a group ahead, a lane per row and 16 bytes (block g of chunk c at
 // byte 4c + g), transposed to bytes 4g + c and put in LDS, so that a lane gets its
 // row's scales of block g for all four chunks as one dword whose byte c the scaled
@@ -562,8 +570,11 @@ hipError_t launch_rows_dw(const MxView &w, const void *x, const uint8_t *xs, uin
   const uint32_t groups = (m + 15u) / 16u, grid = (w.N + 15u) / 16u * groups;
   const uint32_t np = (w.K + MxFmt<DW>::kPiece - 1u) / MxFmt<DW>::kPiece;
   // Four waves share a tile's K, eight where there is at most a tile a CU and K is long
-  // (us with four / eight: m = 2 8192x28672 25 / 27, m = 8 14336x4096 12.6 / 22,
-  // m = 16 4096x14336 14.5 / 13.6).
+  // (us with four / eight, X BF16: m = 16 4096x14336 14.5 / 13.5, 2048x8192 9.3 / 8.3, m = 2
+  // 4096x28672 17.5 / 15.4, m = 8 1024x28672 16.1 / 16.6; more tiles: m = 16 8192x8192 15.6 / 16.9,
+  // 14336x4096 15.1 / 17.7; X MXFP4: m = 16 4096x14336 11.2 / 9.8, m = 1 1024x28672 15.3 / 10.1; more
+  // tiles: m = 8 8192x8192 10.3 / 10.7).  The bound on K was set on long rows: on half as many pieces
+  // eight waves are 5 to 10 % faster too (m = 16 2048x4096 6.1 / 5.5, m = 4 4096x4096 5.1 / 4.8).
   constexpr int U4 = !XMX && NX <= 2 ? 2 : 1;
   if (grid <= (uint32_t)device_cu_count() && np >= 16u)
     k_mx_rows<XMX, DW, 8, 1, NX, AUX><<<grid, 512, 0, stream>>>(w, x, xs, m, groups, y);
