@@ -283,6 +283,119 @@ int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const 
                           uint32_t num_experts, const int8w_moe_call *call, void *workspace,
                           uint64_t workspace_bytes, uint64_t stream);
 
+/* ---- The routing to experts, for int8_moe_gemv, the layers below or a caller's own.  For
+ * token t with router logits l [num_experts]:
+ *   s_e = e^(l_e) / sum e^l (INT8W_ROUTE_SOFTMAX) or 1 / (1 + e^(-l_e)) (INT8W_ROUTE_SIGMOID);
+ *   c_e = s_e + bias_e: what the choice goes by (s alone makes the weights);
+ *   of `groups` groups of num_experts / groups consecutive experts the topk_groups of the
+ *   largest score stay, a group's score being its largest c (INT8W_GROUP_MAX) or the sum of
+ *   its two largest (INT8W_GROUP_TOP2; of one, where a single expert is left);
+ *   the topk experts of largest c in them are taken, largest first;
+ *   weight = routed_scale * s_e, with renormalize routed_scale * s_e / (sum of the taken s)
+ *   (0 where that sum is 0).
+ * Equal values go to the lower index.  Scores are compared in 64 bits; without a bias and
+ * groups c orders as l, which is then compared itself.  An expert whose l or c is -inf is never
+ * taken; the slots that no expert is left for hold the id INT8W_NO_EXPERT and weight 0.  A token
+ * with a NaN among its l or c, or with softmax a +inf among its l, gets INT8W_NO_EXPERT and NaN
+ * weights in all its slots.
+ *   logits   f32 or BF16 [tokens, num_experts] (logits_format), on the device;
+ *   bias     f32 [num_experts] or NULL;
+ *   ids      uint32 [tokens, topk], weights f32 [tokens, topk]: the outputs.
+ * tokens = 0 is a no-op.  Errors: INT8W_ERR_NULL; INT8W_ERR_SHAPE (num_experts outside
+ * 1..INT8W_MAX_MOE_EXPERTS, topk outside 1..min(num_experts, INT8W_MAX_MOE_TOPK), groups not
+ * dividing num_experts or above INT8W_MAX_MOE_GROUPS, topk_groups outside 1..groups, fewer than topk
+ * experts in topk_groups groups); INT8W_ERR_UNSUPPORTED (logits_format, scoring, group_score);
+ * INT8W_ERR_ALIGN (4 bytes; BF16 logits 2); INT8W_ERR_ALIAS. */
+enum { INT8W_ROUTE_SOFTMAX = 0, INT8W_ROUTE_SIGMOID = 1 };
+enum { INT8W_GROUP_MAX = 0, INT8W_GROUP_TOP2 = 1 };
+#define INT8W_NO_EXPERT 0xFFFFFFFFu
+#define INT8W_MAX_MOE_GROUPS 64
+typedef struct {
+  const void *logits;
+  const float *bias;
+  uint32_t *ids;
+  float *weights;
+  uint32_t tokens;
+  uint32_t num_experts;
+  uint32_t topk;
+  uint32_t logits_format; /* INT8W_VALUES_F32 or INT8W_VALUES_BF16 */
+  uint32_t scoring;       /* INT8W_ROUTE_* */
+  uint32_t groups;        /* 1: none */
+  uint32_t topk_groups;
+  uint32_t group_score;   /* INT8W_GROUP_* */
+  uint32_t renormalize;   /* 0 or 1 */
+  float routed_scale;
+} int8w_route_call;
+int int8w_moe_route(const int8w_route_call *call, uint64_t stream);
+
+/* The layers above from a given routing (int8w_moe_route's, or any other):
+ *   y[t] = RNE_bf16( x_resid[t] + sum_j weights[t, j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)) ), e = ids[t, j].
+ * A slot whose id is not below num_experts, or whose weight is 0, runs no expert and adds
+ * nothing; the weights of an expert that a token names twice are added; a token with a NaN
+ * among its weights (whatever their ids) gets NaN outputs.  ids [tokens, topk] uint32 and weights
+ * [tokens, topk] f32 are device arrays, read by the kernels.  topk is 1..INT8W_MAX_MOE_TOPK (also above
+ * num_experts).  Everything else, workspace and errors as for the layers from logits. */
+typedef struct {
+  const uint16_t *x;
+  const uint32_t *ids;
+  const float *weights;
+  const uint16_t *x_resid;
+  uint16_t *y;
+  uint32_t tokens;
+  uint32_t topk;
+} int8w_moe_routed_call;
+int int8_moe_layer_routed(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down,
+                          uint32_t num_experts, const int8w_moe_routed_call *call, void *workspace,
+                          uint64_t workspace_bytes, uint64_t stream);
+int int8w_mxfp4_moe_layer_routed(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down,
+                                 uint32_t num_experts, const int8w_moe_routed_call *call, void *workspace,
+                                 uint64_t workspace_bytes, uint64_t stream);
+
+/* ---- Low-rank adapters of many requests beside a shared projection.  A pool holds num_adapters
+ * pairs of BF16 matrices; row t of a batch takes the adapter that ids[t] names:
+ *   y[t] = RNE_bf16( base[t] + scales[e] * B_e (A_e x[t]) ),  e = ids[t],
+ * exact products, fp32 sums, one rounding.  A row with id INT8W_NO_ADAPTER gets base[t] itself; any
+ * other id not below num_adapters gives a row of the quiet NaN 0x7FC0.  base is typically the output of
+ * int8_gemm or int8w_mxfp4_gemm, in place.  Up to INT8W_MAX_MULTI pools with the same
+ * num_adapters and in_features (q, k and v; gate and up) share x and ids in one call.
+ * Rows may come in any order: rows of single tokens with an adapter each, runs of a prompt's
+ * rows, both; an adapter's matrices are read once for neighbouring rows that share it. */
+#define INT8W_NO_ADAPTER 0xFFFFFFFFu
+#define INT8W_MAX_LORA_RANK 256
+typedef struct {
+  const uint16_t *a;      /* BF16 [num_adapters, rank, in_features] (device), 16-byte aligned */
+  const uint16_t *b;      /* BF16 [num_adapters, out_features, rank] (device), 16-byte aligned */
+  const float *scales;    /* f32 [num_adapters] (device), or NULL: 1 */
+  const uint32_t *ranks;  /* uint32 [num_adapters] (device), or NULL: an adapter's own rank, beyond which its
+                             rows of A and columns of B must be zeros (they are not always read) */
+  uint32_t num_adapters;
+  uint32_t rank;          /* a multiple of 8, 8..INT8W_MAX_LORA_RANK */
+  uint32_t in_features;   /* K: a multiple of 8, below 2^20 */
+  uint32_t out_features;  /* N: below 2^20 */
+} int8w_lora;
+
+/* One pool's output.  Rows are base_stride / y_stride elements apart (at least out_features; no
+ * rule on alignment but BF16's): columns of a wider matrix will do.  base == NULL: zeros, and base_stride is not
+ * looked at.  y may be base itself, with the same stride. */
+typedef struct {
+  const uint16_t *base;
+  uint16_t *y;
+  uint64_t base_stride;
+  uint64_t y_stride;
+} int8w_lora_out;
+
+/* x: BF16 rows x_stride elements apart (at least in_features, a multiple of 8), 16-byte aligned.
+ * ids: uint32 [m], device.  m = 0 is a no-op.  workspace: device scratch, 256-byte aligned, of at least
+ * int8w_lora_workspace_bytes(pools, count, m) bytes; no initial value, none kept; calls that share it must not overlap.
+ * Errors: INT8W_ERR_NULL; INT8W_ERR_SHAPE (count outside 1..INT8W_MAX_MULTI, pools that do not fit
+ * each other, sizes outside the limits, m above 2^21, a stride too small or above 2^32, a workspace
+ * too small); INT8W_ERR_ALIGN; INT8W_ERR_ALIAS (a y or the workspace overlapping an input or another y; columns
+ * of one matrix, strides alike, do not overlap). */
+uint64_t int8w_lora_workspace_bytes(const int8w_lora *pools, uint32_t count, uint32_t m);
+int int8w_lora_add(const int8w_lora *pools, const int8w_lora_out *out, uint32_t count, const uint16_t *x,
+                   uint64_t x_stride, const uint32_t *ids, uint32_t m, void *workspace, uint64_t workspace_bytes,
+                   uint64_t stream);
+
 /* Source: "MlxInt8Weight", method gemv_silu_gate (kernel
  * mlx_int8_gemv_silu_gate: one launch, the gated product kept off memory).
  * gemv_silu_gate: y = W (silu(gate) * up) in one launch, silu(g) = g/(1+e^-g).

@@ -8,5 +8,6 @@ hand-written HIP kernels for gfx950, reached through the C-ABI library
 ``libint8w.so`` (declared in include/int8w.h); this package only marshals
 arguments.  There is no CPU fallback: calls fail when the library is missing.
 """
-from .binding import (Fp8Weight, Int8Weight, Int8wError, Mxfp4Weight, gemv_multi, library_path,  # noqa: F401
-                      load_library, moe_gemv, moe_layer, storage_bytes)
+from .binding import (Fp8Weight, Int8Weight, Int8wError, LoraAdapters, Mxfp4Weight, gemv_multi,  # noqa: F401
+                      library_path, load_library, lora_add, moe_gemv, moe_layer, moe_layer_routed, moe_route,
+                      storage_bytes)

@@ -40,7 +40,8 @@ EXPORTED = (
     "int8_gemv_silu_gate_resid", "int8_gemm", "int8_gemv_multi", "int8_quantize", "int8_moe_gemv",
     "int8w_fp8_gemv", "int8w_last_error", "int8_gemm_workspace_bytes", "int8_gemm_ws", "int8_gemm_noalloc",
     "int8w_mxfp4_quantize", "int8w_mxfp4_dequantize_to", "int8w_mxfp4_gemm", "int8w_mxfp4_gemm_mx",
-    "int8w_moe_workspace_bytes", "int8_moe_layer", "int8w_mxfp4_moe_layer",
+    "int8w_moe_workspace_bytes", "int8_moe_layer", "int8w_mxfp4_moe_layer", "int8w_moe_route",
+    "int8_moe_layer_routed", "int8w_mxfp4_moe_layer_routed", "int8w_lora_workspace_bytes", "int8w_lora_add",
 )
 # calibration streams declared in include/int8w_measure.h
 EXPORTED_MEASURE = ("int8w_stream_read", "int8w_stream_copy", "int8w_stream_expand")
@@ -48,6 +49,10 @@ FP8_PER_ROW, FP8_BLOCK_BF16, FP8_BLOCK_F32, FP8_SINGLE = 0, 1, 2, 3  # INT8W_FP8
 VALUES_BF16, VALUES_F32 = 0, 1  # INT8W_VALUES_*
 MAX_MOE_EXPERTS, MAX_MOE_TOPK = 512, 16  # INT8W_MAX_MOE_EXPERTS, INT8W_MAX_MOE_TOPK
 MAX_MULTI = 4  # INT8W_MAX_MULTI
+MAX_MOE_GROUPS = 64  # INT8W_MAX_MOE_GROUPS
+MAX_LORA_RANK = 256  # INT8W_MAX_LORA_RANK
+ROUTE_SCORING = {"softmax": 0, "sigmoid": 1}  # INT8W_ROUTE_*
+GROUP_SCORES = {"max": 0, "top2": 1}  # INT8W_GROUP_*
 MAX_MOE_SLOTS = 65536  # INT8W_MAX_MOE_SLOTS
 
 
@@ -105,6 +110,63 @@ class MoeCall(ctypes.Structure):
         ("logits_format", ctypes.c_uint32),
         ("renormalize", ctypes.c_uint32),
         ("routed_scale", ctypes.c_float),
+    ]
+
+
+class RouteCall(ctypes.Structure):
+    """Mirror of ``int8w_route_call`` (include/int8w.h)."""
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("tokens", ctypes.c_uint32),
+        ("num_experts", ctypes.c_uint32),
+        ("topk", ctypes.c_uint32),
+        ("logits_format", ctypes.c_uint32),
+        ("scoring", ctypes.c_uint32),
+        ("groups", ctypes.c_uint32),
+        ("topk_groups", ctypes.c_uint32),
+        ("group_score", ctypes.c_uint32),
+        ("renormalize", ctypes.c_uint32),
+        ("routed_scale", ctypes.c_float),
+    ]
+
+
+class MoeRoutedCall(ctypes.Structure):
+    """Mirror of ``int8w_moe_routed_call`` (include/int8w.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("x_resid", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("tokens", ctypes.c_uint32),
+        ("topk", ctypes.c_uint32),
+    ]
+
+
+class LoraDesc(ctypes.Structure):
+    """Mirror of ``int8w_lora`` (include/int8w.h)."""
+    _fields_ = [
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("ranks", ctypes.c_void_p),
+        ("num_adapters", ctypes.c_uint32),
+        ("rank", ctypes.c_uint32),
+        ("in_features", ctypes.c_uint32),
+        ("out_features", ctypes.c_uint32),
+    ]
+
+
+class LoraOut(ctypes.Structure):
+    """Mirror of ``int8w_lora_out`` (include/int8w.h)."""
+    _fields_ = [
+        ("base", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("base_stride", ctypes.c_uint64),
+        ("y_stride", ctypes.c_uint64),
     ]
 
 
@@ -172,6 +234,18 @@ def load_library() -> ctypes.CDLL:
     lib.int8_moe_layer.restype = ctypes.c_int
     lib.int8w_mxfp4_moe_layer.argtypes = [M, M, M, u32, C, P, u64, u64]
     lib.int8w_mxfp4_moe_layer.restype = ctypes.c_int
+    lib.int8w_moe_route.argtypes = [ctypes.POINTER(RouteCall), u64]
+    lib.int8w_moe_route.restype = ctypes.c_int
+    G = ctypes.POINTER(MoeRoutedCall)
+    lib.int8_moe_layer_routed.argtypes = [W, W, W, u32, G, P, u64, u64]
+    lib.int8_moe_layer_routed.restype = ctypes.c_int
+    lib.int8w_mxfp4_moe_layer_routed.argtypes = [M, M, M, u32, G, P, u64, u64]
+    lib.int8w_mxfp4_moe_layer_routed.restype = ctypes.c_int
+    L = ctypes.POINTER(LoraDesc)
+    lib.int8w_lora_workspace_bytes.argtypes = [L, u32, u32]
+    lib.int8w_lora_workspace_bytes.restype = u64
+    lib.int8w_lora_add.argtypes = [L, ctypes.POINTER(LoraOut), u32, P, u64, P, u32, P, u64, u64]
+    lib.int8w_lora_add.restype = ctypes.c_int
     lib.int8w_stream_read.argtypes = [P, u64, P, u64]
     lib.int8w_stream_read.restype = ctypes.c_int
     lib.int8w_stream_copy.argtypes = [P, P, u64, u64]
@@ -289,6 +363,31 @@ def int8_moe_layer(gate: WeightDesc, up: WeightDesc, down: WeightDesc, num_exper
 def int8w_mxfp4_moe_layer(gate: Mxfp4Desc, up: Mxfp4Desc, down: Mxfp4Desc, num_experts: int, call: MoeCall, ws: int,
                           ws_bytes: int, stream: int) -> int:
     return load_library().int8w_mxfp4_moe_layer(gate, up, down, num_experts, call, ws, ws_bytes, stream)
+
+
+def int8w_moe_route(call: RouteCall, stream: int) -> int:
+    return load_library().int8w_moe_route(call, stream)
+
+
+def int8_moe_layer_routed(gate: WeightDesc, up: WeightDesc, down: WeightDesc, num_experts: int, call: MoeRoutedCall,
+                          ws: int, ws_bytes: int, stream: int) -> int:
+    return load_library().int8_moe_layer_routed(gate, up, down, num_experts, call, ws, ws_bytes, stream)
+
+
+def int8w_mxfp4_moe_layer_routed(gate: Mxfp4Desc, up: Mxfp4Desc, down: Mxfp4Desc, num_experts: int,
+                                 call: MoeRoutedCall, ws: int, ws_bytes: int, stream: int) -> int:
+    return load_library().int8w_mxfp4_moe_layer_routed(gate, up, down, num_experts, call, ws, ws_bytes, stream)
+
+
+def int8w_lora_workspace_bytes(pools, count: int, m: int) -> int:
+    """pools: a LoraDesc, or a ctypes array of them."""
+    return load_library().int8w_lora_workspace_bytes(pools, count, m)
+
+
+def int8w_lora_add(pools, out, count: int, x: int, x_stride: int, ids: int, m: int, ws: int, ws_bytes: int,
+                   stream: int) -> int:
+    """pools, out: ctypes arrays of count LoraDesc and LoraOut (or one of each)."""
+    return load_library().int8w_lora_add(pools, out, count, x, x_stride, ids, m, ws, ws_bytes, stream)
 
 
 def int8_gemv_multi(descs, x: int, ys, stream: int) -> int:
@@ -443,6 +542,12 @@ class Int8Weight:
         else:
             _check(int8_gemm(self.desc, x.data_ptr(), y.data_ptr(), m, stream))
         return y
+
+    def gemm_lora(self, x: torch.Tensor, adapters: "LoraAdapters", ids: torch.Tensor,
+                  y: torch.Tensor | None = None) -> torch.Tensor:
+        """gemm with each row's low-rank adapter beside it: lora_add in place on gemm's Y (which gemm has rounded)."""
+        _need_pool(adapters, self.in_features, self.out_features, x, ids)
+        return _add_in_place(adapters, x, ids, self.gemm(x, y))
 
 
 # One gemm workspace per device (scratch for split-K partials), grown on
@@ -622,6 +727,12 @@ class Mxfp4Weight:
         _check(load_library().int8w_mxfp4_gemm(self.desc, x.data_ptr(), y.data_ptr(), m, _stream_of(self.device)))
         return y
 
+    def gemm_lora(self, x: torch.Tensor, adapters: "LoraAdapters", ids: torch.Tensor,
+                  y: torch.Tensor | None = None) -> torch.Tensor:
+        """gemm with each row's low-rank adapter beside it: lora_add in place on gemm's Y (which gemm has rounded)."""
+        _need_pool(adapters, self.k, self.rows, x, ids)
+        return _add_in_place(adapters, x, ids, self.gemm(x, y))
+
     def gemm_mx(self, x: "Mxfp4Weight", y: torch.Tensor | None = None) -> torch.Tensor:
         """Y = X W^T with both operands in MXFP4 (x e.g. from Mxfp4Weight.quantize)."""
         if x.k != self.k:
@@ -680,3 +791,252 @@ def moe_layer(gate, up, down, num_experts: int, x: torch.Tensor, logits: torch.T
     layer = int8w_mxfp4_moe_layer if mx else int8_moe_layer
     _check(layer(gate.desc, up.desc, down.desc, E, call, ws.data_ptr(), ws.numel(), _stream_of(dev)))
     return y
+
+
+def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: torch.Tensor | None = None,
+              groups: int = 1, topk_groups: int | None = None, group_score: str = "top2", renormalize: bool = True,
+              routed_scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """The routing to experts (int8w_moe_route): ids int32 and weights float32 [tokens, topk], largest choice first.
+
+    logits:  float32 or bfloat16 [tokens, num_experts]
+    scoring: "softmax" or "sigmoid", the scores that make the weights
+    bias:    float32 [num_experts], added to the scores for the choice alone
+    groups:  the experts in that many equal groups, of which the topk_groups (default: all) with the largest
+             group_score stay: "max", a group's largest biased score, or "top2", the sum of its two largest
+    A slot that no expert is left for (those at -inf are never taken) holds id -1 and weight 0; a token with NaN
+    among its logits has id -1 and weight NaN in all its slots.  ids goes to moe_gemv (which gives NaN for an
+    id of -1), both to moe_layer_routed.
+    """
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or not logits.is_contiguous() \
+            or logits.device.type != "cuda":
+        raise ValueError("logits must be a contiguous float32 or bfloat16 [tokens, num_experts] GPU tensor")
+    if scoring not in ROUTE_SCORING or group_score not in GROUP_SCORES:
+        raise ValueError(f"scoring is one of {sorted(ROUTE_SCORING)}, group_score one of {sorted(GROUP_SCORES)}")
+    (T, E), dev = logits.shape, logits.device
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or bias.device != dev
+                             or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous float32 [{E}] tensor on the logits' GPU")
+    topk, groups = int(topk), int(groups)
+    topk_groups = groups if topk_groups is None else int(topk_groups)
+    if min(topk, groups, topk_groups) < 1:  # before they size the outputs
+        raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk}, groups {groups}, topk_groups {topk_groups}: below 1")
+    if ids is None:
+        ids = logits.new_empty((T, topk), dtype=torch.int32)
+    else:
+        _need_slots(ids, "ids", (torch.int32, torch.uint32), T, topk, dev)
+    if weights is None:
+        weights = logits.new_empty((T, topk), dtype=torch.float32)
+    else:
+        _need_slots(weights, "weights", (torch.float32,), T, topk, dev)
+    call = RouteCall(logits.data_ptr(), bias.data_ptr() if bias is not None else None, ids.data_ptr(), weights.data_ptr(),
+                     T, E, topk, VALUES_F32 if logits.dtype == torch.float32 else VALUES_BF16, ROUTE_SCORING[scoring],
+                     groups, topk_groups, GROUP_SCORES[group_score], bool(renormalize), routed_scale)
+    with _on(dev):
+        _check(load_library().int8w_moe_route(call, _stream_of(dev)))
+    return ids, weights
+
+
+def moe_layer_routed(gate, up, down, num_experts: int, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                     x_resid: torch.Tensor | None = None, y: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_layer from a given routing, moe_route's or any other (int8_moe_layer_routed, int8w_mxfp4_moe_layer_routed).
+
+    ids:     int32/uint32 [tokens, topk]; a slot whose id is not below num_experts (-1) runs no expert
+    weights: float32 [tokens, topk], of the slots' experts in the token's sum; any NaN makes the token's output NaN
+    returns  bfloat16 [tokens, hidden]: x_resid + the weighted sum over the slots.  The rest as moe_layer.
+    """
+    mx = isinstance(gate, Mxfp4Weight)
+    kind = Mxfp4Weight if mx else Int8Weight
+    if not (isinstance(gate, kind) and isinstance(up, kind) and isinstance(down, kind)):
+        raise TypeError("gate, up and down must be three Int8Weight or three Mxfp4Weight")
+    dev = gate.device
+    if up.device != dev or down.device != dev:
+        raise ValueError("moe_layer_routed: weights on different devices")
+    hidden, inner = (gate.k, down.k) if mx else (gate.in_features, down.in_features)
+    if x.dim() != 2 or x.shape[1] != hidden:
+        raise ValueError(f"x must be [tokens, {hidden}]")
+    T, E = x.shape[0], int(num_experts)
+    _need_bf16(x, "x", T * hidden, dev)
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be [{T}, topk]")
+    topk = ids.shape[1]
+    _need_slots(ids, "ids", (torch.int32, torch.uint32), T, topk, dev)
+    _need_slots(weights, "weights", (torch.float32,), T, topk, dev)
+    if x_resid is not None:
+        _need_bf16(x_resid, "x_resid", T * hidden, dev)
+    if not 1 <= topk <= MAX_MOE_TOPK:  # before it sizes the scratch
+        raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk} outside 1..{MAX_MOE_TOPK}")
+    if y is None:
+        y = torch.empty((T, hidden), dtype=torch.bfloat16, device=dev)
+    _need_bf16(y, "y", T * hidden, dev)
+    ws = x.new_empty(int8w_moe_workspace_bytes(T, topk, inner, hidden), dtype=torch.uint8)  # the call's own, as in moe_layer
+    call = MoeRoutedCall(x.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                         x_resid.data_ptr() if x_resid is not None else None, y.data_ptr(), T, topk)
+    layer = int8w_mxfp4_moe_layer_routed if mx else int8_moe_layer_routed
+    with _on(dev):
+        _check(layer(gate.desc, up.desc, down.desc, E, call, ws.data_ptr(), ws.numel(), _stream_of(dev)))
+    return y
+
+
+def _need_slots(t: torch.Tensor, name: str, dtypes, tokens: int, topk: int, device: torch.device) -> None:
+    if t.dtype not in dtypes or tuple(t.shape) != (tokens, topk) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {' or '.join(map(str, dtypes))} [{tokens}, {topk}] tensor on {device}")
+
+
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device: torch.device):
+    """Kernels go to the current device where the stream is the default one (handle 0), so a call on
+    another device's tensors makes that device current for its launch."""
+    return _HERE if device.index is None or device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+class LoraAdapters:
+    """A pool of low-rank adapters of one projection on the GPU (borrowed tensors).
+
+    a:      bfloat16 [num_adapters, rank, in_features]; rank and in_features multiples of 8, rank up to 256
+    b:      bfloat16 [num_adapters, out_features, rank]
+    scales: float32 [num_adapters], the factor of b (a x); None: 1
+    ranks:  int32/uint32 [num_adapters], where adapters of smaller ranks share the pool: beyond an adapter's
+            own rank its rows of a and columns of b hold zeros, which are then not read
+    """
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor | None = None,
+                 ranks: torch.Tensor | None = None):
+        if a.dim() != 3 or b.dim() != 3 or a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16:
+            raise ValueError("a and b must be 3-D bfloat16 tensors")
+        (num, rank, k), n = a.shape, b.shape[1]
+        if tuple(b.shape) != (num, n, rank):
+            raise ValueError(f"b must be [{num}, out_features, {rank}]")
+        if rank == 0 or rank % 8 or rank > MAX_LORA_RANK or k % 8:
+            raise ValueError(f"rank {rank} must be a multiple of 8 up to {MAX_LORA_RANK}, in_features {k} a multiple of 8")
+        if not a.is_contiguous() or not b.is_contiguous():
+            raise ValueError("a and b must be contiguous")
+        if a.device != b.device or a.device.type != "cuda":
+            raise ValueError("a and b must be on one GPU")
+        for t, name, dtypes in ((scales, "scales", (torch.float32,)), (ranks, "ranks", (torch.int32, torch.uint32))):
+            if t is not None and (t.dtype not in dtypes or tuple(t.shape) != (num,) or t.device != a.device
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {' or '.join(map(str, dtypes))} [{num}] tensor on {a.device}")
+        self.a, self.b, self.scales, self.ranks = a, b, scales, ranks
+        self.num_adapters, self.rank, self.in_features, self.out_features = num, rank, k, n
+        self.device = a.device
+        self.desc = LoraDesc(a.data_ptr(), b.data_ptr(), scales.data_ptr() if scales is not None else None,
+                             ranks.data_ptr() if ranks is not None else None, num, rank, k, n)
+
+    @classmethod
+    def from_list(cls, adapters) -> "LoraAdapters":
+        """A pool from (a [r, in_features], b [out_features, r], scale) of any ranks r: copies, padded with zeros."""
+        adapters = list(adapters)
+        if not adapters:
+            raise ValueError("from_list needs at least one adapter")
+        a0, b0, _ = adapters[0]
+        k, n, dev = a0.shape[-1], b0.shape[0], a0.device
+        for a, b, _ in adapters:
+            if a.dim() != 2 or b.dim() != 2 or a.shape[1] != k or b.shape[0] != n or b.shape[1] != a.shape[0] or a.shape[0] == 0:
+                raise ValueError(f"adapters must be a [r, {k}] and b [{n}, r]")
+        ranks = [a.shape[0] for a, _, _ in adapters]
+        rank = -(-max(ranks) // 8) * 8
+        pa = torch.zeros((len(ranks), rank, k), dtype=torch.bfloat16, device=dev)
+        pb = torch.zeros((len(ranks), n, rank), dtype=torch.bfloat16, device=dev)
+        for i, (a, b, _) in enumerate(adapters):
+            pa[i, :ranks[i]] = a
+            pb[i, :, :ranks[i]] = b
+        return cls(pa, pb, torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=dev),
+                   torch.tensor(ranks, dtype=torch.int32, device=dev))
+
+
+def _rows(t: torch.Tensor, name: str, m: int, n: int, device: torch.device) -> int:
+    """Checks a [m, n] matrix of bfloat16 whose rows may be apart (columns of a wider one); returns its row stride."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, adapters on {device}")
+    if t.dim() != 2 or t.shape[0] != m or t.shape[1] != n:
+        raise ValueError(f"{name} must be [{m}, {n}]")
+    rs, cs = t.stride()
+    if m <= 1:
+        rs = n  # one row: whatever the stride says
+    if (cs != 1 and n > 1) or rs < n:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return rs
+
+
+def _need_pool(pool: LoraAdapters, k: int, n: int, x: torch.Tensor, ids: torch.Tensor) -> None:
+    """What gemm_lora wants before its product is launched."""
+    if not isinstance(pool, LoraAdapters) or pool.in_features != k or pool.out_features != n:
+        raise ValueError(f"adapters must be LoraAdapters of in_features {k} and out_features {n}")
+    if x.dim() != 2 or x.device != pool.device:
+        raise ValueError(f"X must be [m, {k}] on {pool.device}")
+    _need_ids(ids, x.shape[0], pool.device)
+
+
+def _need_ids(ids: torch.Tensor, m: int, device: torch.device) -> None:
+    if ids.dtype not in (torch.int32, torch.uint32) or tuple(ids.shape) != (m,) or ids.device != device \
+            or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous 32-bit [{m}] tensor on {device}")
+
+
+def _add_in_place(pool: LoraAdapters, x: torch.Tensor, ids: torch.Tensor, y: torch.Tensor) -> torch.Tensor:
+    m, n = x.shape[0], pool.out_features
+    rows = y if tuple(y.shape) == (m, n) else y.view(-1)[:m * n].view(m, n)  # gemm takes any buffer that is large enough
+    lora_add(pool, x, ids, rows, rows)
+    return y
+
+
+def lora_add(adapters, x: torch.Tensor, ids: torch.Tensor, base=None, y=None):
+    """y[t] = base[t] + scales[e] * b[e] (a[e] x[t]) with e = ids[t] (int8w_lora_add).
+
+    adapters: one LoraAdapters, or up to four with the same num_adapters and in_features (q, k and v) that share
+              x and ids in one call: then base and y are sequences, and a list comes back
+    x:        bfloat16 [m, in_features]
+    ids:      int32/uint32 [m] on the GPU; -1: no adapter, the row gets base itself; another id outside the pool: NaN
+    base:     bfloat16 [m, out_features], typically the projection's output; None: zeros
+    y:        the output, base itself for in place; None: a new one
+    x, base and y may have rows apart (columns of a wider matrix; x's a multiple of 8 values).
+    Scratch is allocated for the call on the current stream, so calls may overlap on several streams.
+    """
+    one = isinstance(adapters, LoraAdapters)
+    pools = (adapters,) if one else tuple(adapters)
+    count = len(pools)
+    if not 1 <= count <= MAX_MULTI:
+        raise Int8wError(INT8W_ERR_SHAPE, f"lora_add takes 1..{MAX_MULTI} pools, got {count}")
+    p0 = pools[0]
+    dev, k = p0.device, p0.in_features
+    if x.dim() != 2 or x.shape[1] != k:
+        raise ValueError(f"x must be [m, {k}]")
+    m = x.shape[0]
+    xs = _rows(x, "x", m, k, dev)
+    _need_ids(ids, m, dev)
+    bases = (base,) if one else (None,) * count if base is None else tuple(base)
+    ys = [y] if one else [None] * count if y is None else list(y)
+    if len(bases) != count or len(ys) != count:
+        raise ValueError("lora_add: one base and one output per pool")
+    descs, outs = (LoraDesc * count)(), (LoraOut * count)()
+    for i, pool in enumerate(pools):
+        if pool.device != dev:
+            raise ValueError("lora_add: pools on different devices")
+        n, b, o = pool.out_features, bases[i], ys[i]
+        bs = _rows(b, "base", m, n, dev) if b is not None else 0
+        if o is None:
+            o = ys[i] = x.new_empty((m, n))
+            os = n
+        else:
+            os = _rows(o, "y", m, n, dev)
+        descs[i] = pool.desc
+        outs[i] = LoraOut(b.data_ptr() if b is not None else None, o.data_ptr(), bs, os)
+    lib = load_library()
+    need = lib.int8w_lora_workspace_bytes(descs, count, m)
+    ws = x.new_empty(need, dtype=torch.uint8)  # a call's own: one kept for the device would be shared by streams and graphs
+    with _on(dev):
+        _check(lib.int8w_lora_add(descs, outs, count, x.data_ptr(), xs, ids.data_ptr(), m, ws.data_ptr(), need,
+                                  _stream_of(dev)))
+    return ys[0] if one else ys

@@ -510,10 +510,31 @@ void ranges_of(const int8w_mxfp4 *w, Range *r, const char *codes = "codes", cons
   r[1] = range(scales, w->scales, (uint64_t)w->rows * (w->k / 32u));
 }
 
-// The checks that both expert formats share.  ins: the three weights' ranges.
+// A call of an expert layer, from logits or from a given routing.
+struct MoeCall {
+  const uint16_t *x;
+  const void *logits;  // or ids and weights
+  const uint32_t *ids;
+  const float *weights;
+  const uint16_t *x_resid;
+  uint16_t *y;
+  uint32_t tokens, topk;
+  uint32_t logits_format, renormalize;
+  float routed_scale;
+  bool given;
+};
+
+MoeCall moe_call(const int8w_moe_call *c) {
+  return MoeCall{c->x, c->logits, nullptr, nullptr, c->x_resid, c->y, c->tokens, c->topk, c->logits_format, c->renormalize,
+                 c->routed_scale, false};
+}
+MoeCall moe_call(const int8w_moe_routed_call *c) {
+  return MoeCall{c->x, nullptr, c->ids, c->weights, c->x_resid, c->y, c->tokens, c->topk, INT8W_VALUES_F32, 0, 1.f, true};
+}
+
+// The checks that both expert formats and both calls share.  ins: the three weights' ranges.
 int check_moe(uint64_t gate_rows, uint32_t hidden, uint64_t up_rows, uint32_t up_k, uint64_t down_rows, uint32_t inner,
-              uint32_t num_experts, const int8w_moe_call *c, void *ws, uint64_t ws_bytes, Range *ins, int n_ins) {
-  if (!c) return fail(INT8W_ERR_NULL, "call is NULL");
+              uint32_t num_experts, const MoeCall &c, void *ws, uint64_t ws_bytes, Range *ins, int n_ins) {
   if (num_experts == 0 || num_experts > INT8W_MAX_MOE_EXPERTS)
     return fail(INT8W_ERR_SHAPE, "num_experts %u outside 1..%d", num_experts, INT8W_MAX_MOE_EXPERTS);
   if (up_rows != gate_rows || up_k != hidden) return fail(INT8W_ERR_SHAPE, "up is not of gate's shape");
@@ -522,40 +543,159 @@ int check_moe(uint64_t gate_rows, uint32_t hidden, uint64_t up_rows, uint32_t up
                 (unsigned long long)gate_rows, (unsigned long long)down_rows, num_experts, inner, hidden);
   if (hidden >= (1u << 20) || inner >= (1u << 20))
     return fail(INT8W_ERR_SHAPE, "hidden %u or inner %u is not below 2^20", hidden, inner);
-  if (c->topk == 0 || c->topk > INT8W_MAX_MOE_TOPK || c->topk > num_experts)
-    return fail(INT8W_ERR_SHAPE, "topk %u outside 1..min(%u experts, %d)", c->topk, num_experts, INT8W_MAX_MOE_TOPK);
-  if (c->logits_format > INT8W_VALUES_F32)
-    return fail(INT8W_ERR_UNSUPPORTED, "unknown logits_format %u", c->logits_format);
-  if (c->tokens == 0) return INT8W_OK;
-  const uint64_t T = c->tokens;
-  const uint32_t el = c->logits_format == INT8W_VALUES_F32 ? 4 : 2;
-  if (!c->x || !c->logits || !c->y || !ws) return fail(INT8W_ERR_NULL, "x, logits, y or workspace is NULL");
-  if (!aligned(c->x, 16)) return fail(INT8W_ERR_ALIGN, "x is not 16-byte aligned");
-  if (!aligned(c->logits, el)) return fail(INT8W_ERR_ALIGN, "logits is not %u-byte aligned", el);
-  if (!aligned(c->y, 2) || !aligned(c->x_resid, 2)) return fail(INT8W_ERR_ALIGN, "y/x_resid are not 2-byte aligned");
+  if (c.topk == 0 || c.topk > INT8W_MAX_MOE_TOPK || (!c.given && c.topk > num_experts))
+    return c.given ? fail(INT8W_ERR_SHAPE, "topk %u outside 1..%d", c.topk, INT8W_MAX_MOE_TOPK)
+                   : fail(INT8W_ERR_SHAPE, "topk %u outside 1..min(%u experts, %d)", c.topk, num_experts, INT8W_MAX_MOE_TOPK);
+  if (c.logits_format > INT8W_VALUES_F32)
+    return fail(INT8W_ERR_UNSUPPORTED, "unknown logits_format %u", c.logits_format);
+  if (c.tokens == 0) return INT8W_OK;
+  const uint64_t T = c.tokens;
+  const uint32_t el = c.logits_format == INT8W_VALUES_F32 ? 4 : 2;
+  if (!c.x || !c.y || !ws || (c.given ? !c.ids || !c.weights : !c.logits))
+    return fail(INT8W_ERR_NULL, c.given ? "x, ids, weights, y or workspace is NULL" : "x, logits, y or workspace is NULL");
+  if (!aligned(c.x, 16)) return fail(INT8W_ERR_ALIGN, "x is not 16-byte aligned");
+  if (!aligned(c.logits, el)) return fail(INT8W_ERR_ALIGN, "logits is not %u-byte aligned", el);
+  if (!aligned(c.ids, 4) || !aligned(c.weights, 4)) return fail(INT8W_ERR_ALIGN, "ids/weights are not 4-byte aligned");
+  if (!aligned(c.y, 2) || !aligned(c.x_resid, 2)) return fail(INT8W_ERR_ALIGN, "y/x_resid are not 2-byte aligned");
   if (!aligned(ws, 256)) return fail(INT8W_ERR_ALIGN, "workspace is not 256-byte aligned");
-  const uint64_t need = int8w_moe_workspace_bytes(c->tokens, c->topk, inner, hidden);
+  const uint64_t need = int8w_moe_workspace_bytes(c.tokens, c.topk, inner, hidden);
   if (ws_bytes < need)
     return fail(INT8W_ERR_SHAPE, "workspace of %llu bytes, this call needs %llu", (unsigned long long)ws_bytes,
                 (unsigned long long)need);
-  ins[n_ins++] = range("x", c->x, T * hidden * 2);
-  ins[n_ins++] = range("logits", c->logits, T * num_experts * el);
-  const Range y = range("y", c->y, T * hidden * 2), work = range("workspace", ws, need);
-  const Range resid = range("x_resid", c->x_resid, T * hidden * 2);
-  if (c->x_resid && c->x_resid != c->y) {
+  ins[n_ins++] = range("x", c.x, T * hidden * 2);
+  if (c.given) {
+    ins[n_ins++] = range("ids", c.ids, T * c.topk * 4);
+    ins[n_ins++] = range("weights", c.weights, T * c.topk * 4);
+  } else {
+    ins[n_ins++] = range("logits", c.logits, T * num_experts * el);
+  }
+  const Range y = range("y", c.y, T * hidden * 2), work = range("workspace", ws, need);
+  const Range resid = range("x_resid", c.x_resid, T * hidden * 2);
+  if (c.x_resid && c.x_resid != c.y) {
     int rc = check_alias(y, &resid, 1);
     if (rc) return rc;
   }
   int rc = check_alias(y, ins, n_ins);
   if (!rc) rc = check_alias(work, ins, n_ins);
   if (!rc) rc = check_alias(work, &y, 1);
-  if (!rc && c->x_resid) rc = check_alias(work, &resid, 1);
+  if (!rc && c.x_resid) rc = check_alias(work, &resid, 1);
   return rc;
 }
 
-MoeArgs moe_args(const int8w_moe_call *c, uint32_t E, void *ws) {
-  return MoeArgs{E, c->x, c->logits, c->logits_format == INT8W_VALUES_BF16, c->tokens, c->topk, c->renormalize != 0,
-                 c->routed_scale, c->x_resid, c->y, ws};
+MoeArgs moe_args(const MoeCall &c, uint32_t E, void *ws) {
+  return MoeArgs{E, c.x, c.logits, c.ids, c.weights, c.logits_format == INT8W_VALUES_BF16, c.tokens, c.topk, c.renormalize != 0,
+                 c.routed_scale, c.x_resid, c.y, ws};
+}
+
+template <class Call>
+int moe_int8(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down, uint32_t num_experts,
+             const Call *call, void *workspace, uint64_t workspace_bytes, uint64_t stream) {
+  const int8w_weight *w[3] = {gate, up, down};
+  Range ins[12];
+  for (int i = 0; i < 3; ++i) {
+    int rc = validate(w[i]);
+    if (rc) return rc;
+    if (w[i]->group_size != gate->group_size)
+      return fail(INT8W_ERR_SHAPE, "gate, up and down have different group sizes");
+    weight_ranges(w[i], ins + 3 * i);
+  }
+  if (!call) return fail(INT8W_ERR_NULL, "call is NULL");
+  const MoeCall c = moe_call(call);
+  int rc = check_moe(gate->out_features, gate->in_features, up->out_features, up->in_features, down->out_features,
+                     down->in_features, num_experts, c, workspace, workspace_bytes, ins, 9);
+  if (rc) return rc;
+  if (c.tokens == 0) return ok();
+  (void)hipGetLastError();
+  return finish_launch(launch_moe_int8(view(gate), view(up), view(down), moe_args(c, num_experts, workspace), as_stream(stream)),
+                       as_stream(stream));
+}
+
+template <class Call>
+int moe_mx(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down, uint32_t num_experts, const Call *call,
+           void *workspace, uint64_t workspace_bytes, uint64_t stream) {
+  const int8w_mxfp4 *w[3] = {gate, up, down};
+  const char *const names[3] = {"gate", "up", "down"};
+  Range ins[9];
+  for (int i = 0; i < 3; ++i) {
+    int rc = validate_mx(w[i], names[i]);
+    if (rc) return rc;
+    ranges_of(w[i], ins + 2 * i);
+  }
+  if (!call) return fail(INT8W_ERR_NULL, "call is NULL");
+  const MoeCall c = moe_call(call);
+  int rc = check_moe(gate->rows, gate->k, up->rows, up->k, down->rows, down->k, num_experts, c, workspace,
+                     workspace_bytes, ins, 6);
+  if (rc) return rc;
+  if (c.tokens == 0) return ok();
+  (void)hipGetLastError();
+  return finish_launch(launch_moe_mx(view(gate), view(up), view(down), moe_args(c, num_experts, workspace), as_stream(stream)),
+                       as_stream(stream));
+}
+
+// Rows of `width` elements, `stride` apart.
+struct Rows {
+  const char *name;
+  uintptr_t at;
+  uint64_t width, stride, rows;  // elements of 2 bytes
+  Range span() const { return Range{name, at, at + (uintptr_t)(((rows - 1u) * stride + width) * 2u)}; }
+};
+
+// Rows with the same stride may lie side by side in one wider matrix.
+bool rows_overlap(const Rows &a, const Rows &b) {
+  if (!overlaps(a.span(), b.span())) return false;
+  if (a.stride != b.stride) return true;
+  const uint64_t pitch = a.stride * 2u;
+  const Rows &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
+  const uint64_t d = (uint64_t)(hi.at - lo.at) % pitch;
+  return !(d >= lo.width * 2u && d + hi.width * 2u <= pitch);
+}
+
+int validate_lora(const int8w_lora *p) {
+  if (!p->a || !p->b) return fail(INT8W_ERR_NULL, "adapters are missing a tensor (a or b is NULL)");
+  if (p->num_adapters == 0 || p->in_features == 0 || p->out_features == 0)
+    return fail(INT8W_ERR_SHAPE, "adapters: zero dimension (num_adapters=%u in_features=%u out_features=%u)",
+                p->num_adapters, p->in_features, p->out_features);
+  if (p->rank == 0 || p->rank % 8u != 0 || p->rank > INT8W_MAX_LORA_RANK)
+    return fail(INT8W_ERR_SHAPE, "adapters: rank %u is not a multiple of 8 in 8..%d", p->rank, INT8W_MAX_LORA_RANK);
+  if (p->in_features % 8u != 0 || p->in_features >= (1u << 20) || p->out_features >= (1u << 20))
+    return fail(INT8W_ERR_SHAPE, "adapters: in_features %u not a multiple of 8, or it or out_features %u not below 2^20",
+                p->in_features, p->out_features);
+  if (p->num_adapters >= (1u << 24)) return fail(INT8W_ERR_SHAPE, "num_adapters %u is not below 2^24", p->num_adapters);
+  if (!aligned(p->a, 16) || !aligned(p->b, 16)) return fail(INT8W_ERR_ALIGN, "adapters: a or b is not 16-byte aligned");
+  if (!aligned(p->scales, 4) || !aligned(p->ranks, 4))
+    return fail(INT8W_ERR_ALIGN, "adapters: scales or ranks is not 4-byte aligned");
+  return INT8W_OK;
+}
+
+int validate_lora_pools(const int8w_lora *pools, uint32_t count, uint32_t m) {
+  if (count == 0 || count > INT8W_MAX_MULTI) return fail(INT8W_ERR_SHAPE, "count %u outside 1..%d", count, INT8W_MAX_MULTI);
+  if (!pools) return fail(INT8W_ERR_NULL, "pools is NULL");
+  for (uint32_t i = 0; i < count; ++i) {
+    int rc = validate_lora(pools + i);
+    if (rc) return rc;
+    if (pools[i].num_adapters != pools->num_adapters || pools[i].in_features != pools->in_features)
+      return fail(INT8W_ERR_SHAPE, "pools differ in num_adapters or in_features");
+  }
+  if (m > (1u << 21)) return fail(INT8W_ERR_SHAPE, "m=%u rows are more than 2^21", m);
+  return INT8W_OK;
+}
+
+LoraArgs lora_args(const int8w_lora *pools, uint32_t count, uint32_t m) {
+  LoraArgs a = {};
+  for (uint32_t i = 0; i < count; ++i) {
+    LoraStack &s = a.s[i];
+    s.a = pools[i].a;
+    s.b = pools[i].b;
+    s.scales = pools[i].scales;
+    s.ranks = pools[i].ranks;
+    s.R = pools[i].rank;
+    s.N = pools[i].out_features;
+  }
+  a.count = count;
+  a.m = m;
+  a.K = pools->in_features;
+  a.num = pools->num_adapters;
+  return a;
 }
 
 }  // namespace
@@ -645,44 +785,151 @@ uint64_t int8w_moe_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t inne
 
 int int8_moe_layer(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down, uint32_t num_experts,
                    const int8w_moe_call *call, void *workspace, uint64_t workspace_bytes, uint64_t stream) {
-  const int8w_weight *w[3] = {gate, up, down};
-  Range ins[11];
-  for (int i = 0; i < 3; ++i) {
-    int rc = validate(w[i]);
-    if (rc) return rc;
-    if (w[i]->group_size != gate->group_size)
-      return fail(INT8W_ERR_SHAPE, "gate, up and down have different group sizes");
-    weight_ranges(w[i], ins + 3 * i);
-  }
-  int rc = check_moe(gate->out_features, gate->in_features, up->out_features, up->in_features, down->out_features,
-                     down->in_features, num_experts, call, workspace, workspace_bytes, ins, 9);
-  if (rc) return rc;
-  if (call->tokens == 0) return ok();
-  (void)hipGetLastError();
-  return finish_launch(launch_moe_int8(view(gate), view(up), view(down), moe_args(call, num_experts, workspace),
-                                       as_stream(stream)),
-                       as_stream(stream));
+  return moe_int8(gate, up, down, num_experts, call, workspace, workspace_bytes, stream);
 }
 
 int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down,
                           uint32_t num_experts, const int8w_moe_call *call, void *workspace,
                           uint64_t workspace_bytes, uint64_t stream) {
-  const int8w_mxfp4 *w[3] = {gate, up, down};
-  const char *const names[3] = {"gate", "up", "down"};
-  Range ins[8];
-  for (int i = 0; i < 3; ++i) {
-    int rc = validate_mx(w[i], names[i]);
-    if (rc) return rc;
-    ranges_of(w[i], ins + 2 * i);
-  }
-  int rc = check_moe(gate->rows, gate->k, up->rows, up->k, down->rows, down->k, num_experts, call, workspace,
-                     workspace_bytes, ins, 6);
+  return moe_mx(gate, up, down, num_experts, call, workspace, workspace_bytes, stream);
+}
+
+int int8_moe_layer_routed(const int8w_weight *gate, const int8w_weight *up, const int8w_weight *down,
+                          uint32_t num_experts, const int8w_moe_routed_call *call, void *workspace,
+                          uint64_t workspace_bytes, uint64_t stream) {
+  return moe_int8(gate, up, down, num_experts, call, workspace, workspace_bytes, stream);
+}
+
+int int8w_mxfp4_moe_layer_routed(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const int8w_mxfp4 *down,
+                                 uint32_t num_experts, const int8w_moe_routed_call *call, void *workspace,
+                                 uint64_t workspace_bytes, uint64_t stream) {
+  return moe_mx(gate, up, down, num_experts, call, workspace, workspace_bytes, stream);
+}
+
+// ---- the routing by itself
+
+int int8w_moe_route(const int8w_route_call *c, uint64_t stream) {
+  if (!c) return fail(INT8W_ERR_NULL, "call is NULL");
+  const uint32_t E = c->num_experts;
+  if (E == 0 || E > INT8W_MAX_MOE_EXPERTS) return fail(INT8W_ERR_SHAPE, "num_experts %u outside 1..%d", E, INT8W_MAX_MOE_EXPERTS);
+  if (c->topk == 0 || c->topk > INT8W_MAX_MOE_TOPK || c->topk > E)
+    return fail(INT8W_ERR_SHAPE, "topk %u outside 1..min(%u experts, %d)", c->topk, E, INT8W_MAX_MOE_TOPK);
+  if (c->logits_format > INT8W_VALUES_F32) return fail(INT8W_ERR_UNSUPPORTED, "unknown logits_format %u", c->logits_format);
+  if (c->scoring > INT8W_ROUTE_SIGMOID) return fail(INT8W_ERR_UNSUPPORTED, "unknown scoring %u", c->scoring);
+  if (c->group_score > INT8W_GROUP_TOP2) return fail(INT8W_ERR_UNSUPPORTED, "unknown group_score %u", c->group_score);
+  if (c->groups == 0 || c->groups > INT8W_MAX_MOE_GROUPS || E % c->groups != 0)
+    return fail(INT8W_ERR_SHAPE, "%u groups: outside 1..%d, or not dividing %u experts", c->groups, INT8W_MAX_MOE_GROUPS, E);
+  if (c->topk_groups == 0 || c->topk_groups > c->groups)
+    return fail(INT8W_ERR_SHAPE, "topk_groups %u outside 1..%u", c->topk_groups, c->groups);
+  if (c->topk > c->topk_groups * (E / c->groups))
+    return fail(INT8W_ERR_SHAPE, "topk %u of %u groups of %u experts", c->topk, c->topk_groups, E / c->groups);
+  if (c->tokens == 0) return ok();
+  if (!c->logits || !c->ids || !c->weights) return fail(INT8W_ERR_NULL, "logits, ids or weights is NULL");
+  const uint32_t el = c->logits_format == INT8W_VALUES_F32 ? 4 : 2;
+  if (!aligned(c->logits, el)) return fail(INT8W_ERR_ALIGN, "logits is not %u-byte aligned", el);
+  if (!aligned(c->bias, 4) || !aligned(c->ids, 4) || !aligned(c->weights, 4))
+    return fail(INT8W_ERR_ALIGN, "bias, ids or weights is not 4-byte aligned");
+  const uint64_t T = c->tokens;
+  const Range ins[2] = {range("logits", c->logits, T * E * el), range("bias", c->bias, c->bias ? E * 4ull : 0)};
+  const Range ids = range("ids", c->ids, T * c->topk * 4), weights = range("weights", c->weights, T * c->topk * 4);
+  int rc = check_alias(ids, ins, 2);
+  if (!rc) rc = check_alias(weights, ins, 2);
+  if (!rc) rc = check_alias(weights, &ids, 1);
   if (rc) return rc;
-  if (call->tokens == 0) return ok();
+  RouteArgs a = {};
+  a.logits = c->logits;
+  a.bias = c->bias;
+  a.ids = c->ids;
+  a.weights = c->weights;
+  a.tokens = c->tokens;
+  a.E = E;
+  a.topk = c->topk;
+  a.groups = c->groups;
+  a.topk_groups = c->topk_groups;
+  a.logits_bf16 = c->logits_format == INT8W_VALUES_BF16;
+  a.sigmoid = c->scoring == INT8W_ROUTE_SIGMOID;
+  a.top2 = c->group_score == INT8W_GROUP_TOP2;
+  a.renorm = c->renormalize != 0;
+  a.scale = c->routed_scale;
   (void)hipGetLastError();
-  return finish_launch(launch_moe_mx(view(gate), view(up), view(down), moe_args(call, num_experts, workspace),
-                                     as_stream(stream)),
-                       as_stream(stream));
+  return finish_launch(launch_route(a, as_stream(stream)), as_stream(stream));
+}
+
+// ---- low-rank adapters
+
+uint64_t int8w_lora_workspace_bytes(const int8w_lora *pools, uint32_t count, uint32_t m) {
+  if (validate_lora_pools(pools, count, m) != INT8W_OK || m == 0) return 0;
+  uint64_t offsets[INT8W_MAX_MULTI];
+  return lora_workspace(lora_args(pools, count, m), offsets);
+}
+
+int int8w_lora_add(const int8w_lora *pools, const int8w_lora_out *out, uint32_t count, const uint16_t *x,
+                   uint64_t x_stride, const uint32_t *ids, uint32_t m, void *workspace, uint64_t workspace_bytes,
+                   uint64_t stream) {
+  int rc = validate_lora_pools(pools, count, m);
+  if (rc) return rc;
+  if (m == 0) return ok();
+  if (!out || !x || !ids || !workspace) return fail(INT8W_ERR_NULL, "out, x, ids or workspace is NULL");
+  LoraArgs a = lora_args(pools, count, m);
+  constexpr uint64_t kMaxStride = 1ull << 32;
+  if (x_stride < a.K || x_stride % 8u != 0 || x_stride > kMaxStride)
+    return fail(INT8W_ERR_SHAPE, "x_stride %llu: below in_features %u, not a multiple of 8, or above 2^32",
+                (unsigned long long)x_stride, a.K);
+  if (!aligned(x, 16)) return fail(INT8W_ERR_ALIGN, "x is not 16-byte aligned");
+  if (!aligned(ids, 4)) return fail(INT8W_ERR_ALIGN, "ids is not 4-byte aligned");
+  if (!aligned(workspace, 256)) return fail(INT8W_ERR_ALIGN, "workspace is not 256-byte aligned");
+  uint64_t offsets[INT8W_MAX_MULTI];
+  const uint64_t need = lora_workspace(a, offsets);
+  if (workspace_bytes < need)
+    return fail(INT8W_ERR_SHAPE, "workspace of %llu bytes, this call needs %llu", (unsigned long long)workspace_bytes,
+                (unsigned long long)need);
+  const Range work = range("workspace", workspace, need);
+  Range ins[2 + 4 * INT8W_MAX_MULTI];
+  int n_ins = 0;
+  ins[n_ins++] = Rows{"x", reinterpret_cast<uintptr_t>(x), a.K, x_stride, m}.span();
+  ins[n_ins++] = range("ids", ids, (uint64_t)m * 4u);
+  for (uint32_t i = 0; i < count; ++i) {
+    const uint64_t num = a.num, R = a.s[i].R;
+    ins[n_ins++] = range("a", a.s[i].a, num * R * a.K * 2u);
+    ins[n_ins++] = range("b", a.s[i].b, num * R * a.s[i].N * 2u);
+    ins[n_ins++] = range("scales", a.s[i].scales, a.s[i].scales ? num * 4u : 0u);
+    ins[n_ins++] = range("ranks", a.s[i].ranks, a.s[i].ranks ? num * 4u : 0u);
+  }
+  rc = check_alias(work, ins, n_ins);
+  if (rc) return rc;
+  Rows y[INT8W_MAX_MULTI], base[INT8W_MAX_MULTI];
+  for (uint32_t i = 0; i < count; ++i) {
+    const uint32_t N = a.s[i].N;
+    if (!out[i].y) return fail(INT8W_ERR_NULL, "y is NULL");
+    if (!aligned(out[i].y, 2) || !aligned(out[i].base, 2)) return fail(INT8W_ERR_ALIGN, "y/base are not 2-byte aligned");
+    if (out[i].y_stride < N || out[i].y_stride > kMaxStride ||
+        (out[i].base && (out[i].base_stride < N || out[i].base_stride > kMaxStride)))
+      return fail(INT8W_ERR_SHAPE, "y_stride or base_stride below out_features %u or above 2^32", N);
+    y[i] = Rows{"y", reinterpret_cast<uintptr_t>(out[i].y), N, out[i].y_stride, m};
+    base[i] = Rows{"base", reinterpret_cast<uintptr_t>(out[i].base), N, out[i].base_stride, m};
+    a.s[i].base = out[i].base;
+    a.s[i].base_stride = out[i].base_stride;
+    a.s[i].y = out[i].y;
+    a.s[i].y_stride = out[i].y_stride;
+  }
+  const Rows xr = {"x", reinterpret_cast<uintptr_t>(x), a.K, x_stride, m};
+  for (uint32_t i = 0; i < count; ++i) {
+    if (rows_overlap(y[i], xr)) return fail(INT8W_ERR_ALIAS, "output y overlaps input x");
+    rc = check_alias(y[i].span(), ins + 1, n_ins - 1);
+    if (rc) return rc;
+    if (overlaps(y[i].span(), work) || (out[i].base && overlaps(base[i].span(), work)))
+      return fail(INT8W_ERR_ALIAS, "workspace overlaps y or base");
+    for (uint32_t j = 0; j < count; ++j) {
+      if (j < i && rows_overlap(y[i], y[j])) return fail(INT8W_ERR_ALIAS, "two outputs y overlap");
+      const bool in_place = i == j && out[i].base == out[i].y && out[i].base_stride == out[i].y_stride;
+      if (out[j].base && !in_place && rows_overlap(y[i], base[j])) return fail(INT8W_ERR_ALIAS, "output y overlaps input base");
+    }
+  }
+  a.x = x;
+  a.x_stride = x_stride;
+  a.ids = ids;
+  (void)hipGetLastError();
+  return finish_launch(launch_lora(a, workspace, as_stream(stream)), as_stream(stream));
 }
 
 }  // extern "C"

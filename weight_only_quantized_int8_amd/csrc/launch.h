@@ -126,7 +126,9 @@ constexpr uint64_t kMoeHeadBytes = 48u << 10;   // routing tables at the head of
 struct MoeArgs {
   uint32_t E;
   const uint16_t *x;    // [tokens, H]
-  const void *logits;   // [tokens, E], f32 or BF16
+  const void *logits;   // [tokens, E], f32 or BF16; or nullptr:
+  const uint32_t *ids;  // [tokens, topk] and
+  const float *weights; // [tokens, topk], the given routing
   bool logits_bf16;
   uint32_t tokens, topk;
   bool renorm;
@@ -138,6 +140,43 @@ struct MoeArgs {
 hipError_t launch_moe_int8(const WeightView &gate, const WeightView &up, const WeightView &down, const MoeArgs &m,
                            hipStream_t stream);
 hipError_t launch_moe_mx(const MxView &gate, const MxView &up, const MxView &down, const MoeArgs &m, hipStream_t stream);
+
+// ---- routing by itself
+struct RouteArgs {
+  const void *logits;  // [tokens, E], f32 or BF16
+  const float *bias;   // [E] or nullptr
+  uint32_t *ids;       // [tokens, topk]
+  float *weights;
+  uint32_t tokens, E, topk, groups, topk_groups;
+  uint32_t group_size, group_magic;  // set by the launcher
+  bool logits_bf16, sigmoid, top2, renorm;
+  float scale;
+};
+hipError_t launch_route(RouteArgs a, hipStream_t stream);
+
+// ---- low-rank adapters
+struct LoraStack {
+  const uint16_t *a;      // [num, R, K]
+  const uint16_t *b;      // [num, N, R]
+  const float *scales;    // [num] or nullptr
+  const uint32_t *ranks;  // [num] or nullptr
+  const uint16_t *base;   // [m, N] at base_stride, or nullptr
+  uint16_t *y;            // [m, N] at y_stride
+  uint64_t base_stride, y_stride;
+  uint32_t R, N;
+  float *u;  // [parts, m, R]: A x, by parts of K
+};
+struct LoraArgs {
+  LoraStack s[INT8W_MAX_MULTI];
+  const uint16_t *x;
+  uint64_t x_stride;
+  const uint32_t *ids;
+  uint32_t count, m, K, num;
+  uint32_t parts, part_k;  // set by the launcher
+};
+// Bytes of all the stacks' u, each 256-byte aligned; the offsets of the stacks.
+uint64_t lora_workspace(const LoraArgs &a, uint64_t *offsets);
+hipError_t launch_lora(LoraArgs a, void *ws, hipStream_t stream);
 
 // ---- C-ABI internals shared by capi.cpp and noalloc.hip
 // Records the calling thread's last error message and returns code.

@@ -31,6 +31,7 @@
 #include "rows_stream.h"
 #include "token_stream.h"
 #include "launch.h"
+#include "wave_ops.h"
 
 namespace int8w {
 
@@ -55,22 +56,6 @@ struct MoeHead {
   MoeSegment seg[kTok * kMaxTopk];
 };
 static_assert(sizeof(MoeHead) <= kMoeHeadBytes, "workspace head");
-
-// Maximum over the wave, in every lane, by data-parallel moves (a shuffle through LDS costs
-// over a hundred cycles, and top-k takes six a choice).
-__device__ __forceinline__ float wave_max(float v) {
-#define INT8W_DPP_MAX(ctrl, rows)                                                                                  \
-  v = fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(v), (int)__float_as_uint(v), \
-                                                                      ctrl, rows, 0xF, false)))
-  INT8W_DPP_MAX(0x111, 0xF);  // row_shr:1
-  INT8W_DPP_MAX(0x112, 0xF);
-  INT8W_DPP_MAX(0x114, 0xF);
-  INT8W_DPP_MAX(0x118, 0xF);
-  INT8W_DPP_MAX(0x142, 0xA);  // row_bcast:15
-  INT8W_DPP_MAX(0x143, 0xC);  // row_bcast:31
-#undef INT8W_DPP_MAX
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
-}
 
 // One wave routes one token.  Lane l holds the logits of experts l, l + 64, ...
 template <int R>  // ceil(E / 64) at most
@@ -135,9 +120,42 @@ struct RouteToken {
   }
 };
 
-// 16 waves; wave w routes tokens w, w + 16, ...; segments of up to C tokens.
+// One wave takes over a token's given routing.
+struct GivenToken {
+  uint32_t id;  // as in RouteToken, but choices that are none lie anywhere
+  float w;
+  __device__ __forceinline__ void load(const uint32_t *ids, const float *weights, uint32_t t, uint32_t topk, uint32_t lane) {
+    id = lane < topk ? ids[(size_t)t * topk + lane] : 0xFFFFFFFFu;
+    w = lane < topk ? weights[(size_t)t * topk + lane] : 0.f;
+  }
+  // Returns whether a weight is NaN (then nothing is chosen).  An expert named twice is
+  // taken at its first place with the weights added: a token has one bit of an expert's takers.
+  __device__ __forceinline__ bool choose(uint32_t topk, uint32_t E, uint32_t lane) {
+    const bool is_nan = __ballot(w != w) != 0ull;
+    if (id >= E || w == 0.f || is_nan) id = 0xFFFFu;
+    if (id == 0xFFFFu) w = 0.f;
+    for (uint32_t j = 1; j < topk; ++j) {
+      const uint32_t ij = (uint32_t)__builtin_amdgcn_readlane((int)id, (int)j);
+      const unsigned long long same = __ballot(id == ij);
+      if (ij == 0xFFFFu || (uint32_t)__builtin_ctzll(same) == j) continue;
+      const float wj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(w), (int)j));
+      if (lane == (uint32_t)__builtin_ctzll(same)) w += wj;
+      if (lane == j) {
+        id = 0xFFFFu;
+        w = 0.f;
+      }
+    }
+    if (w == 0.f) id = 0xFFFFu;  // added up to nothing
+    return is_nan;
+  }
+};
+
+// 16 waves; wave w routes tokens w, w + 16, ...; segments of up to C tokens.  Without logits
+// the routing is given.
 template <int R>
-__global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ logits, bool bf16, uint32_t T, uint32_t E,
+__global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ logits, bool bf16,
+                                                    const uint32_t *__restrict__ given_ids,
+                                                    const float *__restrict__ given_weights, uint32_t T, uint32_t E,
                                                     uint32_t topk, bool renorm, float scale, uint32_t C,
                                                     MoeHead *__restrict__ head) {
   __shared__ uint16_t ids[kTok * kMaxTopk];
@@ -148,13 +166,26 @@ __global__ __launch_bounds__(1024) void k_moe_route(const void *__restrict__ log
   if (tid < 64u * R) takers[tid] = 0ull;
   __syncthreads();
   for (uint32_t t = wave; t < T; t += 16u) {
-    RouteToken<R> route;
-    route.load(logits, bf16, t, E, lane);
-    const bool is_nan = route.choose(topk, renorm, scale, lane);
+    uint32_t id;
+    float w;
+    bool is_nan;
+    if (logits) {
+      RouteToken<R> route;
+      route.load(logits, bf16, t, E, lane);
+      is_nan = route.choose(topk, renorm, scale, lane);
+      id = route.id;
+      w = route.w;
+    } else {
+      GivenToken route;
+      route.load(given_ids, given_weights, t, topk, lane);
+      is_nan = route.choose(topk, E, lane);
+      id = route.id;
+      w = route.w;
+    }
     if (lane < topk) {
-      ids[t * topk + lane] = (uint16_t)route.id;
-      head->weight[t * topk + lane] = route.w;
-      if (route.id < kMaxE) atomicOr(&takers[route.id], 1ull << t);  // order-free
+      ids[t * topk + lane] = (uint16_t)id;
+      head->weight[t * topk + lane] = w;
+      if (id < kMaxE) atomicOr(&takers[id], 1ull << t);  // order-free
     }
     if (lane == 0) head->nan[t] = is_nan ? 1u : 0u;
   }
@@ -264,22 +295,40 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float *__restrict__ out, 
 // Two launches: each wave of the first routes the token itself (a few hundred cycles, against
 // a launch of its own), so that no kernel has to come before the first weight load.
 
-// Waves share the gate/up row pairs of the chosen experts evenly.  LDS: x.
+// Waves share the gate/up row pairs of the chosen experts evenly.  LDS: x.  R = 0: the routing
+// is given: `logits` are its ids.
 template <class F, int KW, int U, int R>
 __global__ __launch_bounds__(64 * KW) void k_moe1_up(typename F::View wg, typename F::View wu, uint32_t I,
                                                      const uint16_t *__restrict__ x, const void *__restrict__ logits,
-                                                     bool bf16, uint32_t E, uint32_t topk, bool renorm, float scale,
+                                                     const float *__restrict__ given_weights, bool bf16, uint32_t E,
+                                                     uint32_t topk, bool renorm, float scale,
                                                      MoeHead *__restrict__ head, uint16_t *__restrict__ h) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), K = wg.K, segs = token_segs<F>(K);
-  RouteToken<R> route;
-  route.load(logits, bf16, 0, E, lane);
+  typename std::conditional<R == 0, GivenToken, RouteToken<R == 0 ? 1 : R>>::type route;
+  if constexpr (R == 0)
+    route.load((const uint32_t *)logits, given_weights, 0, topk, lane);
+  else
+    route.load(logits, bf16, 0, E, lane);
   TokenStage<F> stage(x, K, 1u, threadIdx.x, 64u * KW);
   stage.load();
-  const bool is_nan = route.choose(topk, renorm, scale, lane);
-  const uint32_t id = route.id;
-  const float w = route.w;
-  const uint32_t n = (uint32_t)__popcll(__ballot(id < kMaxE));  // choices 0 .. n-1: their weights fall
+  bool is_nan;
+  if constexpr (R == 0)
+    is_nan = route.choose(topk, E, lane);
+  else
+    is_nan = route.choose(topk, renorm, scale, lane);
+  uint32_t id = route.id;
+  float w = route.w;
+  const unsigned long long some = __ballot(id < kMaxE);
+  const uint32_t n = (uint32_t)__popcll(some);  // choices 0 .. n-1: a router's weights fall
+  if constexpr (R == 0) {  // lane p: the p-th of the choices that are some
+    unsigned long long left = some;
+    for (uint32_t p = 0; p < lane && p < n; ++p) left &= left - 1ull;
+    const int from = left ? (int)__builtin_ctzll(left) : 0;
+    id = (uint32_t)__shfl((int)id, from, kWave);
+    w = __shfl(w, from, kWave);
+    if (lane >= n) id = 0xFFFFu;
+  }
   if (blockIdx.x == 0 && wave == 0) {
     if (lane < topk) {
       head->seg[lane].expert = id;
@@ -482,8 +531,8 @@ hipError_t launch_one_up(const typename F::View &g, const typename F::View &u, c
     if (e != hipSuccess) return e;
   }
   const uint32_t most = (uint32_t)device_cu_count(), want = (m.topk * I + KW - 1u) / KW;
-  kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits, m.logits_bf16, m.E, m.topk, m.renorm,
-                                                           m.scale, head, h);
+  kern<<<want < most ? want : most, 64 * KW, lds, stream>>>(g, u, I, m.x, m.logits ? m.logits : m.ids, m.weights,
+                                                           m.logits_bf16, m.E, m.topk, m.renorm, m.scale, head, h);
   return hipGetLastError();
 }
 
@@ -504,6 +553,7 @@ hipError_t launch_one_down(const typename F::View &d, const MoeArgs &m, MoeHead 
 template <class F, int KW>
 hipError_t launch_one_up_r(const typename F::View &g, const typename F::View &u, const MoeArgs &m, MoeHead *head,
                            uint16_t *h, uint32_t I, uint32_t lds, hipStream_t stream) {
+  if (!m.logits) return launch_one_up<F, KW, 0>(g, u, m, head, h, I, lds, stream);
   return m.E <= 64u ? launch_one_up<F, KW, 1>(g, u, m, head, h, I, lds, stream)
                     : m.E <= 128u ? launch_one_up<F, KW, 2>(g, u, m, head, h, I, lds, stream)
                                   : launch_one_up<F, KW, 8>(g, u, m, head, h, I, lds, stream);
@@ -539,11 +589,13 @@ hipError_t launch_layer(const typename F::View &g, const typename F::View &u, co
   constexpr int KW = F::kBlockWaves;
   for (uint32_t t0 = 0; t0 < m.tokens; t0 += kTok) {
     const uint32_t T = m.tokens - t0 < kTok ? m.tokens - t0 : kTok, slots = T * m.topk;
-    const uint8_t *logits = (const uint8_t *)m.logits + (size_t)t0 * m.E * (m.logits_bf16 ? 2u : 4u);
+    const void *logits = m.logits ? (const uint8_t *)m.logits + (size_t)t0 * m.E * (m.logits_bf16 ? 2u : 4u) : nullptr;
+    const size_t slot0 = (size_t)t0 * m.topk;
     // segments at most: one an expert taken, one more for each kSegTokens further tokens
     const uint32_t taken = slots < m.E ? slots : m.E, most = taken + (slots - taken) / kSegTokens;
     auto route = m.E <= 64u ? k_moe_route<1> : m.E <= 128u ? k_moe_route<2> : m.E <= 256u ? k_moe_route<4> : k_moe_route<8>;
-    route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, T, m.E, m.topk, m.renorm, m.scale, kSegTokens, head);
+    route<<<1, 1024, 0, stream>>>(logits, m.logits_bf16, logits ? nullptr : m.ids + slot0, logits ? nullptr : m.weights + slot0, T, m.E,
+                                 m.topk, m.renorm, m.scale, kSegTokens, head);
     const size_t at = (size_t)t0 * H;
     const uint32_t ub = (I + 16u * KW - 1u) / (16u * KW), db = (H + 16u * KW - 1u) / (16u * KW);
     // streamed past the caches where a row is whole cache lines (else neighbouring pieces share
