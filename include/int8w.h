@@ -388,7 +388,7 @@ typedef struct {
  * ids: uint32 [m], device.  m = 0 is a no-op.  workspace: device scratch, 256-byte aligned, of at least
  * int8w_lora_workspace_bytes(pools, count, m) bytes; no initial value, none kept; calls that share it must not overlap.
  * Errors: INT8W_ERR_NULL; INT8W_ERR_SHAPE (count outside 1..INT8W_MAX_MULTI, pools that do not fit
- * each other, sizes outside the limits, m above 2^21, a stride too small or above 2^32, a workspace
+ * each other, sizes outside the limits, m above 2^20, a stride too small or above 2^32, a workspace
  * too small); INT8W_ERR_ALIGN; INT8W_ERR_ALIAS (a y or the workspace overlapping an input or another y; columns
  * of one matrix, strides alike, do not overlap). */
 uint64_t int8w_lora_workspace_bytes(const int8w_lora *pools, uint32_t count, uint32_t m);

@@ -676,7 +676,7 @@ int validate_lora_pools(const int8w_lora *pools, uint32_t count, uint32_t m) {
     if (pools[i].num_adapters != pools->num_adapters || pools[i].in_features != pools->in_features)
       return fail(INT8W_ERR_SHAPE, "pools differ in num_adapters or in_features");
   }
-  if (m > (1u << 21)) return fail(INT8W_ERR_SHAPE, "m=%u rows are more than 2^21", m);
+  if (m > (1u << 20)) return fail(INT8W_ERR_SHAPE, "m=%u rows are more than 2^20", m);
   return INT8W_OK;
 }
 

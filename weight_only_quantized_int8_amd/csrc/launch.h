@@ -172,9 +172,12 @@ struct LoraArgs {
   uint64_t x_stride;
   const uint32_t *ids;
   uint32_t count, m, K, num;
-  uint32_t parts, part_k;  // set by the launcher
+  uint32_t parts, part_steps;  // of K, set by the launcher
+  void *plans;             // the workspace's head: groups of the rows of each kLoraPlanRows
 };
-// Bytes of all the stacks' u, each 256-byte aligned; the offsets of the stacks.
+constexpr uint32_t kLoraPlanRows = 1024;
+constexpr uint64_t kLoraPlanBytes = 273u << 10;
+// Bytes of the plans and all the stacks' u, each 256-byte aligned; the offsets of the stacks' u.
 uint64_t lora_workspace(const LoraArgs &a, uint64_t *offsets);
 hipError_t launch_lora(LoraArgs a, void *ws, hipStream_t stream);
 

@@ -3,258 +3,662 @@
 //   u[t] = A_e x[t],  y[t] = base[t] + scale_e B_e u[t],  e = ids[t];
 //   A_e [R, K], B_e [N, R], R far below K and N; id INT8W_NO_ADAPTER: y[t] = base[t].
 //
-// Two launches, on the matrix cores (16x16x32 products):
+// On the matrix cores (16x16x32 products), in two launches:
 //  shrink  u in fp32, K cut into `parts` (the sum over K is the long one, and a single token's
 //          A has to come through many CUs): u [parts, m, R] in the workspace.
 //  expand  sums the parts in their order, scales, multiplies by B_e, adds base, rounds once.
 //          u enters the matrix cores as the sum of two BF16 values (u's own rounding to one
 //          would be as large as the output's); the products are exact and summed in fp32.
-// No atomics: the same bits each time.
+// No atomics in any sum: the same bits each time.
 //
-// Both have two forms.  Few rows (rows form): a decode batch, rows in any order, mostly each with an
-// adapter of its own.  A workgroup stands for a row; of the rows that share an adapter each 16th
-// leads and its workgroup takes it and the next 15 (found by ballots over ids, read by every
-// wave), the others end at once: an adapter is streamed once for up to 16 rows wherever they are.
-// Many rows (tile form): windows of 64 neighbouring rows; a workgroup goes over the adapters
-// that occur in its window, for a prompt one or two.
-// A row is a column of the product, and columns do not mix: what another row or its adapter
+// A workgroup works on a group: rows with one adapter, wherever they are in the batch, so that its
+// matrices are read once for all of them; up to 16 rows with K or N shared out among its waves
+// ("few"), or up to 64 with the rows shared out ("many").
+//  Up to 64 rows in the batch: a workgroup stands for a row; of the rows that share an adapter each
+//   16th leads and takes the next 15 along, found by one ballot; the others end at once.
+//  More: a launch before the others (k_plan) sorts the rows of each 1024 into groups, which
+//   a fixed number of workgroups takes in turn.
+// A row is a row or column of the products, which do not mix: what another row or its adapter
 // holds (infinities, NaN) does not reach it.
-#include "common.h"
-#include "launch.h"
+#include "rows_stream.h"
 
 namespace int8w {
 
 namespace {
 
-constexpr uint32_t kRowsGroup = 16;   // rows of a workgroup in the rows form
-constexpr uint32_t kTileRows = 64;    // in the tile form
-constexpr uint32_t kStepK = 64;       // K of a wave's step: whole cache lines of A and x
-constexpr uint32_t kTileN = 256;      // output columns of a workgroup of four waves
-constexpr uint32_t kRowsMax = 256;    // most rows that the rows form takes
+constexpr uint32_t kFew = 16;         // rows of a group, with K or N shared out among the waves
+constexpr uint32_t kMany = 64;        // ... with the rows shared out
+constexpr uint32_t kBallotRows = 64;  // largest batch without a plan
+constexpr uint32_t kStepK = 64;       // K of a step: a cache line of a row
+constexpr uint32_t kBlockN = 128;     // output columns of a step
+constexpr uint32_t kShrinkBlocks = 512;
 
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+#define INT8W_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) >> 4) << 14) | 0x0F70 | ((n) & 15))
+#define INT8W_LGKMCNT0() __builtin_amdgcn_s_waitcnt(0xC07F)
 
-__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+// ---- DMA of 16 bytes a lane into LDS: lane l of the wave writes `to` + 16 l
+__device__ __align__(16) uint32_t g_zeros[4];  // what lanes beyond the end of K load
+
+__device__ __forceinline__ void dma(const uint16_t *from, uint8_t *to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t from, uint32_t off, uint8_t *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)off, 0, 0, 0);
 }
 
 // The adapter's own rank, rounded up to whole 16-byte pieces of a row of B.
 __device__ __forceinline__ uint32_t own_rank(const LoraStack &s, uint32_t e) {
   if (!s.ranks) return s.R;
-  const uint32_t r = (s.ranks[e] + 7u) & ~7u;
-  return r < s.R ? r : s.R;
+  const uint32_t r = s.ranks[e];
+  return r < s.R ? (r + 7u) & ~7u : s.R;
 }
 
-// Rows form: whether row i leads, and then list[0 .. n-1] = the rows of its group.  Every wave
-// finds the same and writes the same list.
-__device__ __forceinline__ bool gather_rows(const uint32_t *ids, uint32_t m, uint32_t i, uint32_t id, uint32_t lane,
-                                            uint32_t *list, uint32_t &n) {
-  uint32_t before = 0;
-  n = 0;
-  for (uint32_t j0 = 0; j0 < m && n < kRowsGroup; j0 += 64u) {
-    const uint32_t j = j0 + lane;
-    const unsigned long long same = __ballot(j < m && ids[j < m ? j : 0u] == id);
-    const unsigned long long mine = j0 + 64u <= i ? 0ull : j0 >= i ? ~0ull : ~0ull << (i - j0);  // rows from i on
-    before += (uint32_t)__popcll(same & ~mine);
-    const unsigned long long next = same & mine;
-    const uint32_t at = n + (uint32_t)__popcll(next & ((1ull << lane) - 1ull));
-    if ((next >> lane & 1ull) && at < kRowsGroup) list[at] = j;
-    n += (uint32_t)__popcll(next);
+// ---- groups --------------------------------------------------------------------------------
+
+// A batch of up to 64 rows: whether row i, with id, leads, and then list[0 .. n-1] = the rows of its
+// group.  Every wave finds the same and writes the same list.
+__device__ __forceinline__ bool gather_rows(uint32_t own, uint32_t i, uint32_t id, uint32_t lane, uint32_t *list, uint32_t &n) {
+  const unsigned long long same = __ballot(own == id), next = same >> i << i;
+  const uint32_t at = (uint32_t)__popcll(next & ((1ull << lane) - 1ull));
+  if ((next >> lane & 1ull) && at < kFew) list[at] = lane;
+  n = (uint32_t)__popcll(next);
+  if (n > kFew) n = kFew;
+  return (uint32_t)__popcll(same ^ next) % kFew == 0u;
+}
+
+struct PlanItem {
+  uint32_t e;  // adapter; num: rows without one; num + 1: rows with an id outside the pool
+  uint32_t n;  // 1 .. kMany
+  uint32_t pad[2];
+  uint32_t rows[kMany];  // of the batch
+};
+struct LoraPlan {  // of kLoraPlanRows rows
+  uint32_t items;
+  uint32_t steps;  // of K a part
+  uint32_t parts;
+  uint32_t pad[13];
+  PlanItem item[kLoraPlanRows];
+};
+static_assert(sizeof(LoraPlan) <= kLoraPlanBytes && kLoraPlanBytes % 256u == 0, "workspace");
+
+// Sorts the rows of a piece of the batch into groups; a thread has a row.  Rows with the same id
+// find each other in their wave by ballots over the id's bits, then across the waves by a
+// hash table in LDS with a count of each wave.  A row's place among the rows with its id goes by
+// their order in the batch, and so does the cut into groups; only where a group lies in the
+// plan depends on the atomics' order, and no result does.
+__global__ __launch_bounds__(kLoraPlanRows) void k_plan(const uint32_t *__restrict__ ids, uint32_t m, uint32_t num, uint32_t bits,
+                                                        uint32_t steps, uint32_t most_parts, uint32_t shrink_blocks,
+                                                        LoraPlan *__restrict__ plans) {
+  constexpr uint32_t kSlots = 2u * kLoraPlanRows, kWaves = kLoraPlanRows / 64u, kEmpty = 0xFFFFFFFFu;
+  static_assert(kWaves == 16u, "a slot's counts are 16 bytes");
+  __shared__ uint32_t key[kSlots];
+  __shared__ __attribute__((aligned(16))) uint8_t count[kSlots][kWaves];
+  __shared__ uint32_t item0[kSlots];
+  __shared__ uint32_t items;
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, t = blockIdx.x * kLoraPlanRows + tid;
+  LoraPlan &plan = plans[blockIdx.x];
+  const bool live = t < m;
+  const uint32_t id = live ? ids[t] : 0u, e = id < num ? id : id == INT8W_NO_ADAPTER ? num : num + 1u;
+  for (uint32_t i = tid; i < kSlots; i += kLoraPlanRows) {
+    key[i] = kEmpty;
+    *reinterpret_cast<uint4 *>(count[i]) = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (n > kRowsGroup) n = kRowsGroup;
-  return before % kRowsGroup == 0u;
-}
-
-// acc[t] += A rows 16 t .. 16 t + 15 of the step times x.  Lane (c, q) holds of a row 32 bytes
-// from k0 + 16 q: both operands alike, and a row's four lanes cover a cache line.
-template <int RT>
-struct ShrinkStep {
-  u32x4 x[2], a[RT][2];
-  __device__ __forceinline__ void load(const uint16_t *xrow, __amdgpu_buffer_rsrc_t ra, uint32_t K, uint32_t rank,
-                                       uint32_t k0, uint32_t lane) {
-    const uint32_t c = lane & 15u, k = k0 + 16u * (lane >> 4);
+  if (tid == 0u) items = 0u;
+  __syncthreads();
+  unsigned long long same = __ballot(live);
+  for (uint32_t b = 0; b < bits; ++b) {
+    const unsigned long long set = __ballot(e >> b & 1u);
+    same &= e >> b & 1u ? set : ~set;
+  }
+  const uint32_t leader = live ? (uint32_t)__builtin_ctzll(same) : lane;
+  uint32_t slot = 0;
+  if (live && lane == leader) {
+    slot = e * 2654435761u >> 21;  // of 2048; at most 1024 are taken, so a free one is found
+    while (true) {
+      const uint32_t was = atomicCAS(&key[slot], kEmpty, e);
+      if (was == kEmpty || was == e) break;
+      slot = (slot + 1u) % kSlots;
+    }
+    count[slot][wave] = (uint8_t)__popcll(same);
+  }
+  slot = (uint32_t)__shfl((int)slot, (int)leader, 64);
+  __syncthreads();
+  uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1ull)), total = 0;
+  const u32x4 c = *reinterpret_cast<const u32x4 *>(count[slot]);
 #pragma unroll
-    for (uint32_t h = 0; h < 2u; ++h) {
-      const bool in = k + 8u * h < K;
-      x[h] = *reinterpret_cast<const u32x4 *>(xrow + (in ? k + 8u * h : 0u));
-      if (!in) x[h] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (uint32_t t = 0; t < RT; ++t) {
-        const uint32_t r = 16u * t + c;
-        a[t][h] = buf_load_b128(ra, in && r < rank ? (r * K + k + 8u * h) * 2u : kOutOfRange);
-      }
+  for (uint32_t w = 0; w < kWaves; ++w) {
+    const uint32_t n = c[w / 4u] >> 8u * (w % 4u) & 0xFFu;
+    total += n;
+    if (w < wave) rank += n;
+  }
+  if (live && rank == 0u) item0[slot] = atomicAdd(&items, (total + kMany - 1u) / kMany);
+  __syncthreads();
+  if (live) {
+    PlanItem &it = plan.item[item0[slot] + rank / kMany];
+    it.rows[rank % kMany] = t;
+    if (rank % kMany == 0u) {
+      it.e = e;
+      it.n = total - rank < kMany ? total - rank : kMany;
     }
   }
-  __device__ __forceinline__ void multiply(f32x4 (&acc)[RT]) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int t = 0; t < RT; ++t) acc[t] = mfma(a[t][h], x[h], acc[t]);
+  if (tid == 0u) {  // K in as many parts as give each workgroup of shrink one
+    uint32_t parts = shrink_blocks / items;
+    parts = parts < 1u ? 1u : parts > most_parts ? most_parts : parts;
+    const uint32_t each = (steps + parts - 1u) / parts;
+    plan.items = items;
+    plan.steps = each;
+    plan.parts = (steps + each - 1u) / each;
+  }
+}
+
+// ---- shrink --------------------------------------------------------------------------------
+// A load in the layout of a matrix operand, neighbouring lanes in different rows, costs the
+// address unit a cycle a lane.  So rows come by DMA, eight lanes side by side on a row's cache
+// line (64 values, a step of K), and are read from LDS as operands.  Chunk p (16 bytes) of
+// row r lies at chunk row_swizzle<8>(r, p) of its row: no bank conflicts.
+
+// Operand `half` (32 of the 64 values) of 16 rows: row l%16, chunk 4 half + l/16.
+__device__ __forceinline__ u32x4 get_rows(const uint8_t *lds, uint32_t half, uint32_t lane) {
+  const uint32_t r = lane & 15u;
+  return *reinterpret_cast<const u32x4 *>(lds + 128u * r + 16u * row_swizzle<8>(r, 4u * half + (lane >> 4)));
+}
+// Byte offset of chunk p of row r of A at K 0 (from which K's, below 2^22, stays out of range).
+__device__ __forceinline__ uint32_t a_offset(uint32_t r, uint32_t rank, uint32_t K, uint32_t p) {
+  const uint32_t at = (r * K + 8u * p) * 2u;
+  return r < rank ? at : kOutOfRange;
+}
+
+// A part of K, from a step that differs from group to group: the same step of all rows of all
+// adapters tends to lie in the same memory channel.  `start` goes by the adapter or the rows, never
+// by a group's place in the plan, since the sum's order depends on it.
+struct PartK {
+  uint32_t first, end, steps, turn;
+  uint32_t part;
+  __device__ __forceinline__ PartK(const LoraArgs &g, uint32_t part_, uint32_t part_steps, uint32_t start) {
+    part = part_;
+    first = part * part_steps * kStepK;
+    end = first + part_steps * kStepK < g.K ? first + part_steps * kStepK : g.K;
+    steps = (end - first + kStepK - 1u) / kStepK;
+    turn = start % steps;
+  }
+  __device__ __forceinline__ uint32_t at(uint32_t step) const {  // `end` beyond the last step
+    const uint32_t turned = step + turn < steps ? step + turn : step + turn - steps;
+    return step < steps ? first + turned * kStepK : end;
   }
 };
 
-// grid (parts, rows, stacks).  The four waves of a workgroup take steps of the part in turn.
+// u of the n <= 16 rows in `list` (LDS, may lie where lds does), this part of K.  The four waves
+// take steps in turn, each with two stages of its own in LDS; their sums are added up there.
+template <int RT>  // 16-row tiles of A at a time
+struct ShrinkFew {
+  static constexpr uint32_t kStage = (RT + 1) * 2048u;  // A, then x
+  static constexpr uint32_t kLds = 4u * 2u * kStage;
+  static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
+                                             const PartK &part_k, uint8_t *lds, uint32_t lane, uint32_t wave) {
+    const uint32_t r = lane >> 3, rank = own_rank(s, e);
+    uint8_t *const mine = lds + wave * 2u * kStage;
+    // load j: rows 8 j + l/8; chunk l%8 in LDS is this one of the row
+    const uint32_t p0 = 8u * row_swizzle<8>(r, lane & 7u), p1 = 8u * row_swizzle<8>(8u + r, lane & 7u);
+    const uint16_t *const x0 = g.x + list[r < n ? r : 0u] * g.x_stride + p0;  // rows from n on: any, unused
+    const uint16_t *const x1 = g.x + list[8u + r < n ? 8u + r : 0u] * g.x_stride + p1;
+    const uint32_t out_row = list[(threadIdx.x & 15u) < n ? threadIdx.x & 15u : 0u];
+    __syncthreads();
+    const auto ra = make_rsrc(s.a + (size_t)e * s.R * g.K, s.R * g.K * 2u);
+    const bool more = n > 8u;
+    for (uint32_t r0 = 0; r0 < s.R; r0 += 16u * RT) {
+      f32x4 acc[RT] = {};
+      uint32_t oa[2 * RT];
+#pragma unroll
+      for (uint32_t j = 0; j < 2u * RT; ++j) oa[j] = a_offset(r0 + 8u * j + r, rank, g.K, (j & 1u ? p1 : p0) / 8u);
+      auto load = [&](uint32_t step, uint8_t *to) {  // beyond the part: zeros, without touching A or x
+        const uint32_t at = part_k.at(step);
+        const bool in0 = at + p0 < part_k.end, in1 = at + p1 < part_k.end;
+#pragma unroll
+        for (uint32_t j = 0; j < 2u * RT; ++j) dma(ra, (j & 1u ? in1 : in0) ? oa[j] + 2u * at : kOutOfRange, to + 1024u * j);
+        dma(in0 ? x0 + at : (const uint16_t *)g_zeros, to + 2048u * RT);
+        if (more) dma(in1 ? x1 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 1024u);
+      };
+      auto step = [&](uint8_t *at, uint32_t next) {  // one stage: await, read, refill, multiply
+        if (more)
+          INT8W_VMCNT(2 * RT + 2);
+        else
+          INT8W_VMCNT(2 * RT + 1);
+        keep_order();
+        u32x4 a[RT][2], x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[h] = get_rows(at + 2048u * RT, h, lane);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) a[t][h] = get_rows(at + 2048u * t, h, lane);
+        }
+        INT8W_LGKMCNT0();  // read before it is written again
+        keep_order();
+        load(next, at);
+        keep_order();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[t] = mfma16(a[t][h], x[h], acc[t]);
+      };
+      uint32_t b = wave;
+      if (r0 < rank && b < part_k.steps) {
+        load(b, mine);
+        load(b + 4u, mine + kStage);
+        while (true) {
+          step(mine, b + 8u);
+          if ((b += 4u) >= part_k.steps) break;
+          step(mine + kStage, b + 8u);
+          if ((b += 4u) >= part_k.steps) break;
+        }
+        INT8W_VMCNT(0);  // the look-ahead has landed
+      }
+      __syncthreads();
+      // acc[t]: row 16 t + 4 (l / 16) + i of the tile for row l%16 of the group
+      f32x4 *const sums = reinterpret_cast<f32x4 *>(lds);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) sums[(wave * RT + t) * 64u + lane] = acc[t];
+      __syncthreads();
+      const uint32_t p = threadIdx.x, row = r0 + 16u * (p >> 6) + 4u * (p >> 4 & 3u);
+      if (p < RT * 64u && (p & 15u) < n && row < s.R) {
+        f32x4 v = sums[p];
+#pragma unroll
+        for (uint32_t w = 1; w < 4u; ++w) v += sums[w * RT * 64u + p];
+        *reinterpret_cast<f32x4 *>(s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = v;
+      }
+      __syncthreads();
+    }
+  }
+};
+
+// The same for up to 64 rows: a wave has 16 of them, A is shared.  NS stages in LDS, one barrier a step.
+template <int RT>
+struct ShrinkMany {
+  static constexpr uint32_t kStage = (RT + 4) * 2048u;  // A, then x
+  static constexpr int NS = 4;
+  static constexpr uint32_t kLds = NS * kStage;
+  static constexpr int kA = RT >= 2 ? RT / 2 : 1;  // loads of A a wave (of one tile: waves 2 and 3 repeat them)
+  static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
+                                             const PartK &part_k, uint8_t *lds, uint32_t lane, uint32_t wave) {
+    const uint32_t r = lane >> 3, rank = own_rank(s, e);
+    const uint32_t p0 = 8u * row_swizzle<8>(r, lane & 7u), p1 = 8u * row_swizzle<8>(8u + r, lane & 7u);
+    const uint32_t i0 = 16u * wave + r, i1 = i0 + 8u, io = 16u * wave + (lane & 15u);
+    const uint16_t *const x0 = g.x + list[i0 < n ? i0 : 0u] * g.x_stride + p0;
+    const uint16_t *const x1 = g.x + list[i1 < n ? i1 : 0u] * g.x_stride + p1;
+    const uint32_t out_row = list[io < n ? io : 0u];
+    __syncthreads();
+    const auto ra = make_rsrc(s.a + (size_t)e * s.R * g.K, s.R * g.K * 2u);
+    for (uint32_t r0 = 0; r0 < s.R; r0 += 16u * RT) {
+      f32x4 acc[RT] = {};
+      if (r0 < rank) {
+        uint32_t oa[kA], pa[kA];
+#pragma unroll
+        for (uint32_t i = 0; i < kA; ++i) {
+          const uint32_t j = (wave * kA + i) % (2u * RT);
+          pa[i] = j & 1u ? p1 : p0;
+          oa[i] = a_offset(r0 + 8u * j + r, rank, g.K, pa[i] / 8u);
+        }
+        auto load = [&](uint32_t step, uint8_t *to) {
+          const uint32_t at = part_k.at(step);
+#pragma unroll
+          for (uint32_t i = 0; i < kA; ++i)
+            dma(ra, at + pa[i] < part_k.end ? oa[i] + 2u * at : kOutOfRange, to + (wave * kA + i) % (2u * RT) * 1024u);
+          dma(at + p0 < part_k.end ? x0 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 2048u * wave);
+          dma(at + p1 < part_k.end ? x1 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 2048u * wave + 1024u);
+          keep_order();
+        };
+#pragma unroll
+        for (int i = 0; i < NS - 1; ++i) load(i, lds + i * kStage);
+        for (uint32_t b = 0; b < part_k.steps;) {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            // this wave's loads of step b have landed; the barrier makes all of them visible, and frees step b - 1's stage
+            INT8W_VMCNT((NS - 2) * (kA + 2));
+            INT8W_LGKMCNT0();
+            asm volatile("s_barrier" ::: "memory");
+            load(b + NS - 1u, lds + (i + NS - 1) % NS * kStage);
+            const uint8_t *const at = lds + i * kStage;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const u32x4 x = get_rows(at + 2048u * RT + 2048u * wave, h, lane);
+#pragma unroll
+              for (int t = 0; t < RT; ++t) acc[t] = mfma16(get_rows(at + 2048u * t, h, lane), x, acc[t]);
+            }
+            if (++b >= part_k.steps) break;
+          }
+        }
+        INT8W_VMCNT(0);  // the look-ahead has landed
+        __syncthreads();
+      }
+#pragma unroll
+      for (uint32_t t = 0; t < RT; ++t) {
+        const uint32_t row = r0 + 16u * t + 4u * (lane >> 4);
+        if (io < n && row < s.R) *reinterpret_cast<f32x4 *>(s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = acc[t];
+      }
+    }
+  }
+};
+
+// grid (parts, rows, stacks).
 template <int RT>
 __global__ __launch_bounds__(256) void k_shrink_rows(const LoraArgs g) {
-  __shared__ uint32_t list[kRowsGroup];
-  constexpr int kTiles = RT < 4 ? RT : 4;  // added up at a time
-  __shared__ f32x4 sums[4][kTiles * 64];
-  const LoraStack &s = g.s[blockIdx.z];
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6), part = blockIdx.x, i = blockIdx.y;
-  const uint32_t id = uniform(g.ids[i]);
-  if (id >= g.num) return;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  uint32_t *const list = reinterpret_cast<uint32_t *>(lds);
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), i = blockIdx.y;
+  const uint32_t own = lane < g.m ? g.ids[lane] : INT8W_NO_ADAPTER, id = (uint32_t)__builtin_amdgcn_readlane((int)own, (int)i);
   uint32_t n;
-  if (!gather_rows(g.ids, g.m, i, id, lane, list, n)) return;
+  if (id >= g.num || !gather_rows(own, i, id, lane, list, n)) return;
   __syncthreads();
-  const uint32_t c = lane & 15u, rank = own_rank(s, id);
-  const uint16_t *xrow = g.x + list[c < n ? c : 0u] * g.x_stride;  // columns from n on repeat a row, unused
-  const auto ra = make_rsrc(s.a + (size_t)id * s.R * g.K, s.R * g.K * 2u);
-  f32x4 acc[RT] = {};
-  const uint32_t k1 = (part + 1u) * g.part_k < g.K ? (part + 1u) * g.part_k : g.K;
-  for (uint32_t k0 = part * g.part_k + wave * kStepK; k0 < k1; k0 += 4u * kStepK) {
-    ShrinkStep<RT> step;
-    step.load(xrow, ra, g.K, rank, k0, lane);
-    step.multiply(acc);
-  }
-#pragma unroll
-  for (int t0 = 0; t0 < RT; t0 += kTiles) {
-    if (t0) __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) sums[wave][64 * t + lane] = acc[t0 + t];
-    __syncthreads();
-    const uint32_t p = threadIdx.x, r = 16u * (t0 + (p >> 6)) + 4u * (p >> 4 & 3u), col = p & 15u;
-    if (p < kTiles * 64u && col < n && r < s.R) {
-      const f32x4 v = (sums[0][p] + sums[1][p]) + (sums[2][p] + sums[3][p]);
-      *reinterpret_cast<f32x4 *>(s.u + ((size_t)part * g.m + list[col]) * s.R + r) = v;
-    }
-  }
+  ShrinkFew<RT>::run(g, g.s[blockIdx.z], id, list, n, PartK(g, blockIdx.x, g.part_steps, id), lds, lane, wave);
 }
 
-// grid (parts, windows, stacks).  A wave has 16 of the window's rows.
+// Group i of a plan: f(adapter, n) with its rows in `list`.
+template <class F>
+__device__ __forceinline__ void with_item(const LoraPlan &plan, uint32_t i, uint32_t *list, F f) {
+  const PlanItem &it = plan.item[i];
+  const uint32_t row = threadIdx.x < kMany ? it.rows[threadIdx.x] : 0u;  // beyond n: no row, unused
+  const uint32_t e = uniform32(it.e), n = uniform32(it.n);
+  __syncthreads();  // the last group is done with
+  if (threadIdx.x < kMany) list[threadIdx.x] = row;
+  __syncthreads();
+  f(e, n);
+}
+
+// grid (blocks, plans, stacks): the blocks take the groups' parts in turn.
 template <int RT>
-__global__ __launch_bounds__(256) void k_shrink_tile(const LoraArgs g) {
+__global__ __launch_bounds__(256) void k_shrink_items(const LoraArgs g) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  uint32_t *const list = reinterpret_cast<uint32_t *>(lds);
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6);
   const LoraStack &s = g.s[blockIdx.z];
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6), part = blockIdx.x;
-  const uint32_t row = blockIdx.y * kTileRows + 16u * wave + (lane & 15u);
-  uint32_t id = row < g.m ? g.ids[row] : INT8W_NO_ADAPTER;
-  if (id >= g.num) id = INT8W_NO_ADAPTER;
-  const uint16_t *xrow = g.x + (row < g.m ? row : g.m - 1u) * g.x_stride;
-  const uint32_t k1 = (part + 1u) * g.part_k < g.K ? (part + 1u) * g.part_k : g.K;
-  unsigned long long left = __ballot(id != INT8W_NO_ADAPTER);
-  while (left) {
-    const uint32_t e = (uint32_t)__builtin_amdgcn_readlane((int)id, __builtin_ctzll(left));
-    left &= ~__ballot(id == e);
-    const uint32_t rank = own_rank(s, e);
-    const auto ra = make_rsrc(s.a + (size_t)e * s.R * g.K, s.R * g.K * 2u);
-    f32x4 acc[RT] = {};
-    for (uint32_t k0 = part * g.part_k; k0 < k1; k0 += kStepK) {
-      ShrinkStep<RT> step;
-      step.load(xrow, ra, g.K, rank, k0, lane);
-      step.multiply(acc);
-    }
-    if (id == e) {
-#pragma unroll
-      for (uint32_t t = 0; t < RT; ++t) {
-        const uint32_t r = 16u * t + 4u * (lane >> 4);
-        if (r < s.R) *reinterpret_cast<f32x4 *>(s.u + ((size_t)part * g.m + row) * s.R + r) = acc[t];
-      }
-    }
+  const LoraPlan &plan = reinterpret_cast<const LoraPlan *>(g.plans)[blockIdx.y];
+  const uint32_t parts = uniform32(plan.parts), steps = uniform32(plan.steps), end = uniform32(plan.items) * parts;
+  for (uint32_t i = blockIdx.x; i < end; i += gridDim.x) {
+    with_item(plan, i / parts, list, [&](uint32_t e, uint32_t n) {
+      if (e >= g.num) return;
+      const PartK part_k(g, i % parts, steps, n <= kFew ? e : list[0] / kMany);
+      if (n <= kFew)
+        ShrinkFew<RT>::run(g, s, e, list, n, part_k, lds, lane, wave);
+      else
+        ShrinkMany<RT>::run(g, s, e, list, n, part_k, lds, lane, wave);
+    });
   }
 }
 
-// u of up to ROWS rows in LDS: summed over the parts, scaled, as two BF16 values.  A row is
-// padded by 16 bytes so that the sixteen rows of an operand lie in different banks.
-template <int KS>  // steps of 32 of the rank
-struct ExpandU {
-  static constexpr uint32_t kRow = 64u * KS + 16u;
-  // Thread's share of rows x rank; row(c) >= m: zeros.
-  template <class Row, class Scale>
-  static __device__ __forceinline__ void stage(uint8_t *hi, uint8_t *lo, const LoraArgs &g, const LoraStack &s, uint32_t rows,
-                                               Row row, Scale scale) {
-    for (uint32_t p = threadIdx.x; p < rows * 8u * KS; p += blockDim.x) {
-      const uint32_t c = p / (8u * KS), r = 4u * (p % (8u * KS)), t = row(c);
-      f32x4 v = {};
-      if (t < g.m && r < s.R) {
-        const float *from = s.u + (size_t)t * s.R + r;
-        for (uint32_t i = 0; i < g.parts; ++i) v += *reinterpret_cast<const f32x4 *>(from + (size_t)i * g.m * s.R);
-        v *= scale(c);
-      }
-      uint2 h = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      // a value beyond BF16's range has an infinity for its upper part and NaN for the difference
-      float d[4] = {v[0] - bf16_lo(h.x), v[1] - bf16_hi(h.x), v[2] - bf16_lo(h.y), v[3] - bf16_hi(h.y)};
+// ---- expand --------------------------------------------------------------------------------
+// The product has u's rows as rows and B's as columns: a result register of lane (c, q) holds row
+// 4 q + i, column c of a tile.  Tile t of a block's eight takes columns 8 c + t, so that a lane
+// has eight neighbouring columns and 16 lanes a row's 256 bytes.
+// A block of B, 128 columns, comes by DMA, P chunks of 16 bytes a column at a time (P = 2 or 4: the
+// whole rank; 8: 64 of it).  LDS row 16 t + c is column 8 c + t.
+
+template <int P>
+__device__ __forceinline__ uint32_t b_swizzle(uint32_t c, uint32_t p) {  // as quarter_at() for 4
+  if constexpr (P == 2) return p;
+  if constexpr (P == 4) return p ^ ((c >> 1) & 3u);
+  return row_swizzle<8>(c, p);
+}
+
+// Load j of the 2 P of a block's rank chunk r0.  n0: its first column.
+template <int P>
+__device__ __forceinline__ void dma_b(__amdgpu_buffer_rsrc_t rb, uint32_t R, uint32_t rank, uint32_t n0, uint32_t r0, uint32_t j,
+                                      uint8_t *to, uint32_t lane) {
+  const uint32_t row = (64u * j + lane) / P, c = row & 15u, t = row >> 4;
+  const uint32_t r = r0 + 8u * b_swizzle<P>(c, lane % P), n = n0 + 8u * c + t;  // a column past the last one: zeros by the resource
+  dma(rb, r < rank ? (n * R + r) * 2u : kOutOfRange, to + 1024u * j);
+}
+
+// u of 16 rows as operands: lane (c, q) of row c.  P = 2: one operand, the upper BF16 values in
+// lane groups 0 and 1, the lower in 2 and 3, against the same columns of B in both.
+template <int P, int NCH>
+struct UOperand {
+  static constexpr int kSteps = P == 8 ? 2 : 1, kAll = kSteps * NCH;
+  u32x4 hi[kAll], lo[P == 2 ? 1 : kAll];
+};
+
+// Two BF16 values that add up to each of eight.  A value beyond BF16's range has an infinity for
+// its upper part, and no lower one.
+__device__ __forceinline__ void split_bf16(const f32x4 &a, const f32x4 &b, u32x4 &hi, u32x4 &lo) {
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = fabsf(d[i]) < __builtin_inff() ? d[i] : 0.f;
-      *reinterpret_cast<uint2 *>(hi + c * kRow + 2u * r) = h;
-      *reinterpret_cast<uint2 *>(lo + c * kRow + 2u * r) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    float d0 = v[2 * i] - bf16_lo(hi[i]), d1 = v[2 * i + 1] - bf16_hi(hi[i]);
+    d0 = fabsf(d0) < __builtin_inff() ? d0 : 0.f;
+    d1 = fabsf(d1) < __builtin_inff() ? d1 : 0.f;
+    lo[i] = pack_bf16x2(d0, d1);
+  }
+}
+
+// u of one row: COUNT pieces of four values, piece i from offset at(i) of the row, the parts added in their
+// order and scaled.  All pieces of several parts are in flight at a time.
+template <int COUNT, class At>
+__device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, const LoraStack &s, uint32_t row, uint32_t parts,
+                                          float scale, At at) {
+  constexpr uint32_t kAhead = COUNT >= 16 ? 1 : 16 / COUNT;
+  const float *from = s.u + (size_t)row * s.R;
+  const size_t next = (size_t)g.m * s.R;
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t p = 0; p < parts; p += kAhead) {
+    f32x4 w[kAhead][COUNT];
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) {
+        w[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (p + j < parts && at(i) < s.R) w[j][i] = *reinterpret_cast<const f32x4 *>(from + (p + j) * next + at(i));
+      }
+    keep_order();
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) v[i] += w[j][i];
+  }
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) v[i] *= scale;
+}
+
+// Four rows of a lane: y = base + v for eight columns from n.
+struct OutRows {
+  const uint16_t *base[4];
+  uint16_t *y[4];
+  bool have[4];
+  bool wide;  // 16-byte accesses are aligned
+  uint32_t N;
+  bool read;
+  __device__ __forceinline__ OutRows(const LoraStack &s, const uint32_t *list, uint32_t i0, uint32_t n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(s.y) | (s.y_stride * 2u) | reinterpret_cast<uintptr_t>(s.base) |
+                         (s.base ? s.base_stride * 2u : 0u);
+    wide = (at & 15u) == 0u;
+    read = s.base != nullptr;
+    N = s.N;
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; ++i) {
+      have[i] = i0 + i < n;
+      const uint64_t row = list[have[i] ? i0 + i : 0u];
+      base[i] = read ? s.base + row * s.base_stride : nullptr;
+      y[i] = s.y + row * s.y_stride;
     }
   }
-  static __device__ __forceinline__ u32x4 get(const uint8_t *lds, uint32_t c, uint32_t step, uint32_t lane) {
-    return *reinterpret_cast<const u32x4 *>(lds + c * kRow + 64u * step + 16u * (lane >> 4));
+  __device__ __forceinline__ void load(u32x4 (&o)[4], uint32_t n) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = u32x4{0u, 0u, 0u, 0u};
+      if (read && wide && have[i] && n + 8u <= N) o[i] = *reinterpret_cast<const u32x4 *>(base[i] + n);
+    }
+  }
+  // v[t][i]: row i, column n + t
+  __device__ __forceinline__ void add(const u32x4 (&o)[4], const f32x4 (&v)[8], uint32_t n) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!have[i]) continue;
+      if (wide && n + 8u <= N) {
+        u32x4 w;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = pack_bf16x2(bf16_lo(o[i][t]) + v[2 * t][i], bf16_hi(o[i][t]) + v[2 * t + 1][i]);
+        *reinterpret_cast<u32x4 *>(y[i] + n) = w;
+      } else {
+#pragma unroll
+        for (uint32_t t = 0; t < 8u; ++t)
+          if (n + t < N) y[i][n + t] = to_bf16_bits((read ? bf16_bits_to_f32(base[i][n + t]) : 0.f) + v[t][i]);
+      }
+    }
   }
 };
 
-// 64 columns from n0 in four tiles: as a row of the product's first operand lane (c, q) loads
-// column n0 + 16 (c / 4) + 4 t + c % 4 of tile t, so that as a result it holds n0 + 16 q + 4 t + i:
-// sixteen neighbouring outputs of its row.
-template <int KS>
-__device__ __forceinline__ void load_b(u32x4 (&b)[4][KS], __amdgpu_buffer_rsrc_t rb, uint32_t R, uint32_t rank, uint32_t n0,
-                                       uint32_t lane) {
-  const uint32_t c = lane & 15u;
+// Rows without an adapter (base itself) or with an id outside the pool (NaN), columns [n0, end).
+__device__ __forceinline__ void pass_rows(const LoraStack &s, const uint32_t *list, uint32_t n, bool nan, uint32_t n0, uint32_t end) {
+  if (!nan && s.base == s.y) return;  // in place
+  for (uint32_t i = 0; i < n; ++i) {
+    const uint64_t row = list[i];
+    for (uint32_t c = n0 + threadIdx.x; c < end; c += 256u)
+      s.y[row * s.y_stride + c] = nan ? 0x7FC0u : s.base ? s.base[row * s.base_stride + c] : 0u;
+  }
+}
+
+template <int P, int NCH>
+__device__ __forceinline__ void multiply_block(f32x4 (&acc)[8], const UOperand<P, NCH> &u, int ch, const uint8_t *b, uint32_t lane) {
+  const uint32_t c = lane & 15u, q = lane >> 4;
 #pragma unroll
-  for (uint32_t t = 0; t < 4u; ++t) {
-    const uint32_t n = n0 + 16u * (c >> 2) + 4u * t + (c & 3u);  // past the last one: zeros by the resource
+  for (int k = 0; k < UOperand<P, NCH>::kSteps; ++k) {
+    const uint8_t *const at = b + 16u * (c * P + b_swizzle<P>(c, P == 2 ? q & 1u : 4u * k + q));
+    const int i = UOperand<P, NCH>::kSteps * ch + k;
 #pragma unroll
-    for (uint32_t k = 0; k < KS; ++k) {
-      const uint32_t r = 32u * k + 8u * (lane >> 4);
-      b[t][k] = buf_load_b128(rb, r < rank ? (n * R + r) * 2u : kOutOfRange);
+    for (int t = 0; t < 8; ++t) {
+      const u32x4 bt = *reinterpret_cast<const u32x4 *>(at + 256u * P * t);
+      acc[t] = mfma16(u.hi[i], bt, acc[t]);
+      if constexpr (P != 2) acc[t] = mfma16(u.lo[i], bt, acc[t]);
     }
   }
 }
 
-// Sixteen neighbouring values of a row: y = base + v, columns from n on.
-struct OutRow {
-  const uint16_t *base;
-  uint16_t *y;
-  uint32_t left;  // columns to the row's end
-  bool wide;      // 16-byte pieces
-  __device__ __forceinline__ OutRow(const LoraStack &s, size_t row, uint32_t n, bool wide_) {
-    left = n < s.N ? s.N - n : 0u;
-    base = s.base ? s.base + row * s.base_stride + n : nullptr;
-    y = s.y + row * s.y_stride + n;
-    wide = wide_ && left >= 16u;
+// The n <= 16 rows in `list`, columns n0 .. n0 + 511: a wave has 128 of them.  u goes through LDS,
+// where all 256 threads have summed its parts.
+template <int P, int NCH>
+struct ExpandFew {
+  typedef UOperand<P, NCH> U;
+  static constexpr uint32_t kBlock = 2048u * P;             // of B, a wave
+  static constexpr uint32_t kRanks = 8u * P * NCH;          // largest rank
+  static constexpr uint32_t kRow = 2u * kRanks + 16u;       // a row of u, padded: banks
+  static constexpr uint32_t kLds = 4u * kBlock + 2u * kFew * kRow;
+  static constexpr uint32_t kColumns = 4u * kBlockN;
+  static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
+                                             uint32_t n0, uint8_t *lds, uint32_t lane, uint32_t wave) {
+    const uint32_t c = lane & 15u, q = lane >> 4, rank = own_rank(s, e), w0 = n0 + kBlockN * wave;
+    uint8_t *const b = lds + kBlock * wave, *const hi = lds + 4u * kBlock, *const lo = hi + kFew * kRow;
+    const auto rb = make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u);
+#pragma unroll
+    for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, rank, w0, 0u, j, b, lane);
+    const OutRows out(s, list, 4u * q, n);
+    u32x4 o[4];
+    out.load(o, w0 + 8u * c);
+    const float scale = s.scales ? s.scales[e] : 1.f;
+    for (uint32_t p = threadIdx.x; p < kFew * kRanks / 8u; p += 256u) {
+      const uint32_t i = p / (kRanks / 8u), r = 8u * (p % (kRanks / 8u));
+      f32x4 v[2] = {};
+      if (i < n && r < s.R) sum_parts(v, g, s, list[i], g.parts, scale, [&](uint32_t j) { return r + 4u * j; });
+      u32x4 h, l;
+      split_bf16(v[0], v[1], h, l);
+      *reinterpret_cast<u32x4 *>(hi + i * kRow + 2u * r) = h;
+      *reinterpret_cast<u32x4 *>(lo + i * kRow + 2u * r) = l;
+    }
+    __syncthreads();
+    U u;
+#pragma unroll
+    for (int k = 0; k < U::kAll; ++k) {
+      if constexpr (P == 2) {
+        u.hi[0] = *reinterpret_cast<const u32x4 *>((q < 2u ? hi : lo) + c * kRow + 16u * (q & 1u));
+      } else {
+        u.hi[k] = *reinterpret_cast<const u32x4 *>(hi + c * kRow + 64u * k + 16u * q);
+        u.lo[k] = *reinterpret_cast<const u32x4 *>(lo + c * kRow + 64u * k + 16u * q);
+      }
+    }
+    f32x4 acc[8] = {};
+#pragma unroll
+    for (int ch = 0; ch < NCH; ++ch) {
+      if (64u * ch >= rank && ch > 0) break;
+      INT8W_VMCNT(0);
+      keep_order();
+      multiply_block<P, NCH>(acc, u, ch, b, lane);
+      if (ch + 1 < NCH) {
+        INT8W_LGKMCNT0();
+        keep_order();
+#pragma unroll
+        for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, rank, w0, 64u * (ch + 1), j, b, lane);
+      }
+    }
+    out.add(o, acc, w0 + 8u * c);
   }
-  __device__ __forceinline__ void add(const f32x4 (&v)[4]) const {
-    if (wide) {
+};
+
+// Up to 64 rows, columns [n0, end): a wave has 16 of the rows, blocks of B are shared, one ahead.
+template <int P, int NCH>
+struct ExpandMany {
+  typedef UOperand<P, NCH> U;
+  static constexpr uint32_t kBlock = 2048u * P;
+  static constexpr uint32_t kLds = 2u * kBlock;
+  static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
+                                             uint32_t parts, uint32_t n0, uint32_t end, uint8_t *lds, uint32_t lane, uint32_t wave) {
+    const uint32_t c = lane & 15u, q = lane >> 4, rank = own_rank(s, e);
+    const auto rb = make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u);
+    const OutRows out(s, list, 16u * wave + 4u * q, n);
+    const float scale = s.scales ? s.scales[e] : 1.f;
+    const uint32_t mine = 16u * wave + c;
+    const uint32_t row = list[mine < n ? mine : 0u];
+    const bool idle = 16u * wave >= n;  // a wave without a row loads its share of B
+    U u;
+    f32x4 v[2 * U::kAll] = {};
+    if (mine < n)
+      sum_parts(v, g, s, row, parts, scale, [&](uint32_t j) { return (P == 2 ? 8u * (q & 1u) : 32u * (j / 2u) + 8u * q) + 4u * (j % 2u); });
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 o = base ? *reinterpret_cast<const u32x4 *>(base + 8 * h) : u32x4{0u, 0u, 0u, 0u};
+    for (int k = 0; k < U::kAll; ++k) {
+      u32x4 h, l;
+      split_bf16(v[2 * k], v[2 * k + 1], h, l);
+      if constexpr (P == 2) {
+        u.hi[0] = q < 2u ? h : l;
+      } else {
+        u.hi[k] = h;
+        u.lo[k] = l;
+      }
+    }
+    const uint32_t blocks = (end - n0 + kBlockN - 1u) / kBlockN;
+    auto load_b = [&](uint32_t block, int ch, uint8_t *to) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 &w = v[2 * h + i / 2];
-          o[i] = pack_bf16x2(bf16_lo(o[i]) + w[2 * (i & 1)], bf16_hi(o[i]) + w[2 * (i & 1) + 1]);
+      for (uint32_t i = 0; i < P / 2u; ++i) dma_b<P>(rb, s.R, rank, n0 + kBlockN * block, 64u * ch, wave * (P / 2u) + i, to, lane);
+    };
+    u32x4 next[4];
+    load_b(0, 0, lds);
+    out.load(next, n0 + 8u * c);
+    uint32_t stage = 0;
+    for (uint32_t i = 0; i < blocks; ++i) {
+      const uint32_t n1 = n0 + kBlockN * i + 8u * c;
+      u32x4 o[4];
+      f32x4 acc[8] = {};
+#pragma unroll
+      for (int ch = 0; ch < NCH; ++ch) {
+        INT8W_VMCNT(0);
+        INT8W_LGKMCNT0();
+        asm volatile("s_barrier" ::: "memory");  // this chunk is there for all waves, the other stage is done with
+        if (ch == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r] = next[r];
         }
-        *reinterpret_cast<u32x4 *>(y + 8 * h) = o;
+        uint8_t *const other = lds + (stage ^ 1u) * kBlock;
+        if (ch + 1 < NCH) {
+          load_b(i, ch + 1, other);
+        } else if (i + 1u < blocks) {
+          load_b(i + 1u, 0, other);
+          out.load(next, n1 + kBlockN);
+        }
+        keep_order();
+        if (!idle) multiply_block<P, NCH>(acc, u, ch, lds + stage * kBlock, lane);
+        stage ^= 1u;
       }
-    } else {
-#pragma unroll
-      for (uint32_t i = 0; i < 16u; ++i)
-        if (i < left) y[i] = to_bf16_bits((base ? bf16_bits_to_f32(base[i]) : 0.f) + v[i / 4][i % 4]);
+      out.add(o, acc, n1);
     }
-  }
-  // no adapter: base itself; an id outside the pool: NaN
-  __device__ __forceinline__ void pass(bool nan) const {
-    if (!nan && base == y) return;
-#pragma unroll
-    for (uint32_t i = 0; i < 16u; ++i)
-      if (i < left) y[i] = nan ? 0x7FC0u : base ? base[i] : 0u;
+    __syncthreads();
   }
 };
-
-__device__ __forceinline__ bool wide_rows(const LoraStack &s) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(s.y) | (s.y_stride * 2u) | reinterpret_cast<uintptr_t>(s.base) |
-                       (s.base ? s.base_stride * 2u : 0u);
-  return (at & 15u) == 0u;
-}
 
 // The stack and column tile of a block: the stacks' tiles one after the other.
 __device__ __forceinline__ const LoraStack &stack_of(const LoraArgs &g, uint32_t &tile, uint32_t tile_n) {
@@ -267,143 +671,113 @@ __device__ __forceinline__ const LoraStack &stack_of(const LoraArgs &g, uint32_t
   return g.s[i];
 }
 
-// grid (column tiles of all stacks, rows).  A wave has 64 columns.
-template <int KS>
+// grid (column tiles of all stacks, rows).
+template <int P, int NCH>
 __global__ __launch_bounds__(256) void k_expand_rows(const LoraArgs g) {
-  typedef ExpandU<KS> U;
-  __shared__ uint32_t list[kRowsGroup];
-  __shared__ __attribute__((aligned(16))) uint8_t hi[kRowsGroup * U::kRow], lo[kRowsGroup * U::kRow];
+  typedef ExpandFew<P, NCH> Few;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ uint32_t list[kFew];
   uint32_t tile = blockIdx.x;
-  const LoraStack &s = stack_of(g, tile, kTileN);
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6), i = blockIdx.y, c = lane & 15u;
-  const uint32_t n0 = tile * kTileN + 64u * wave, id = uniform(g.ids[i]);
+  const LoraStack &s = stack_of(g, tile, Few::kColumns);
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), i = blockIdx.y, n0 = tile * Few::kColumns;
+  const uint32_t own = lane < g.m ? g.ids[lane] : INT8W_NO_ADAPTER, id = (uint32_t)__builtin_amdgcn_readlane((int)own, (int)i);
   if (id >= g.num) {
-    if (threadIdx.x < kTileN / 16u)
-      OutRow(s, i, tile * kTileN + 16u * threadIdx.x, false).pass(id != INT8W_NO_ADAPTER);
+    pass_rows(s, &i, 1u, id != INT8W_NO_ADAPTER, n0, n0 + Few::kColumns < s.N ? n0 + Few::kColumns : s.N);
     return;
   }
   uint32_t n;
-  if (!gather_rows(g.ids, g.m, i, id, lane, list, n)) return;
-  const uint32_t rank = own_rank(s, id);
-  const auto rb = make_rsrc(s.b + (size_t)id * s.N * s.R, s.N * s.R * 2u);
-  u32x4 b[4][KS];
-  load_b<KS>(b, rb, s.R, rank, n0, lane);
-  const float scale = s.scales ? s.scales[id] : 1.f;
+  if (!gather_rows(own, i, id, lane, list, n)) return;
   __syncthreads();
-  U::stage(hi, lo, g, s, kRowsGroup, [&](uint32_t r) { return r < n ? list[r] : g.m; }, [&](uint32_t) { return scale; });
-  __syncthreads();
-  f32x4 acc[4] = {};
-#pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    const u32x4 uh = U::get(hi, c, k, lane), ul = U::get(lo, c, k, lane);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[t] = mfma(b[t][k], ul, mfma(b[t][k], uh, acc[t]));
-  }
-  if (c < n) OutRow(s, list[c], n0 + 16u * (lane >> 4), wide_rows(s)).add(acc);
+  Few::run(g, s, id, list, n, n0, lds, lane, wave);
 }
 
-// grid (chunks of chunk_n columns of all stacks, windows).  The waves take blocks of 64 columns in turn.
-template <int KS>
-__global__ __launch_bounds__(256) void k_expand_tile(const LoraArgs g, uint32_t chunk_n) {
-  typedef ExpandU<KS> U;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  uint8_t *const hi = lds, *const lo = lds + kTileRows * U::kRow;
+// grid (chunks of chunk_n columns of all stacks, slots, plans).
+template <int P, int NCH>
+__global__ __launch_bounds__(256, NCH == 1 ? 3 : 2) void k_expand_items(const LoraArgs g, uint32_t chunk_n) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[ExpandMany<P, NCH>::kLds];
+  __shared__ uint32_t list[kMany];
   uint32_t tile = blockIdx.x;
   const LoraStack &s = stack_of(g, tile, chunk_n);
-  const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6), c = lane & 15u;
-  const uint32_t row0 = blockIdx.y * kTileRows;
-  const uint32_t own = row0 + lane < g.m ? g.ids[row0 + lane] : INT8W_NO_ADAPTER;
-  const bool here = row0 + lane < g.m;
-  U::stage(hi, lo, g, s, kTileRows,
-           [&](uint32_t r) {
-             const uint32_t t = row0 + r;
-             return t < g.m && g.ids[t] < g.num ? t : g.m;
-           },
-           [&](uint32_t r) { return s.scales ? s.scales[g.ids[row0 + r]] : 1.f; });
-  __syncthreads();
-  const bool wide = wide_rows(s);
-  const unsigned long long some = __ballot(here && own < g.num), bad = __ballot(here && own >= g.num && own != INT8W_NO_ADAPTER);
-  const unsigned long long none = __ballot(here && own == INT8W_NO_ADAPTER);
-  const uint32_t end = (tile + 1u) * chunk_n < s.N ? (tile + 1u) * chunk_n : s.N;
-  for (uint32_t n0 = tile * chunk_n + 64u * wave; n0 < end; n0 += 256u) {
-    for (unsigned long long left = some; left;) {
-      const uint32_t e = (uint32_t)__builtin_amdgcn_readlane((int)own, __builtin_ctzll(left));
-      const unsigned long long rows = __ballot(own == e) & some;
-      left &= ~rows;
-      const uint32_t rank = own_rank(s, e);
-      u32x4 b[4][KS];
-      load_b<KS>(b, make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u), s.R, rank, n0, lane);
-#pragma unroll
-      for (uint32_t tt = 0; tt < kTileRows / 16u; ++tt) {
-        if ((rows >> (16u * tt) & 0xFFFFull) == 0ull) continue;
-        f32x4 acc[4] = {};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const u32x4 uh = U::get(hi, 16u * tt + c, k, lane), ul = U::get(lo, 16u * tt + c, k, lane);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[t] = mfma(b[t][k], ul, mfma(b[t][k], uh, acc[t]));
-        }
-        if (rows >> (16u * tt + c) & 1ull) OutRow(s, row0 + 16u * tt + c, n0 + 16u * (lane >> 4), wide).add(acc);
-      }
-    }
-    if ((none | bad) != 0ull)
-      for (uint32_t tt = 0; tt < kTileRows / 16u; ++tt) {
-        const uint32_t r = 16u * tt + c;
-        if ((none | bad) >> r & 1ull) OutRow(s, row0 + r, n0 + 16u * (lane >> 4), wide).pass(bad >> r & 1ull);
-      }
+  const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6);
+  const uint32_t n0 = tile * chunk_n, end = n0 + chunk_n < s.N ? n0 + chunk_n : s.N;
+  const LoraPlan &plan = reinterpret_cast<const LoraPlan *>(g.plans)[blockIdx.z];
+  const uint32_t items = uniform32(plan.items), parts = uniform32(plan.parts);
+  for (uint32_t i = blockIdx.y; i < items; i += gridDim.y)
+    with_item(plan, i, list, [&](uint32_t e, uint32_t n) {
+      if (e >= g.num)
+        pass_rows(s, list, n, e != g.num, n0, end);
+      else
+        ExpandMany<P, NCH>::run(g, s, e, list, n, parts, n0, end, lds, lane, wave);
+    });
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+bool planned(const LoraArgs &a) { return a.m > kBallotRows; }
+uint32_t plans(const LoraArgs &a) { return (a.m + kLoraPlanRows - 1u) / kLoraPlanRows; }
+
+// Workgroups that share a plan's groups: a prompt's rows make 16.
+uint32_t slots(const LoraArgs &a, uint32_t others) {
+  const uint32_t most = a.m < 64u ? a.m : 64u, want = 2048u / (plans(a) * others);
+  return want < 16u ? 16u : want < most ? want : most;
+}
+
+uint32_t k_steps(const LoraArgs &a) { return (a.K + kStepK - 1u) / kStepK; }
+
+// Workgroups of shrink that share a plan's groups and parts.
+uint32_t shrink_blocks(const LoraArgs &a) {
+  const uint32_t n = kShrinkBlocks / (plans(a) * a.count);
+  return n < 16u ? 16u : n;
+}
+
+// How K is cut: two steps a wave.  With a plan that is the most; the plan may take fewer parts.
+void cut_k(LoraArgs &a) {
+  a.part_steps = 8u;
+  a.parts = (k_steps(a) + 7u) / 8u;
+  if (planned(a)) {
+    const uint32_t most = shrink_blocks(a) / ((a.m + plans(a) * kMany - 1u) / (plans(a) * kMany));  // groups of a plan at least
+    a.parts = a.parts < most ? a.parts : most < 1u ? 1u : most;
   }
 }
 
-bool rows_form(uint32_t m) { return m <= kRowsMax; }
-
-uint32_t max_rank(const LoraArgs &a) {
-  uint32_t r = 0;
-  for (uint32_t i = 0; i < a.count; ++i) r = a.s[i].R > r ? a.s[i].R : r;
-  return r;
-}
-
-// How K is cut: enough workgroups to load from every CU, each with a step for every wave.
-void cut_k(LoraArgs &a) {
-  const uint32_t steps = (a.K + kStepK - 1u) / kStepK;
-  const uint32_t blocks = a.count * (rows_form(a.m) ? a.m : (a.m + kTileRows - 1u) / kTileRows);
-  uint32_t parts = 1024u / blocks, most = rows_form(a.m) ? 32u : 8u;
-  if (rows_form(a.m) && parts < 8u) parts = 8u;
-  if (parts > most) parts = most;
-  if (parts > (steps + 3u) / 4u) parts = (steps + 3u) / 4u;
-  if (parts < 1u) parts = 1u;
-  const uint32_t each = (steps + parts - 1u) / parts;
-  a.part_k = each * kStepK;
-  a.parts = (steps + each - 1u) / each;
+template <class Kern>
+hipError_t allow(LdsAllowance &allowance, Kern kern, uint32_t dynamic_bytes, uint32_t static_bytes) {
+  return needs_lds_allowance(dynamic_bytes, static_bytes) ? allow_lds(allowance, kern, (int)dynamic_bytes) : hipSuccess;
 }
 
 template <int RT>
-void launch_shrink(const LoraArgs &a, hipStream_t stream) {
-  if (rows_form(a.m))
-    k_shrink_rows<RT><<<dim3(a.parts, a.m, a.count), 256, 0, stream>>>(a);
-  else
-    k_shrink_tile<RT><<<dim3(a.parts, (a.m + kTileRows - 1u) / kTileRows, a.count), 256, 0, stream>>>(a);
+hipError_t launch_shrink(const LoraArgs &a, hipStream_t stream) {
+  if (!planned(a)) {
+    constexpr uint32_t lds = ShrinkFew<RT>::kLds;
+    static LdsAllowance allowance;
+    const hipError_t e = allow(allowance, k_shrink_rows<RT>, lds, 0);
+    if (e != hipSuccess) return e;
+    k_shrink_rows<RT><<<dim3(a.parts, a.m, a.count), 256, lds, stream>>>(a);
+  } else {
+    constexpr uint32_t lds = ShrinkFew<RT>::kLds > ShrinkMany<RT>::kLds ? ShrinkFew<RT>::kLds : ShrinkMany<RT>::kLds;
+    static LdsAllowance allowance;
+    const hipError_t e = allow(allowance, k_shrink_items<RT>, lds, 0);
+    if (e != hipSuccess) return e;
+    k_shrink_items<RT><<<dim3(shrink_blocks(a), plans(a), a.count), 256, lds, stream>>>(a);
+  }
+  return hipGetLastError();
 }
 
-template <int KS>
+template <int P, int NCH>
 hipError_t launch_expand(const LoraArgs &a, hipStream_t stream) {
+  typedef ExpandFew<P, NCH> Few;
   uint32_t tiles = 0;
-  if (rows_form(a.m)) {
-    for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + kTileN - 1u) / kTileN;
-    k_expand_rows<KS><<<dim3(tiles, a.m), 256, 0, stream>>>(a);
+  if (!planned(a)) {
+    static LdsAllowance allowance;
+    const hipError_t e = allow(allowance, k_expand_rows<P, NCH>, Few::kLds, sizeof(uint32_t[kFew]));
+    if (e != hipSuccess) return e;
+    for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + Few::kColumns - 1u) / Few::kColumns;
+    k_expand_rows<P, NCH><<<dim3(tiles, a.m), 256, Few::kLds, stream>>>(a);
     return hipGetLastError();
   }
-  const uint32_t lds = 2u * kTileRows * ExpandU<KS>::kRow, windows = (a.m + kTileRows - 1u) / kTileRows;
-  static LdsAllowance allowance;
-  if (needs_lds_allowance(lds, 0)) {
-    const hipError_t e = allow_lds(allowance, k_expand_tile<KS>, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  uint32_t all = 0;
-  for (uint32_t i = 0; i < a.count; ++i) all += (a.s[i].N + kTileN - 1u) / kTileN;
-  const uint32_t chunks = 2048u / windows < 1u ? 1u : 2048u / windows;  // per window
-  const uint32_t chunk_n = (all + chunks - 1u) / chunks * kTileN;
+  const uint32_t chunk_n = a.m > 256u ? 2u * Few::kColumns : Few::kColumns;
   for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + chunk_n - 1u) / chunk_n;
-  k_expand_tile<KS><<<dim3(tiles, windows), 256, lds, stream>>>(a, chunk_n);
+  k_expand_items<P, NCH><<<dim3(tiles, slots(a, tiles), plans(a)), 256, 0, stream>>>(a, chunk_n);
   return hipGetLastError();
 }
 
@@ -412,7 +786,7 @@ hipError_t launch_expand(const LoraArgs &a, hipStream_t stream) {
 uint64_t lora_workspace(const LoraArgs &given, uint64_t *offsets) {
   LoraArgs a = given;
   cut_k(a);
-  uint64_t bytes = 0;
+  uint64_t bytes = planned(a) ? plans(a) * kLoraPlanBytes : 0u;
   for (uint32_t i = 0; i < a.count; ++i) {
     offsets[i] = bytes;
     bytes += ((uint64_t)a.parts * a.m * a.s[i].R * 4u + 255u) & ~255ull;
@@ -424,24 +798,27 @@ hipError_t launch_lora(LoraArgs a, void *ws, hipStream_t stream) {
   cut_k(a);
   uint64_t offsets[INT8W_MAX_MULTI];
   lora_workspace(a, offsets);
-  for (uint32_t i = 0; i < a.count; ++i) a.s[i].u = reinterpret_cast<float *>((uint8_t *)ws + offsets[i]);
-  const uint32_t R = max_rank(a);
-  if (R <= 16u)
-    launch_shrink<1>(a, stream);
-  else if (R <= 32u)
-    launch_shrink<2>(a, stream);
-  else if (R <= 64u)
-    launch_shrink<4>(a, stream);
-  else if (R <= 128u)
-    launch_shrink<8>(a, stream);
-  else
-    launch_shrink<16>(a, stream);
-  const hipError_t e = hipGetLastError();
+  uint32_t R = 0;
+  for (uint32_t i = 0; i < a.count; ++i) {
+    a.s[i].u = reinterpret_cast<float *>((uint8_t *)ws + offsets[i]);
+    R = a.s[i].R > R ? a.s[i].R : R;
+  }
+  a.plans = ws;
+  if (planned(a)) {
+    uint32_t bits = 1;
+    while (a.num + 1u >> bits) ++bits;  // ids up to num + 1
+    k_plan<<<plans(a), kLoraPlanRows, 0, stream>>>(a.ids, a.m, a.num, bits, k_steps(a), a.parts, shrink_blocks(a),
+                                                          reinterpret_cast<LoraPlan *>(ws));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const hipError_t e = R <= 16u ? launch_shrink<1>(a, stream) : R <= 32u ? launch_shrink<2>(a, stream) : launch_shrink<4>(a, stream);
   if (e != hipSuccess) return e;
-  if (R <= 32u) return launch_expand<1>(a, stream);
-  if (R <= 64u) return launch_expand<2>(a, stream);
-  if (R <= 128u) return launch_expand<4>(a, stream);
-  return launch_expand<8>(a, stream);
+  if (R <= 16u) return launch_expand<2, 1>(a, stream);
+  if (R <= 32u) return launch_expand<4, 1>(a, stream);
+  if (R <= 64u) return launch_expand<8, 1>(a, stream);
+  if (R <= 128u) return launch_expand<8, 2>(a, stream);
+  return launch_expand<8, 4>(a, stream);
 }
 
 }  // namespace int8w
