@@ -31,16 +31,25 @@ constexpr uint32_t kMany = 64;        // ... with the rows shared out
 constexpr uint32_t kBallotRows = 64;  // largest batch without a plan
 constexpr uint32_t kStepK = 64;       // K of a step: a cache line of a row
 constexpr uint32_t kBlockN = 128;     // output columns of a step
-constexpr uint32_t kShrinkBlocks = 512;
+constexpr uint32_t kShrinkBlocks = 512;  // workgroups over a plan's groups: what fits the CUs
+constexpr uint32_t kExpandBlocks = 1024;
 
 #define INT8W_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) >> 4) << 14) | 0x0F70 | ((n) & 15))
 #define INT8W_LGKMCNT0() __builtin_amdgcn_s_waitcnt(0xC07F)
 
+// Pointers out of the stacks' table, whose memory the compiler does not know: with plain ones it
+// emits flat accesses, which wait for LDS and its DMA as well.
+typedef __attribute__((address_space(1))) uint16_t g_u16;
+typedef __attribute__((address_space(1))) float g_f32;
+typedef __attribute__((address_space(1))) u32x4 g_u32x4;
+typedef __attribute__((address_space(1))) f32x4 g_f32x4;
+
 // ---- DMA of 16 bytes a lane into LDS: lane l of the wave writes `to` + 16 l
 __device__ __align__(16) uint32_t g_zeros[4];  // what lanes beyond the end of K load
 
+template <int AUX = 0>
 __device__ __forceinline__ void dma(const uint16_t *from, uint8_t *to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (__attribute__((address_space(3))) void *)to, 16, 0, AUX);
 }
 __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t from, uint32_t off, uint8_t *to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)off, 0, 0, 0);
@@ -74,9 +83,7 @@ struct PlanItem {
 };
 struct LoraPlan {  // of kLoraPlanRows rows
   uint32_t items;
-  uint32_t steps;  // of K a part
-  uint32_t parts;
-  uint32_t pad[13];
+  uint32_t pad[15];
   PlanItem item[kLoraPlanRows];
 };
 static_assert(sizeof(LoraPlan) <= kLoraPlanBytes && kLoraPlanBytes % 256u == 0, "workspace");
@@ -87,7 +94,6 @@ static_assert(sizeof(LoraPlan) <= kLoraPlanBytes && kLoraPlanBytes % 256u == 0, 
 // their order in the batch, and so does the cut into groups; only where a group lies in the
 // plan depends on the atomics' order, and no result does.
 __global__ __launch_bounds__(kLoraPlanRows) void k_plan(const uint32_t *__restrict__ ids, uint32_t m, uint32_t num, uint32_t bits,
-                                                        uint32_t steps, uint32_t most_parts, uint32_t shrink_blocks,
                                                         LoraPlan *__restrict__ plans) {
   constexpr uint32_t kSlots = 2u * kLoraPlanRows, kWaves = kLoraPlanRows / 64u, kEmpty = 0xFFFFFFFFu;
   static_assert(kWaves == 16u, "a slot's counts are 16 bytes");
@@ -141,14 +147,55 @@ __global__ __launch_bounds__(kLoraPlanRows) void k_plan(const uint32_t *__restri
       it.n = total - rank < kMany ? total - rank : kMany;
     }
   }
-  if (tid == 0u) {  // K in as many parts as give each workgroup of shrink one
-    uint32_t parts = shrink_blocks / items;
-    parts = parts < 1u ? 1u : parts > most_parts ? most_parts : parts;
-    const uint32_t each = (steps + parts - 1u) / parts;
-    plan.items = items;
-    plan.steps = each;
-    plan.parts = (steps + each - 1u) / each;
+  if (tid == 0u) plan.items = items;
+}
+
+// The groups of up to 64 plans, one after the other, as every workgroup that works on them sees them.
+struct Groups {
+  const LoraPlan *plans;
+  uint32_t until;  // lane p: groups of plans 0 .. p
+  uint32_t total;
+  __device__ __forceinline__ Groups(const LoraArgs &g, uint32_t plan0, uint32_t lane) {
+    plans = reinterpret_cast<const LoraPlan *>(g.plans) + plan0;
+    const uint32_t have = (g.m + kLoraPlanRows - 1u) / kLoraPlanRows - plan0;
+    until = lane < have ? plans[lane].items : 0u;
+#pragma unroll
+    for (uint32_t off = 1; off < 64u; off <<= 1) {
+      const uint32_t up = (uint32_t)__shfl_up((int)until, off, 64);
+      if (lane >= off) until += up;
+    }
+    total = (uint32_t)__builtin_amdgcn_readlane((int)until, 63);
   }
+  // Parts of K, one workgroup of shrink to each where there are that many: shrink and expand find the same.
+  __device__ __forceinline__ uint32_t parts(const LoraArgs &g, uint32_t &steps) const {
+    uint32_t n = kShrinkBlocks / total;
+    n = n < 1u ? 1u : n > g.parts ? g.parts : n;
+    const uint32_t all = (g.K + kStepK - 1u) / kStepK;
+    steps = (all + n - 1u) / n;
+    return (all + steps - 1u) / steps;
+  }
+  // Group i: f(adapter, n) with its rows in `list`.
+  template <class F>
+  __device__ __forceinline__ void with(uint32_t i, uint32_t *list, F f) const {
+    const uint32_t p = (uint32_t)__popcll(__ballot(until <= i));
+    const uint32_t before = p ? (uint32_t)__builtin_amdgcn_readlane((int)until, (int)(p - 1u)) : 0u;
+    const PlanItem &it = plans[p].item[i - before];
+    const uint32_t row = threadIdx.x < kMany ? it.rows[threadIdx.x] : 0u;  // beyond n: no row, unused
+    const uint32_t e = uniform32(it.e), n = uniform32(it.n);
+    __syncthreads();  // the last group is done with
+    if (threadIdx.x < kMany) list[threadIdx.x] = row;
+    __syncthreads();
+    f(e, n);
+  }
+};
+
+// f(i) for this workgroup's share of 0 .. end - 1: an eighth in a row to the workgroups of each XCD (the grid
+// is a multiple of 8).  With a part of K or a run of columns of all groups after the other, an XCD's L2 sees an eighth
+// of the adapters' matrices, and groups of many rows and of few are spread evenly.
+template <class F>
+__device__ __forceinline__ void each_share(uint32_t end, F f) {
+  const uint32_t per = (end + 7u) / 8u, from = blockIdx.x % 8u * per, until = from + per < end ? from + per : end;
+  for (uint32_t i = from + blockIdx.x / 8u; i < until; i += gridDim.x / 8u) f(i);
 }
 
 // ---- shrink --------------------------------------------------------------------------------
@@ -168,23 +215,16 @@ __device__ __forceinline__ uint32_t a_offset(uint32_t r, uint32_t rank, uint32_t
   return r < rank ? at : kOutOfRange;
 }
 
-// A part of K, from a step that differs from group to group: the same step of all rows of all
-// adapters tends to lie in the same memory channel.  `start` goes by the adapter or the rows, never
-// by a group's place in the plan, since the sum's order depends on it.
+// A part of K.
 struct PartK {
-  uint32_t first, end, steps, turn;
-  uint32_t part;
-  __device__ __forceinline__ PartK(const LoraArgs &g, uint32_t part_, uint32_t part_steps, uint32_t start) {
+  uint32_t part, first, end, steps;
+  __device__ __forceinline__ PartK(const LoraArgs &g, uint32_t part_, uint32_t part_steps) {
     part = part_;
     first = part * part_steps * kStepK;
     end = first + part_steps * kStepK < g.K ? first + part_steps * kStepK : g.K;
     steps = (end - first + kStepK - 1u) / kStepK;
-    turn = start % steps;
   }
-  __device__ __forceinline__ uint32_t at(uint32_t step) const {  // `end` beyond the last step
-    const uint32_t turned = step + turn < steps ? step + turn : step + turn - steps;
-    return step < steps ? first + turned * kStepK : end;
-  }
+  __device__ __forceinline__ uint32_t at(uint32_t step) const { return step < steps ? first + step * kStepK : end; }
 };
 
 // u of the n <= 16 rows in `list` (LDS, may lie where lds does), this part of K.  The four waves
@@ -263,7 +303,7 @@ struct ShrinkFew {
         f32x4 v = sums[p];
 #pragma unroll
         for (uint32_t w = 1; w < 4u; ++w) v += sums[w * RT * 64u + p];
-        *reinterpret_cast<f32x4 *>(s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = v;
+        *(g_f32x4 *)((g_f32 *)s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = v;
       }
       __syncthreads();
     }
@@ -302,8 +342,8 @@ struct ShrinkMany {
 #pragma unroll
           for (uint32_t i = 0; i < kA; ++i)
             dma(ra, at + pa[i] < part_k.end ? oa[i] + 2u * at : kOutOfRange, to + (wave * kA + i) % (2u * RT) * 1024u);
-          dma(at + p0 < part_k.end ? x0 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 2048u * wave);
-          dma(at + p1 < part_k.end ? x1 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 2048u * wave + 1024u);
+          dma<kAuxNontemporal>(at + p0 < part_k.end ? x0 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 2048u * wave);
+          dma<kAuxNontemporal>(at + p1 < part_k.end ? x1 + at : (const uint16_t *)g_zeros, to + 2048u * RT + 2048u * wave + 1024u);
           keep_order();
         };
 #pragma unroll
@@ -332,7 +372,7 @@ struct ShrinkMany {
 #pragma unroll
       for (uint32_t t = 0; t < RT; ++t) {
         const uint32_t row = r0 + 16u * t + 4u * (lane >> 4);
-        if (io < n && row < s.R) *reinterpret_cast<f32x4 *>(s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = acc[t];
+        if (io < n && row < s.R) *(g_f32x4 *)((g_f32 *)s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = acc[t];
       }
     }
   }
@@ -348,40 +388,29 @@ __global__ __launch_bounds__(256) void k_shrink_rows(const LoraArgs g) {
   uint32_t n;
   if (id >= g.num || !gather_rows(own, i, id, lane, list, n)) return;
   __syncthreads();
-  ShrinkFew<RT>::run(g, g.s[blockIdx.z], id, list, n, PartK(g, blockIdx.x, g.part_steps, id), lds, lane, wave);
+  ShrinkFew<RT>::run(g, g.s[blockIdx.z], id, list, n, PartK(g, blockIdx.x, g.part_steps), lds, lane, wave);
 }
 
-// Group i of a plan: f(adapter, n) with its rows in `list`.
-template <class F>
-__device__ __forceinline__ void with_item(const LoraPlan &plan, uint32_t i, uint32_t *list, F f) {
-  const PlanItem &it = plan.item[i];
-  const uint32_t row = threadIdx.x < kMany ? it.rows[threadIdx.x] : 0u;  // beyond n: no row, unused
-  const uint32_t e = uniform32(it.e), n = uniform32(it.n);
-  __syncthreads();  // the last group is done with
-  if (threadIdx.x < kMany) list[threadIdx.x] = row;
-  __syncthreads();
-  f(e, n);
-}
-
-// grid (blocks, plans, stacks): the blocks take the groups' parts in turn.
+// grid (blocks, 64 plans, stacks): the blocks take the groups' parts in turn.
 template <int RT>
 __global__ __launch_bounds__(256) void k_shrink_items(const LoraArgs g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   uint32_t *const list = reinterpret_cast<uint32_t *>(lds);
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6);
-  const LoraStack &s = g.s[blockIdx.z];
-  const LoraPlan &plan = reinterpret_cast<const LoraPlan *>(g.plans)[blockIdx.y];
-  const uint32_t parts = uniform32(plan.parts), steps = uniform32(plan.steps), end = uniform32(plan.items) * parts;
-  for (uint32_t i = blockIdx.x; i < end; i += gridDim.x) {
-    with_item(plan, i / parts, list, [&](uint32_t e, uint32_t n) {
+  const LoraStack s = g.s[blockIdx.z];
+  const Groups groups(g, 64u * blockIdx.y, lane);
+  uint32_t steps;
+  const uint32_t parts = groups.parts(g, steps), end = groups.total * parts;
+  each_share(end, [&](uint32_t i) {
+    groups.with(i % groups.total, list, [&](uint32_t e, uint32_t n) {
       if (e >= g.num) return;
-      const PartK part_k(g, i % parts, steps, n <= kFew ? e : list[0] / kMany);
+      const PartK part_k(g, i / groups.total, steps);
       if (n <= kFew)
         ShrinkFew<RT>::run(g, s, e, list, n, part_k, lds, lane, wave);
       else
         ShrinkMany<RT>::run(g, s, e, list, n, part_k, lds, lane, wave);
     });
-  }
+  });
 }
 
 // ---- expand --------------------------------------------------------------------------------
@@ -415,12 +444,11 @@ struct UOperand {
   u32x4 hi[kAll], lo[P == 2 ? 1 : kAll];
 };
 
-// Two BF16 values that add up to each of eight.  A value beyond BF16's range has an infinity for
+// Two BF16 values that add up to each of four.  A value beyond BF16's range has an infinity for
 // its upper part, and no lower one.
-__device__ __forceinline__ void split_bf16(const f32x4 &a, const f32x4 &b, u32x4 &hi, u32x4 &lo) {
-  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+__device__ __forceinline__ void split_bf16(const f32x4 &v, u32x2 &hi, u32x2 &lo) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     float d0 = v[2 * i] - bf16_lo(hi[i]), d1 = v[2 * i + 1] - bf16_hi(hi[i]);
     d0 = fabsf(d0) < __builtin_inff() ? d0 : 0.f;
@@ -429,16 +457,21 @@ __device__ __forceinline__ void split_bf16(const f32x4 &a, const f32x4 &b, u32x4
   }
 }
 
-// u of one row: COUNT pieces of four values, piece i from offset at(i) of the row, the parts added in their
-// order and scaled.  All pieces of several parts are in flight at a time.
-template <int COUNT, class At>
-__device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, const LoraStack &s, uint32_t row, uint32_t parts,
-                                          float scale, At at) {
-  constexpr uint32_t kAhead = COUNT >= 16 ? 1 : 16 / COUNT;
-  const float *from = s.u + (size_t)row * s.R;
+// COUNT pieces of four values of u, piece i of row(i) from offset at(i) of it: the parts added in their order,
+// scaled.  All pieces of several parts are in flight at a time.
+template <int COUNT, class Row, class At>
+__device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, const LoraStack &s, uint32_t parts, float scale, Row row,
+                                          At at) {
+  constexpr uint32_t kAhead = 8 / COUNT;
   const size_t next = (size_t)g.m * s.R;
+  const g_f32 *from[COUNT];
+  bool have[COUNT];
 #pragma unroll
-  for (int i = 0; i < COUNT; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < COUNT; ++i) {
+    v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    have[i] = row(i) < g.m && at(i) < s.R;
+    from[i] = (const g_f32 *)s.u + (have[i] ? (size_t)row(i) * s.R + at(i) : 0u);
+  }
   for (uint32_t p = 0; p < parts; p += kAhead) {
     f32x4 w[kAhead][COUNT];
 #pragma unroll
@@ -446,7 +479,7 @@ __device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, 
 #pragma unroll
       for (int i = 0; i < COUNT; ++i) {
         w[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (p + j < parts && at(i) < s.R) w[j][i] = *reinterpret_cast<const f32x4 *>(from + (p + j) * next + at(i));
+        if (p + j < parts && have[i]) w[j][i] = *(const g_f32x4 *)(from[i] + (p + j) * next);
       }
     keep_order();
 #pragma unroll
@@ -458,34 +491,41 @@ __device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, 
   for (int i = 0; i < COUNT; ++i) v[i] *= scale;
 }
 
+// Whether eight columns of a row from a multiple of 8 are a 16-byte access.
+__device__ __forceinline__ bool wide_rows(const LoraStack &s) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(s.y) | (s.y_stride * 2u) | reinterpret_cast<uintptr_t>(s.base) |
+                       (s.base ? s.base_stride * 2u : 0u);
+  return (at & 15u) == 0u;
+}
+
 // Four rows of a lane: y = base + v for eight columns from n.
 struct OutRows {
-  const uint16_t *base[4];
-  uint16_t *y[4];
+  const g_u16 *base[4];
+  g_u16 *y[4];
   bool have[4];
   bool wide;  // 16-byte accesses are aligned
   uint32_t N;
   bool read;
   __device__ __forceinline__ OutRows(const LoraStack &s, const uint32_t *list, uint32_t i0, uint32_t n) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(s.y) | (s.y_stride * 2u) | reinterpret_cast<uintptr_t>(s.base) |
-                         (s.base ? s.base_stride * 2u : 0u);
-    wide = (at & 15u) == 0u;
+    wide = wide_rows(s);
     read = s.base != nullptr;
     N = s.N;
 #pragma unroll
     for (uint32_t i = 0; i < 4u; ++i) {
       have[i] = i0 + i < n;
       const uint64_t row = list[have[i] ? i0 + i : 0u];
-      base[i] = read ? s.base + row * s.base_stride : nullptr;
-      y[i] = s.y + row * s.y_stride;
+      base[i] = read ? (const g_u16 *)s.base + row * s.base_stride : (const g_u16 *)(const void *)g_zeros;
+      y[i] = (g_u16 *)s.y + row * s.y_stride;
     }
   }
+  // Without a branch, and from somewhere in any case: otherwise the compiler waits for all that is in
+  // flight, stores too, before it sets the registers of a load that may not happen.
   __device__ __forceinline__ void load(u32x4 (&o)[4], uint32_t n) const {
+    if (!wide) return;
+    const uint32_t at = read && n + 8u <= N ? n : 0u;
+    const bool some = !read || N >= 8u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = u32x4{0u, 0u, 0u, 0u};
-      if (read && wide && have[i] && n + 8u <= N) o[i] = *reinterpret_cast<const u32x4 *>(base[i] + n);
-    }
+    for (int i = 0; i < 4; ++i) o[i] = *(const g_u32x4 *)(some ? base[i] + at : (const g_u16 *)(const void *)g_zeros);
   }
   // v[t][i]: row i, column n + t
   __device__ __forceinline__ void add(const u32x4 (&o)[4], const f32x4 (&v)[8], uint32_t n) const {
@@ -496,7 +536,7 @@ struct OutRows {
         u32x4 w;
 #pragma unroll
         for (int t = 0; t < 4; ++t) w[t] = pack_bf16x2(bf16_lo(o[i][t]) + v[2 * t][i], bf16_hi(o[i][t]) + v[2 * t + 1][i]);
-        *reinterpret_cast<u32x4 *>(y[i] + n) = w;
+        *(g_u32x4 *)(y[i] + n) = w;
       } else {
 #pragma unroll
         for (uint32_t t = 0; t < 8u; ++t)
@@ -506,13 +546,44 @@ struct OutRows {
   }
 };
 
-// Rows without an adapter (base itself) or with an id outside the pool (NaN), columns [n0, end).
+// Rows without an adapter (base itself) or with an id outside the pool (NaN), columns [n0, end): pieces
+// of eight columns, four a thread in flight.
 __device__ __forceinline__ void pass_rows(const LoraStack &s, const uint32_t *list, uint32_t n, bool nan, uint32_t n0, uint32_t end) {
   if (!nan && s.base == s.y) return;  // in place
-  for (uint32_t i = 0; i < n; ++i) {
-    const uint64_t row = list[i];
-    for (uint32_t c = n0 + threadIdx.x; c < end; c += 256u)
-      s.y[row * s.y_stride + c] = nan ? 0x7FC0u : s.base ? s.base[row * s.base_stride + c] : 0u;
+  const bool read = !nan && s.base != nullptr, wide = wide_rows(s);
+  const uint32_t across = (end - n0 + 7u) / 8u, all = n * across;
+  for (uint32_t p0 = threadIdx.x; p0 < all; p0 += 4u * 256u) {
+    u32x4 v[4];
+    uint64_t row[4];
+    uint32_t c[4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4u; ++j) {
+      const uint32_t p = p0 + 256u * j < all ? p0 + 256u * j : p0;
+      row[j] = list[p / across];
+      c[j] = n0 + 8u * (p % across);
+      v[j] = nan ? u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u} : u32x4{0u, 0u, 0u, 0u};
+      if (!read) continue;
+      const g_u16 *const from = (const g_u16 *)s.base + row[j] * s.base_stride + c[j];
+      if (wide && c[j] + 8u <= end) {
+        v[j] = *(const g_u32x4 *)from;
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 8u; ++i)
+          if (c[j] + i < end) v[j][i / 2u] |= (uint32_t)from[i] << 16u * (i % 2u);
+      }
+    }
+    keep_order();
+#pragma unroll
+    for (uint32_t j = 0; j < 4u; ++j) {  // a piece past the last one: the first again
+      g_u16 *const to = (g_u16 *)s.y + row[j] * s.y_stride + c[j];
+      if (wide && c[j] + 8u <= end) {
+        *(g_u32x4 *)to = v[j];
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 8u; ++i)
+          if (c[j] + i < end) to[i] = (uint16_t)(v[j][i / 2u] >> 16u * (i % 2u));
+      }
+    }
   }
 }
 
@@ -540,7 +611,7 @@ struct ExpandFew {
   static constexpr uint32_t kBlock = 2048u * P;             // of B, a wave
   static constexpr uint32_t kRanks = 8u * P * NCH;          // largest rank
   static constexpr uint32_t kRow = 2u * kRanks + 16u;       // a row of u, padded: banks
-  static constexpr uint32_t kLds = 4u * kBlock + 2u * kFew * kRow;
+  static constexpr uint32_t kList = 4u * kBlock + 2u * kFew * kRow, kLds = kList + 4u * kFew;
   static constexpr uint32_t kColumns = 4u * kBlockN;
   static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
                                              uint32_t n0, uint8_t *lds, uint32_t lane, uint32_t wave) {
@@ -553,14 +624,14 @@ struct ExpandFew {
     u32x4 o[4];
     out.load(o, w0 + 8u * c);
     const float scale = s.scales ? s.scales[e] : 1.f;
-    for (uint32_t p = threadIdx.x; p < kFew * kRanks / 8u; p += 256u) {
-      const uint32_t i = p / (kRanks / 8u), r = 8u * (p % (kRanks / 8u));
-      f32x4 v[2] = {};
-      if (i < n && r < s.R) sum_parts(v, g, s, list[i], g.parts, scale, [&](uint32_t j) { return r + 4u * j; });
-      u32x4 h, l;
-      split_bf16(v[0], v[1], h, l);
-      *reinterpret_cast<u32x4 *>(hi + i * kRow + 2u * r) = h;
-      *reinterpret_cast<u32x4 *>(lo + i * kRow + 2u * r) = l;
+    for (uint32_t p = threadIdx.x; p < kFew * kRanks / 4u; p += 256u) {
+      const uint32_t i = p / (kRanks / 4u), r = 4u * (p % (kRanks / 4u)), from = i < n ? list[i] : g.m;
+      f32x4 v[1];
+      sum_parts(v, g, s, g.parts, scale, [&](int) { return from; }, [&](int) { return r; });
+      u32x2 h, l;
+      split_bf16(v[0], h, l);
+      *reinterpret_cast<u32x2 *>(hi + i * kRow + 2u * r) = h;
+      *reinterpret_cast<u32x2 *>(lo + i * kRow + 2u * r) = l;
     }
     __syncthreads();
     U u;
@@ -596,65 +667,106 @@ template <int P, int NCH>
 struct ExpandMany {
   typedef UOperand<P, NCH> U;
   static constexpr uint32_t kBlock = 2048u * P;
-  static constexpr uint32_t kLds = 2u * kBlock;
+  static constexpr uint32_t kList = 2u * kBlock, kLds = kList + 4u * kMany;
   static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
                                              uint32_t parts, uint32_t n0, uint32_t end, uint8_t *lds, uint32_t lane, uint32_t wave) {
+    // Without this the lane's many places in LDS are all kept in registers over the loop around the
+    // call, 40 to 60 of which then spill.
+    asm volatile("" : "+v"(lane));
     const uint32_t c = lane & 15u, q = lane >> 4, rank = own_rank(s, e);
     const auto rb = make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u);
-    const OutRows out(s, list, 16u * wave + 4u * q, n);
     const float scale = s.scales ? s.scales[e] : 1.f;
-    const uint32_t mine = 16u * wave + c;
-    const uint32_t row = list[mine < n ? mine : 0u];
     const bool idle = 16u * wave >= n;  // a wave without a row loads its share of B
-    U u;
-    f32x4 v[2 * U::kAll] = {};
-    if (mine < n)
-      sum_parts(v, g, s, row, parts, scale, [&](uint32_t j) { return (P == 2 ? 8u * (q & 1u) : 32u * (j / 2u) + 8u * q) + 4u * (j % 2u); });
-#pragma unroll
-    for (int k = 0; k < U::kAll; ++k) {
-      u32x4 h, l;
-      split_bf16(v[2 * k], v[2 * k + 1], h, l);
-      if constexpr (P == 2) {
-        u.hi[0] = q < 2u ? h : l;
-      } else {
-        u.hi[k] = h;
-        u.lo[k] = l;
-      }
-    }
     const uint32_t blocks = (end - n0 + kBlockN - 1u) / kBlockN;
+    // Blocks from one that differs from workgroup to workgroup: the same columns of all rows tend to lie in
+    // the same memory channels.
+    const uint32_t turn = blockIdx.x % blocks;
+    auto column = [&](uint32_t i) { return n0 + kBlockN * (i + turn < blocks ? i + turn : i + turn - blocks); };
     auto load_b = [&](uint32_t block, int ch, uint8_t *to) {
 #pragma unroll
-      for (uint32_t i = 0; i < P / 2u; ++i) dma_b<P>(rb, s.R, rank, n0 + kBlockN * block, 64u * ch, wave * (P / 2u) + i, to, lane);
+      for (uint32_t i = 0; i < P / 2u; ++i) dma_b<P>(rb, s.R, rank, column(block), 64u * ch, wave * (P / 2u) + i, to, lane);
     };
-    u32x4 next[4];
     load_b(0, 0, lds);
-    out.load(next, n0 + 8u * c);
-    uint32_t stage = 0;
-    for (uint32_t i = 0; i < blocks; ++i) {
-      const uint32_t n1 = n0 + kBlockN * i + 8u * c;
-      u32x4 o[4];
-      f32x4 acc[8] = {};
+    keep_order();
+    // u of the wave's rows, by way of the second stage: summed with neighbouring lanes on a row
+    U u;
+    uint8_t *const hi = lds + kBlock + kBlock / 8u * wave, *const lo = hi + kBlock / 2u;
 #pragma unroll
-      for (int ch = 0; ch < NCH; ++ch) {
-        INT8W_VMCNT(0);
-        INT8W_LGKMCNT0();
-        asm volatile("s_barrier" ::: "memory");  // this chunk is there for all waves, the other stage is done with
-        if (ch == 0) {
+    for (int ch = 0; ch < NCH; ++ch) {
+      constexpr int kPieces = P / 2;  // a lane: 16 rows of 8 P values
+      f32x4 v[kPieces];
+      auto piece = [&](int i) { return 64u * i + lane; };
+      sum_parts(v, g, s, parts, scale,
+                [&](int i) {
+                  const uint32_t at = 16u * wave + piece(i) / (2u * P);
+                  return at < n ? list[at] : g.m;
+                },
+                [&](int i) { return 64u * ch + 4u * (piece(i) % (2u * P)); });
+      wave_fence();
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = next[r];
-        }
-        uint8_t *const other = lds + (stage ^ 1u) * kBlock;
-        if (ch + 1 < NCH) {
-          load_b(i, ch + 1, other);
-        } else if (i + 1u < blocks) {
-          load_b(i + 1u, 0, other);
-          out.load(next, n1 + kBlockN);
-        }
-        keep_order();
-        if (!idle) multiply_block<P, NCH>(acc, u, ch, lds + stage * kBlock, lane);
-        stage ^= 1u;
+      for (int i = 0; i < kPieces; ++i) {
+        const uint32_t r = piece(i) / (2u * P), half = piece(i) % (2u * P), to = 16u * (r * P + b_swizzle<P>(r, half >> 1)) + 8u * (half & 1u);
+        u32x2 h, l;
+        split_bf16(v[i], h, l);
+        *reinterpret_cast<u32x2 *>(hi + to) = h;
+        *reinterpret_cast<u32x2 *>(lo + to) = l;
       }
-      out.add(o, acc, n1);
+      wave_fence();
+#pragma unroll
+      for (int k = 0; k < U::kSteps; ++k) {
+        const uint32_t from = 16u * (c * P + b_swizzle<P>(c, P == 2 ? q & 1u : 4u * k + q));
+        const int i = U::kSteps * ch + k;
+        if constexpr (P == 2) {
+          u.hi[0] = *reinterpret_cast<const u32x4 *>((q < 2u ? hi : lo) + from);
+        } else {
+          u.hi[i] = *reinterpret_cast<const u32x4 *>(hi + from);
+          u.lo[i] = *reinterpret_cast<const u32x4 *>(lo + from);
+        }
+      }
+    }
+    const OutRows out(s, list, 16u * wave + 4u * q, n);
+    f32x4 acc[8];
+    u32x4 o[4];
+    // One chunk of a block's rank, from stage `at`; the next one goes to `other`.  Two stages with constant places: the
+    // compiler can then tell the DMA's writes from this chunk's reads, and does not wait for them.
+    const uint32_t rows = 16u * wave < n ? n - 16u * wave : 0u, full_stores = out.wide ? rows < 4u ? rows : 4u : 0u;
+    uint32_t stores = 0;  // at least so many of the last block follow the DMA that is waited for, and may go on
+    auto chunk = [&](uint32_t i, int ch, const uint8_t *at, uint8_t *other) {
+      switch (ch == 0 ? stores : 0u) {
+        case 0: INT8W_VMCNT(0); break;
+        case 1: INT8W_VMCNT(1); break;
+        case 2: INT8W_VMCNT(2); break;
+        case 3: INT8W_VMCNT(3); break;
+        default: INT8W_VMCNT(4); break;
+      }
+      INT8W_LGKMCNT0();
+      asm volatile("s_barrier" ::: "memory");  // this chunk is there for all waves, the other stage is done with
+      if (ch == 0) {
+        out.load(o, column(i) + 8u * c);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      if (ch + 1 < NCH)
+        load_b(i, ch + 1, other);
+      else if (i + 1u < blocks)
+        load_b(i + 1u, 0, other);
+      keep_order();
+      if (!idle) multiply_block<P, NCH>(acc, u, ch, at, lane);
+      if (ch + 1 == NCH) {
+        out.add(o, acc, column(i) + 8u * c);
+        stores = column(i) + kBlockN <= s.N ? full_stores : 0u;
+      }
+    };
+    for (uint32_t i = 0; i < blocks;) {
+      if constexpr (NCH == 1) {
+        chunk(i, 0, lds, lds + kBlock);
+        if (++i == blocks) break;
+        chunk(i, 0, lds + kBlock, lds);
+      } else {
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) chunk(i, ch, lds + (ch & 1) * kBlock, lds + (~ch & 1) * kBlock);
+      }
+      ++i;
     }
     __syncthreads();
   }
@@ -676,9 +788,9 @@ template <int P, int NCH>
 __global__ __launch_bounds__(256) void k_expand_rows(const LoraArgs g) {
   typedef ExpandFew<P, NCH> Few;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ uint32_t list[kFew];
+  uint32_t *const list = reinterpret_cast<uint32_t *>(lds + Few::kList);
   uint32_t tile = blockIdx.x;
-  const LoraStack &s = stack_of(g, tile, Few::kColumns);
+  const LoraStack s = stack_of(g, tile, Few::kColumns);
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6), i = blockIdx.y, n0 = tile * Few::kColumns;
   const uint32_t own = lane < g.m ? g.ids[lane] : INT8W_NO_ADAPTER, id = (uint32_t)__builtin_amdgcn_readlane((int)own, (int)i);
   if (id >= g.num) {
@@ -691,24 +803,42 @@ __global__ __launch_bounds__(256) void k_expand_rows(const LoraArgs g) {
   Few::run(g, s, id, list, n, n0, lds, lane, wave);
 }
 
-// grid (chunks of chunk_n columns of all stacks, slots, plans).
+// grid (blocks, 64 plans): the blocks take the groups' runs of 128-column blocks (the stacks' one after the
+// other) in turn, as many runs as give each workgroup one.
 template <int P, int NCH>
-__global__ __launch_bounds__(256, NCH == 1 ? 3 : 2) void k_expand_items(const LoraArgs g, uint32_t chunk_n) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[ExpandMany<P, NCH>::kLds];
-  __shared__ uint32_t list[kMany];
-  uint32_t tile = blockIdx.x;
-  const LoraStack &s = stack_of(g, tile, chunk_n);
+__global__ __launch_bounds__(256, NCH == 1 ? 4 : 2) void k_expand_items(const LoraArgs g, uint32_t column_blocks) {
+  // one dynamic array: behind a static one of its own the compiler waits for the DMA before every read
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  uint32_t *const list = reinterpret_cast<uint32_t *>(lds + ExpandMany<P, NCH>::kList);
   const uint32_t lane = threadIdx.x & 63u, wave = uniform32(threadIdx.x >> 6);
-  const uint32_t n0 = tile * chunk_n, end = n0 + chunk_n < s.N ? n0 + chunk_n : s.N;
-  const LoraPlan &plan = reinterpret_cast<const LoraPlan *>(g.plans)[blockIdx.z];
-  const uint32_t items = uniform32(plan.items), parts = uniform32(plan.parts);
-  for (uint32_t i = blockIdx.y; i < items; i += gridDim.y)
-    with_item(plan, i, list, [&](uint32_t e, uint32_t n) {
-      if (e >= g.num)
-        pass_rows(s, list, n, e != g.num, n0, end);
-      else
-        ExpandMany<P, NCH>::run(g, s, e, list, n, parts, n0, end, lds, lane, wave);
+  const Groups groups(g, 64u * blockIdx.y, lane);
+  uint32_t steps;
+  const uint32_t parts = groups.parts(g, steps);
+  uint32_t runs = gridDim.x / groups.total;
+  runs = runs < 1u ? 1u : runs > column_blocks ? column_blocks : runs;
+  const uint32_t run = (column_blocks + runs - 1u) / runs;
+  runs = (column_blocks + run - 1u) / run;
+  each_share(groups.total * runs, [&](uint32_t i) {
+    groups.with(i % groups.total, list, [&](uint32_t e, uint32_t n) {
+      uint32_t at = i / groups.total * run, left = run;
+      for (uint32_t k = 0; k < g.count && left; ++k) {
+        const LoraStack s = g.s[k];
+        const uint32_t blocks = (s.N + kBlockN - 1u) / kBlockN;
+        if (at >= blocks) {
+          at -= blocks;
+          continue;
+        }
+        const uint32_t here = left < blocks - at ? left : blocks - at, n0 = at * kBlockN;
+        const uint32_t end = n0 + here * kBlockN < s.N ? n0 + here * kBlockN : s.N;
+        if (e >= g.num)
+          pass_rows(s, list, n, e != g.num, n0, end);
+        else
+          ExpandMany<P, NCH>::run(g, s, e, list, n, parts, n0, end, lds, lane, wave);
+        at = 0;
+        left -= here;
+      }
     });
+  });
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -716,33 +846,29 @@ __global__ __launch_bounds__(256, NCH == 1 ? 3 : 2) void k_expand_items(const Lo
 bool planned(const LoraArgs &a) { return a.m > kBallotRows; }
 uint32_t plans(const LoraArgs &a) { return (a.m + kLoraPlanRows - 1u) / kLoraPlanRows; }
 
-// Workgroups that share a plan's groups: a prompt's rows make 16.
-uint32_t slots(const LoraArgs &a, uint32_t others) {
-  const uint32_t most = a.m < 64u ? a.m : 64u, want = 2048u / (plans(a) * others);
-  return want < 16u ? 16u : want < most ? want : most;
-}
-
 uint32_t k_steps(const LoraArgs &a) { return (a.K + kStepK - 1u) / kStepK; }
 
-// Workgroups of shrink that share a plan's groups and parts.
-uint32_t shrink_blocks(const LoraArgs &a) {
-  const uint32_t n = kShrinkBlocks / (plans(a) * a.count);
-  return n < 16u ? 16u : n;
+// Workgroups of each 64 plans.
+uint32_t blocks_of(const LoraArgs &a, uint32_t blocks) {
+  const uint32_t n = blocks / ((plans(a) + 63u) / 64u);
+  return n < 64u ? 64u : n & ~7u;
 }
 
-// How K is cut: two steps a wave.  With a plan that is the most; the plan may take fewer parts.
+// How K is cut: two steps a wave.  With a plan that is the most; the groups may be too many for it.
 void cut_k(LoraArgs &a) {
   a.part_steps = 8u;
   a.parts = (k_steps(a) + 7u) / 8u;
   if (planned(a)) {
-    const uint32_t most = shrink_blocks(a) / ((a.m + plans(a) * kMany - 1u) / (plans(a) * kMany));  // groups of a plan at least
-    a.parts = a.parts < most ? a.parts : most < 1u ? 1u : most;
+    const uint32_t least = ((a.m < 64u * kLoraPlanRows ? a.m : 64u * kLoraPlanRows) + kMany - 1u) / kMany;  // groups of the first plans
+    const uint32_t most = kShrinkBlocks / least;
+    a.parts = most < 1u ? 1u : a.parts < most ? a.parts : most;
   }
 }
 
+// The LDS of a kernel that has dynamic LDS alone.
 template <class Kern>
-hipError_t allow(LdsAllowance &allowance, Kern kern, uint32_t dynamic_bytes, uint32_t static_bytes) {
-  return needs_lds_allowance(dynamic_bytes, static_bytes) ? allow_lds(allowance, kern, (int)dynamic_bytes) : hipSuccess;
+hipError_t allow(LdsAllowance &allowance, Kern kern, uint32_t bytes) {
+  return needs_lds_allowance(bytes, 0) ? allow_lds(allowance, kern, (int)bytes) : hipSuccess;
 }
 
 template <int RT>
@@ -750,15 +876,15 @@ hipError_t launch_shrink(const LoraArgs &a, hipStream_t stream) {
   if (!planned(a)) {
     constexpr uint32_t lds = ShrinkFew<RT>::kLds;
     static LdsAllowance allowance;
-    const hipError_t e = allow(allowance, k_shrink_rows<RT>, lds, 0);
+    const hipError_t e = allow(allowance, k_shrink_rows<RT>, lds);
     if (e != hipSuccess) return e;
     k_shrink_rows<RT><<<dim3(a.parts, a.m, a.count), 256, lds, stream>>>(a);
   } else {
     constexpr uint32_t lds = ShrinkFew<RT>::kLds > ShrinkMany<RT>::kLds ? ShrinkFew<RT>::kLds : ShrinkMany<RT>::kLds;
     static LdsAllowance allowance;
-    const hipError_t e = allow(allowance, k_shrink_items<RT>, lds, 0);
+    const hipError_t e = allow(allowance, k_shrink_items<RT>, lds);
     if (e != hipSuccess) return e;
-    k_shrink_items<RT><<<dim3(shrink_blocks(a), plans(a), a.count), 256, lds, stream>>>(a);
+    k_shrink_items<RT><<<dim3(blocks_of(a, kShrinkBlocks), (plans(a) + 63u) / 64u, a.count), 256, lds, stream>>>(a);
   }
   return hipGetLastError();
 }
@@ -769,15 +895,14 @@ hipError_t launch_expand(const LoraArgs &a, hipStream_t stream) {
   uint32_t tiles = 0;
   if (!planned(a)) {
     static LdsAllowance allowance;
-    const hipError_t e = allow(allowance, k_expand_rows<P, NCH>, Few::kLds, sizeof(uint32_t[kFew]));
+    const hipError_t e = allow(allowance, k_expand_rows<P, NCH>, Few::kLds);
     if (e != hipSuccess) return e;
     for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + Few::kColumns - 1u) / Few::kColumns;
     k_expand_rows<P, NCH><<<dim3(tiles, a.m), 256, Few::kLds, stream>>>(a);
     return hipGetLastError();
   }
-  const uint32_t chunk_n = a.m > 256u ? 2u * Few::kColumns : Few::kColumns;
-  for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + chunk_n - 1u) / chunk_n;
-  k_expand_items<P, NCH><<<dim3(tiles, slots(a, tiles), plans(a)), 256, 0, stream>>>(a, chunk_n);
+  for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + kBlockN - 1u) / kBlockN;
+  k_expand_items<P, NCH><<<dim3(blocks_of(a, kExpandBlocks), (plans(a) + 63u) / 64u), 256, ExpandMany<P, NCH>::kLds, stream>>>(a, tiles);
   return hipGetLastError();
 }
 
@@ -807,8 +932,7 @@ hipError_t launch_lora(LoraArgs a, void *ws, hipStream_t stream) {
   if (planned(a)) {
     uint32_t bits = 1;
     while (a.num + 1u >> bits) ++bits;  // ids up to num + 1
-    k_plan<<<plans(a), kLoraPlanRows, 0, stream>>>(a.ids, a.m, a.num, bits, k_steps(a), a.parts, shrink_blocks(a),
-                                                          reinterpret_cast<LoraPlan *>(ws));
+    k_plan<<<plans(a), kLoraPlanRows, 0, stream>>>(a.ids, a.m, a.num, bits, reinterpret_cast<LoraPlan *>(ws));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
