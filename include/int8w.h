@@ -286,15 +286,14 @@ int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const 
 /* ---- The routing to experts, for int8_moe_gemv, the layers below or a caller's own.  For
  * token t with router logits l [num_experts]:
  *   s_e = e^(l_e) / sum e^l (INT8W_ROUTE_SOFTMAX) or 1 / (1 + e^(-l_e)) (INT8W_ROUTE_SIGMOID);
- *   c_e = s_e + bias_e: what the choice goes by (s alone makes the weights);
+ *   c_e = s_e + bias_e, or l_e without a bias: what the choice goes by (s alone makes the weights);
  *   of `groups` groups of num_experts / groups consecutive experts the topk_groups of the
  *   largest score stay, a group's score being its largest c (INT8W_GROUP_MAX) or the sum of
- *   its two largest (INT8W_GROUP_TOP2; of one, where a single expert is left);
+ *   its two largest s_e + bias_e (INT8W_GROUP_TOP2; of one, where a single expert is left);
  *   the topk experts of largest c in them are taken, largest first;
  *   weight = routed_scale * s_e, with renormalize routed_scale * s_e / (sum of the taken s)
  *   (0 where that sum is 0).
- * Equal values go to the lower index.  Scores are compared in 64 bits; without a bias and
- * groups c orders as l, which is then compared itself.  An expert whose l or c is -inf is never
+ * Equal values go to the lower index.  Scores are compared as if formed in 64 bits.  An expert whose l or c is -inf is never
  * taken; the slots that no expert is left for hold the id INT8W_NO_EXPERT and weight 0.  A token
  * with a NaN among its l or c, or with softmax a +inf among its l, gets INT8W_NO_EXPERT and NaN
  * weights in all its slots.

@@ -49,7 +49,7 @@ def route(logits, topk, scoring="softmax", bias=None, groups=1, topk_groups=None
     topk_groups = groups if topk_groups is None else topk_groups
     size = E // groups
     ids, weights = np.full((T, topk), -1), np.zeros((T, topk))
-    direct = bias is None and groups == 1
+    direct = bias is None
     for t in range(T):
         l = logits[t]
         b = np.zeros(E) if bias is None else bias.astype(np.float64)
@@ -67,11 +67,12 @@ def route(logits, topk, scoring="softmax", bias=None, groups=1, topk_groups=None
             weights[t] = np.nan
             continue
         c = {e: l[e] if direct else s[e] + b[e] for e in free}
+        two = {e: s[e] + b[e] for e in free}
         free = [e for e in free if c[e] > -np.inf]
         if groups > 1:
             of = {}
             for g in range(groups):
-                best = sorted((c[e] for e in free if e // size == g), reverse=True)[:2]
+                best = sorted(((two if group_score == "top2" else c)[e] for e in free if e // size == g), reverse=True)[:2]
                 if best:
                     of[g] = sum(best) if group_score == "top2" else best[0]
             stay = sorted((g for g in of if of[g] > -np.inf), key=lambda g: (-of[g], g))[:topk_groups]

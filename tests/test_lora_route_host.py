@@ -195,9 +195,31 @@ def test_a_wrong_topk_is_refused_before_it_sizes_the_scratch(topk, monkeypatch):
 
 
 def test_another_device_is_made_current_for_the_launch(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    assert isinstance(B._on(torch.device("cuda", 0)), torch.cuda.device)
+    seen = []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(self.device)
+
+        def __exit__(self, *exc):
+            seen.append("back")
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", Device)
     for here in (torch.device("cuda", 1), torch.device("cuda"), torch.device("cpu")):
-        with B._on(here):
-            pass
-        assert not isinstance(B._on(here), torch.cuda.device)
+        B._call(here, lambda *a: B.INT8W_OK, 1, 2)
+    assert seen == []
+    B._call(torch.device("cuda", 0), lambda *a: B.INT8W_OK)
+    assert seen == [torch.device("cuda", 0), "back"]
+    with pytest.raises(B.Int8wError):
+        B._call(torch.device("cuda", 0), lambda *a: B.INT8W_ERR_SHAPE)
+    assert seen[2:] == [torch.device("cuda", 0), "back"]
+
+
+def test_packed_arguments_are_the_structures():
+    c = route(bias=9 * A, tokens=7, experts=60, topk=3, scoring=1, groups=6, topk_groups=2, group_score=1)
+    packed = B._ROUTE_CALL.pack(A, 9 * A, 2 * A, 3 * A, 7, 60, 3, 1, 1, 6, 2, 1, 1, 1.0)
+    assert bytes(B.RouteCall.from_buffer_copy(packed))[:72] == bytes(c)[:72]
+    assert B._LORA_OUT.pack(4 * A, 5 * A, 96, 97) == bytes(out(ys=97))

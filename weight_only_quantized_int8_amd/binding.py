@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -170,6 +171,10 @@ class LoraOut(ctypes.Structure):
     ]
 
 
+_ROUTE_CALL = struct.Struct("PPPP9If")  # int8w_route_call
+_LORA_OUT = struct.Struct("PPQQ")  # int8w_lora_out
+assert _ROUTE_CALL.size == ctypes.sizeof(RouteCall) and _LORA_OUT.size == ctypes.sizeof(LoraOut)
+
 _lib = None
 
 
@@ -246,6 +251,15 @@ def load_library() -> ctypes.CDLL:
     lib.int8w_lora_workspace_bytes.restype = u64
     lib.int8w_lora_add.argtypes = [L, ctypes.POINTER(LoraOut), u32, P, u64, P, u32, P, u64, u64]
     lib.int8w_lora_add.restype = ctypes.c_int
+    # The same entries for argument blocks packed as bytes: filling a ctypes structure by its fields took 1.5 us
+    # of a routing call's 8, and packing takes 0.4.
+    lib.packed_route = lib["int8w_moe_route"]
+    lib.packed_route.argtypes, lib.packed_route.restype = [P, u64], ctypes.c_int
+    lib.packed_lora_bytes = lib["int8w_lora_workspace_bytes"]
+    lib.packed_lora_bytes.argtypes, lib.packed_lora_bytes.restype = [P, u32, u32], u64
+    lib.packed_lora_add = lib["int8w_lora_add"]
+    lib.packed_lora_add.argtypes = [P, P, u32, P, u64, P, u32, P, u64, u64]
+    lib.packed_lora_add.restype = ctypes.c_int
     lib.int8w_stream_read.argtypes = [P, u64, P, u64]
     lib.int8w_stream_read.restype = ctypes.c_int
     lib.int8w_stream_copy.argtypes = [P, P, u64, u64]
@@ -807,19 +821,20 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: t
     among its logits has id -1 and weight NaN in all its slots.  ids goes to moe_gemv (which gives NaN for an
     id of -1), both to moe_layer_routed.
     """
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or not logits.is_contiguous() \
-            or logits.device.type != "cuda":
+    dev, f32 = logits.device, logits.dtype is torch.float32
+    if not (f32 or logits.dtype is torch.bfloat16) or logits.dim() != 2 or not logits.is_contiguous() or dev.type != "cuda":
         raise ValueError("logits must be a contiguous float32 or bfloat16 [tokens, num_experts] GPU tensor")
-    if scoring not in ROUTE_SCORING or group_score not in GROUP_SCORES:
+    how, of_group = ROUTE_SCORING.get(scoring), GROUP_SCORES.get(group_score)
+    if how is None or of_group is None:
         raise ValueError(f"scoring is one of {sorted(ROUTE_SCORING)}, group_score one of {sorted(GROUP_SCORES)}")
-    (T, E), dev = logits.shape, logits.device
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or bias.device != dev
+    T, E = logits.shape
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (E,) or bias.device != dev
                              or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 [{E}] tensor on the logits' GPU")
     topk, groups = int(topk), int(groups)
     topk_groups = groups if topk_groups is None else int(topk_groups)
-    if min(topk, groups, topk_groups) < 1:  # before they size the outputs
-        raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk}, groups {groups}, topk_groups {topk_groups}: below 1")
+    if not (1 <= topk <= MAX_MOE_TOPK and 1 <= groups <= MAX_MOE_GROUPS and 1 <= topk_groups <= groups):  # before they size the outputs
+        raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk}, groups {groups} or topk_groups {topk_groups} out of range")
     if ids is None:
         ids = logits.new_empty((T, topk), dtype=torch.int32)
     else:
@@ -828,11 +843,10 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: t
         weights = logits.new_empty((T, topk), dtype=torch.float32)
     else:
         _need_slots(weights, "weights", (torch.float32,), T, topk, dev)
-    call = RouteCall(logits.data_ptr(), bias.data_ptr() if bias is not None else None, ids.data_ptr(), weights.data_ptr(),
-                     T, E, topk, VALUES_F32 if logits.dtype == torch.float32 else VALUES_BF16, ROUTE_SCORING[scoring],
-                     groups, topk_groups, GROUP_SCORES[group_score], bool(renormalize), routed_scale)
-    with _on(dev):
-        _check(load_library().int8w_moe_route(call, _stream_of(dev)))
+    _call(dev, load_library().packed_route,
+          _ROUTE_CALL.pack(logits.data_ptr(), bias.data_ptr() if bias is not None else 0, ids.data_ptr(), weights.data_ptr(), T, E, topk,
+                           VALUES_F32 if f32 else VALUES_BF16, how, groups, topk_groups, of_group, bool(renormalize), routed_scale),
+          _stream_of(dev))
     return ids, weights
 
 
@@ -871,32 +885,30 @@ def moe_layer_routed(gate, up, down, num_experts: int, x: torch.Tensor, ids: tor
     ws = x.new_empty(int8w_moe_workspace_bytes(T, topk, inner, hidden), dtype=torch.uint8)  # the call's own, as in moe_layer
     call = MoeRoutedCall(x.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                          x_resid.data_ptr() if x_resid is not None else None, y.data_ptr(), T, topk)
-    layer = int8w_mxfp4_moe_layer_routed if mx else int8_moe_layer_routed
-    with _on(dev):
-        _check(layer(gate.desc, up.desc, down.desc, E, call, ws.data_ptr(), ws.numel(), _stream_of(dev)))
+    lib = load_library()
+    layer = lib.int8w_mxfp4_moe_layer_routed if mx else lib.int8_moe_layer_routed
+    _call(dev, layer, gate.desc, up.desc, down.desc, E, call, ws.data_ptr(), ws.numel(), _stream_of(dev))
     return y
 
 
 def _need_slots(t: torch.Tensor, name: str, dtypes, tokens: int, topk: int, device: torch.device) -> None:
-    if t.dtype not in dtypes or tuple(t.shape) != (tokens, topk) or t.device != device or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != (tokens, topk) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {' or '.join(map(str, dtypes))} [{tokens}, {topk}] tensor on {device}")
 
 
-class _Here:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # without a check for initialisation
 
 
-_HERE = _Here()
-
-
-def _on(device: torch.device):
-    """Kernels go to the current device where the stream is the default one (handle 0), so a call on
-    another device's tensors makes that device current for its launch."""
-    return _HERE if device.index is None or device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _call(device: torch.device, entry, *args) -> None:
+    """Calls a C entry that launches on `device`.  Kernels go to the current device where the stream is the default
+    one (handle 0), so another device is made current for the launch."""
+    if device.index is None or device.index == _current_device():
+        rc = entry(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args)
+    if rc != INT8W_OK:
+        _check(rc)
 
 
 class LoraAdapters:
@@ -931,6 +943,7 @@ class LoraAdapters:
         self.device = a.device
         self.desc = LoraDesc(a.data_ptr(), b.data_ptr(), scales.data_ptr() if scales is not None else None,
                              ranks.data_ptr() if ranks is not None else None, num, rank, k, n)
+        self.packed = bytes(self.desc)  # as lora_add passes it
 
     @classmethod
     def from_list(cls, adapters) -> "LoraAdapters":
@@ -956,11 +969,11 @@ class LoraAdapters:
 
 def _rows(t: torch.Tensor, name: str, m: int, n: int, device: torch.device) -> int:
     """Checks a [m, n] matrix of bfloat16 whose rows may be apart (columns of a wider one); returns its row stride."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, adapters on {device}")
-    if t.dim() != 2 or t.shape[0] != m or t.shape[1] != n:
+    if t.shape != (m, n):
         raise ValueError(f"{name} must be [{m}, {n}]")
     rs, cs = t.stride()
     if m <= 1:
@@ -980,8 +993,7 @@ def _need_pool(pool: LoraAdapters, k: int, n: int, x: torch.Tensor, ids: torch.T
 
 
 def _need_ids(ids: torch.Tensor, m: int, device: torch.device) -> None:
-    if ids.dtype not in (torch.int32, torch.uint32) or tuple(ids.shape) != (m,) or ids.device != device \
-            or not ids.is_contiguous():
+    if ids.dtype not in (torch.int32, torch.uint32) or ids.shape != (m,) or ids.device != device or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous 32-bit [{m}] tensor on {device}")
 
 
@@ -1005,38 +1017,39 @@ def lora_add(adapters, x: torch.Tensor, ids: torch.Tensor, base=None, y=None):
     Scratch is allocated for the call on the current stream, so calls may overlap on several streams.
     """
     one = isinstance(adapters, LoraAdapters)
-    pools = (adapters,) if one else tuple(adapters)
+    if one:
+        pools, bases, ys = (adapters,), (base,), [y]
+    else:
+        pools = tuple(adapters)
+        bases = (None,) * len(pools) if base is None else tuple(base)
+        ys = [None] * len(pools) if y is None else list(y)
     count = len(pools)
     if not 1 <= count <= MAX_MULTI:
         raise Int8wError(INT8W_ERR_SHAPE, f"lora_add takes 1..{MAX_MULTI} pools, got {count}")
-    p0 = pools[0]
-    dev, k = p0.device, p0.in_features
+    if len(bases) != count or len(ys) != count:
+        raise ValueError("lora_add: one base and one output per pool")
+    dev, k = pools[0].device, pools[0].in_features
     if x.dim() != 2 or x.shape[1] != k:
         raise ValueError(f"x must be [m, {k}]")
     m = x.shape[0]
     xs = _rows(x, "x", m, k, dev)
     _need_ids(ids, m, dev)
-    bases = (base,) if one else (None,) * count if base is None else tuple(base)
-    ys = [y] if one else [None] * count if y is None else list(y)
-    if len(bases) != count or len(ys) != count:
-        raise ValueError("lora_add: one base and one output per pool")
-    descs, outs = (LoraDesc * count)(), (LoraOut * count)()
+    descs = outs = b""
     for i, pool in enumerate(pools):
         if pool.device != dev:
             raise ValueError("lora_add: pools on different devices")
         n, b, o = pool.out_features, bases[i], ys[i]
-        bs = _rows(b, "base", m, n, dev) if b is not None else 0
         if o is None:
             o = ys[i] = x.new_empty((m, n))
             os = n
         else:
             os = _rows(o, "y", m, n, dev)
-        descs[i] = pool.desc
-        outs[i] = LoraOut(b.data_ptr() if b is not None else None, o.data_ptr(), bs, os)
+        descs += pool.packed
+        outs += _LORA_OUT.pack(0, o.data_ptr(), 0, os) if b is None else \
+            _LORA_OUT.pack(b.data_ptr(), o.data_ptr(), _rows(b, "base", m, n, dev), os)
     lib = load_library()
-    need = lib.int8w_lora_workspace_bytes(descs, count, m)
-    ws = x.new_empty(need, dtype=torch.uint8)  # a call's own: one kept for the device would be shared by streams and graphs
-    with _on(dev):
-        _check(lib.int8w_lora_add(descs, outs, count, x.data_ptr(), xs, ids.data_ptr(), m, ws.data_ptr(), need,
-                                  _stream_of(dev)))
+    need = lib.packed_lora_bytes(descs, count, m)
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None  # a call's own: one kept for the device would be shared by streams and graphs
+    _call(dev, lib.packed_lora_add, descs, outs, count, x.data_ptr(), xs, ids.data_ptr(), m, ws.data_ptr() if need else 0, need,
+          _stream_of(dev))
     return ys[0] if one else ys

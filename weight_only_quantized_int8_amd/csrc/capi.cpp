@@ -869,7 +869,7 @@ int int8w_lora_add(const int8w_lora *pools, const int8w_lora_out *out, uint32_t 
   int rc = validate_lora_pools(pools, count, m);
   if (rc) return rc;
   if (m == 0) return ok();
-  if (!out || !x || !ids || !workspace) return fail(INT8W_ERR_NULL, "out, x, ids or workspace is NULL");
+  if (!out || !x || !ids) return fail(INT8W_ERR_NULL, "out, x or ids is NULL");
   LoraArgs a = lora_args(pools, count, m);
   constexpr uint64_t kMaxStride = 1ull << 32;
   if (x_stride < a.K || x_stride % 8u != 0 || x_stride > kMaxStride)
@@ -880,6 +880,7 @@ int int8w_lora_add(const int8w_lora *pools, const int8w_lora_out *out, uint32_t 
   if (!aligned(workspace, 256)) return fail(INT8W_ERR_ALIGN, "workspace is not 256-byte aligned");
   uint64_t offsets[INT8W_MAX_MULTI];
   const uint64_t need = lora_workspace(a, offsets);
+  if (need && !workspace) return fail(INT8W_ERR_NULL, "workspace is NULL");
   if (workspace_bytes < need)
     return fail(INT8W_ERR_SHAPE, "workspace of %llu bytes, this call needs %llu", (unsigned long long)workspace_bytes,
                 (unsigned long long)need);

@@ -148,8 +148,8 @@ struct RouteArgs {
   uint32_t *ids;       // [tokens, topk]
   float *weights;
   uint32_t tokens, E, topk, groups, topk_groups;
-  uint32_t group_size, group_magic;  // set by the launcher
-  bool logits_bf16, sigmoid, top2, renorm;
+  uint32_t group_size, group_magic, group_lanes;  // set by the launcher, as whole and whole_bias
+  bool logits_bf16, sigmoid, top2, renorm, whole, whole_bias;
   float scale;
 };
 hipError_t launch_route(RouteArgs a, hipStream_t stream);

@@ -21,6 +21,7 @@
 // A row is a row or column of the products, which do not mix: what another row or its adapter
 // holds (infinities, NaN) does not reach it.
 #include "rows_stream.h"
+#include "token_stream.h"
 
 namespace int8w {
 
@@ -841,10 +842,128 @@ __global__ __launch_bounds__(256, NCH == 1 ? 4 : 2) void k_expand_items(const Lo
   });
 }
 
+// ---- one launch for a few rows ---------------------------------------------------------------
+// A workgroup of 16 waves forms all of u for its row, on the vector ALUs with rows of A as they lie in memory, and
+// then 512 columns of y: A is read again for each 512 columns, out of the caches, which costs less than a
+// second launch as long as it is small.  u stays in fp32.
+constexpr uint32_t kSoloColumns = 512;
+constexpr uint32_t kSoloK = 16384;  // most of x in LDS
+
+// P2: 16-byte pieces of a column of B a thread, two threads a column (rank up to 16 P2).
+template <int P2>
+__global__ __launch_bounds__(1024) void k_solo(const LoraArgs g) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // x
+  __shared__ __attribute__((aligned(16))) float u[16 * P2];
+  __shared__ float half_u[16];
+  constexpr uint32_t kChunk = 512, kAhead = 8;  // values of a row a load of the wave; loads in flight
+  uint32_t tile = blockIdx.x;
+  const LoraStack s = stack_of(g, tile, kSoloColumns);
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = uniform32(tid >> 6), i = blockIdx.y, n0 = tile * kSoloColumns;
+  const uint32_t id = uniform32(g.ids[i]);
+  const g_u16 *const x = (const g_u16 *)g.x + i * g.x_stride;
+  for (uint32_t p = 8u * tid; p < g.K; p += 8u * 1024u) *reinterpret_cast<u32x4 *>(lds + 2u * p) = *(const g_u32x4 *)(x + p);
+  if (id >= g.num) {
+    const uint32_t row[1] = {i}, end = n0 + kSoloColumns < s.N ? n0 + kSoloColumns : s.N;
+    if (tid < 256u) pass_rows(s, row, 1u, id != INT8W_NO_ADAPTER, n0, end);
+    return;
+  }
+  const uint32_t rank = own_rank(s, id), n = n0 + tid / 2u;
+  const float scale = s.scales ? s.scales[id] : 1.f;
+  // this thread's part of its column of B, and base, while A comes
+  u32x4 b[P2];
+  const auto rb = make_rsrc(s.b + (size_t)id * s.N * s.R, s.N * s.R * 2u);
+#pragma unroll
+  for (uint32_t j = 0; j < P2; ++j) {
+    const uint32_t r = 8u * (P2 * (tid & 1u) + j);
+    b[j] = buf_load_b128(rb, r < rank ? (n * s.R + r) * 2u : kOutOfRange);  // past the last column: zeros
+  }
+  const bool write = (tid & 1u) == 0u && n < s.N;
+  const float base = write && s.base ? bf16_bits_to_f32(((const g_u16 *)s.base)[i * s.base_stride + n]) : 0.f;
+  keep_order();
+  // rows of A: a wave has row wave, wave + 16, ..; of eight rows two waves share each, a half of K apiece
+  const bool halves = s.R == 8u;
+  const uint32_t chunks = (g.K + kChunk - 1u) / kChunk, c0 = halves && wave >= 8u ? chunks / 2u : 0u, c1 = halves && wave < 8u ? chunks / 2u : chunks;
+  const auto ra = make_rsrc(s.a + (size_t)id * s.R * g.K, s.R * g.K * 2u);
+  bool staged = false;
+  for (uint32_t r = halves ? wave % 8u : wave; r < s.R; r += 16u) {
+    float sum = 0.f;
+    for (uint32_t c = c0; c < c1; c += kAhead) {
+      u32x4 a[kAhead];
+#pragma unroll
+      for (uint32_t j = 0; j < kAhead; ++j) {
+        const uint32_t k = (c + j) * kChunk + 8u * lane;
+        a[j] = buf_load_b128(ra, r < rank && c + j < c1 && k < g.K ? (r * g.K + k) * 2u : kOutOfRange);
+      }
+      keep_order();
+      if (!staged) {
+        __syncthreads();
+        staged = true;
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kAhead; ++j) {
+        const uint32_t k = (c + j) * kChunk + 8u * lane;
+        if (c + j < c1 && k < g.K) {
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + 2u * k);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) sum = dot2(a[j][t], v[t], sum);
+        }
+      }
+    }
+    sum = token_sum(sum);
+    if (lane == 0u) {
+      if (halves && wave >= 8u)
+        half_u[r] = sum;
+      else
+        u[r] = sum;
+    }
+  }
+  if (!staged) __syncthreads();
+  if (tid >= s.R && tid < 16u * P2) u[tid] = 0.f;
+  __syncthreads();
+  float v = 0.f;
+#pragma unroll
+  for (uint32_t j = 0; j < P2; ++j) {
+    const uint32_t r = 8u * (P2 * (tid & 1u) + j);
+    const f32x4 lo = *reinterpret_cast<const f32x4 *>(u + r), hi = *reinterpret_cast<const f32x4 *>(u + r + 4u);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float even = t < 2 ? lo[2 * t] : hi[2 * t - 4], odd = t < 2 ? lo[2 * t + 1] : hi[2 * t - 3];
+      if (halves && r == 0u) {
+        even += half_u[2 * t];
+        odd += half_u[2 * t + 1];
+      }
+      v = __builtin_fmaf(bf16_lo(b[j][t]), even, v);
+      v = __builtin_fmaf(bf16_hi(b[j][t]), odd, v);
+    }
+  }
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0xB1, 0xF, 0xF, true));  // the neighbour's
+  if (write) ((g_u16 *)s.y)[i * s.y_stride + n] = to_bf16_bits(base + scale * v);
+}
+
 // ---- host ----------------------------------------------------------------------------------
 
 bool planned(const LoraArgs &a) { return a.m > kBallotRows; }
 uint32_t plans(const LoraArgs &a) { return (a.m + kLoraPlanRows - 1u) / kLoraPlanRows; }
+
+uint32_t max_rank(const LoraArgs &a) {
+  uint32_t r = 0;
+  for (uint32_t i = 0; i < a.count; ++i) r = a.s[i].R > r ? a.s[i].R : r;
+  return r;
+}
+
+// One launch for few rows of small A's, by what its workgroups read of A in all and each after the other.  us with one launch /
+// with two (a graph of calls; outside one the second launch costs the host 2.5 more):
+// 4096x4096, rank 16 (A 128 KiB): 1 row 3.9 / 6.5, 16 rows (17 MB) 5.5 / 6.8, 32 (34 MB) 7.0 / 7.0, 48 10.2 / 8.4;
+// q, k and v of rank 32 (256 KiB): 8 rows (25 MB) 7.4 / 7.8, 32 (100 MB) 16.5 / 11.8;
+// gate and up of 14336x4096, rank 16: 4 rows (29 MB) 5.1 / 6.8, 8 (57 MB) 8.7 / 7.6;
+// 4096x14336, rank 16 (448 KiB): 1 row (3.7 MB) 7.1 / 8.0, 4 (15 MB) 9.4 / 8.5; rank 64 (1.8 MB): 1 row 24.8 / 9.7.
+bool solo(const LoraArgs &a) {
+  uint64_t all = 0;
+  for (uint32_t i = 0; i < a.count; ++i) all += (uint64_t)((a.s[i].N + kSoloColumns - 1u) / kSoloColumns) * a.s[i].R;
+  all *= 2u * (uint64_t)a.K * a.m;
+  const uint64_t each = 2u * (uint64_t)a.K * max_rank(a);
+  return a.K <= kSoloK && max_rank(a) <= 64u && all <= (each <= (256u << 10) ? 40000000u : each <= (512u << 10) ? 8000000u : 0u);
+}
 
 uint32_t k_steps(const LoraArgs &a) { return (a.K + kStepK - 1u) / kStepK; }
 
@@ -869,6 +988,14 @@ void cut_k(LoraArgs &a) {
 template <class Kern>
 hipError_t allow(LdsAllowance &allowance, Kern kern, uint32_t bytes) {
   return needs_lds_allowance(bytes, 0) ? allow_lds(allowance, kern, (int)bytes) : hipSuccess;
+}
+
+template <int P2>
+hipError_t launch_solo(const LoraArgs &a, hipStream_t stream) {
+  uint32_t tiles = 0;
+  for (uint32_t i = 0; i < a.count; ++i) tiles += (a.s[i].N + kSoloColumns - 1u) / kSoloColumns;
+  k_solo<P2><<<dim3(tiles, a.m), 1024, (a.K * 2u + 15u) & ~15u, stream>>>(a);
+  return hipGetLastError();
 }
 
 template <int RT>
@@ -910,6 +1037,7 @@ hipError_t launch_expand(const LoraArgs &a, hipStream_t stream) {
 
 uint64_t lora_workspace(const LoraArgs &given, uint64_t *offsets) {
   LoraArgs a = given;
+  if (solo(a)) return 0;
   cut_k(a);
   uint64_t bytes = planned(a) ? plans(a) * kLoraPlanBytes : 0u;
   for (uint32_t i = 0; i < a.count; ++i) {
@@ -920,14 +1048,12 @@ uint64_t lora_workspace(const LoraArgs &given, uint64_t *offsets) {
 }
 
 hipError_t launch_lora(LoraArgs a, void *ws, hipStream_t stream) {
+  const uint32_t R = max_rank(a);
+  if (solo(a)) return R <= 16u ? launch_solo<1>(a, stream) : R <= 32u ? launch_solo<2>(a, stream) : launch_solo<4>(a, stream);
   cut_k(a);
   uint64_t offsets[INT8W_MAX_MULTI];
   lora_workspace(a, offsets);
-  uint32_t R = 0;
-  for (uint32_t i = 0; i < a.count; ++i) {
-    a.s[i].u = reinterpret_cast<float *>((uint8_t *)ws + offsets[i]);
-    R = a.s[i].R > R ? a.s[i].R : R;
-  }
+  for (uint32_t i = 0; i < a.count; ++i) a.s[i].u = reinterpret_cast<float *>((uint8_t *)ws + offsets[i]);
   a.plans = ws;
   if (planned(a)) {
     uint32_t bits = 1;
