@@ -4,13 +4,12 @@
 //   the best topk_groups by their largest c or the sum of the two largest s + bias;  in them the
 //   topk largest c, the lower index first among equals;  weight = scale s [/ sum of the taken s].
 //
-// A wave routes a token: lane l holds experts l R .. l R + R - 1, sorted, so that top-k is a
-// maximum over the lanes' heads, a ballot for its place (the lowest lane: the lowest index among
-// equals) and one step of that lane's list, topk times.
-// Which experts are taken must not hang on how a score was rounded.  Logits are compared
-// themselves; scores are formed in fp32 within a known error (below), and a token with two of them
-// too near to tell is done again in fp64.  The weights of the few taken experts are formed in
-// fp64 as well and rounded once.
+// A wave routes a token: lane l holds experts l R .. l R + R - 1.  A candidate is one 32-bit integer:
+// the upper bits of c in an order that integers have, the expert in the lower bits (the lower index as
+// the larger value), so that the lanes sort theirs by minima and maxima and top-k is topk times a maximum over
+// the lanes' first ones and a step in the lane that had it.
+// Which experts are taken must not hang on how a score was rounded or cut off: scores are formed within
+// a known error (below), and a token with two values too near to tell is done again in fp64.
 #include "rows_stream.h"
 #include "wave_ops.h"
 
@@ -29,6 +28,33 @@ constexpr uint32_t kRouteWaves = 4;
 // are in their true order.
 __device__ __forceinline__ float score_margin(bool sigmoid, float top_score) { return sigmoid ? 0x1p-20f : 0x1p-16f * top_score; }
 constexpr float kMarginOf = 0x1p-21f;  // ... and this part of the values' magnitudes
+
+// Integers in the order of floats (no NaN), and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k ^ ((uint32_t)((int)~k >> 31) | 0x80000000u));
+}
+// Maximum over the wave: over rows of 16 lanes by data-parallel moves, which are part of the maximum's own
+// instruction where lanes without a source give 0, over the four rows on the scalar unit.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = dpp_max<0x111>(v);  // row_shr:1
+  v = dpp_max<0x112>(v);
+  v = dpp_max<0x114>(v);
+  v = dpp_max<0x118>(v);
+  const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 15), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 31);
+  const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 47), d = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  uint32_t x = a > b ? a : b, y = c > d ? c : d;
+  x = x > y ? x : y;
+  return uniform32(x);
+}
 
 __device__ __forceinline__ double score64(float l, bool sigmoid, float top, double total) {
   if (!(l > -__builtin_inff())) return 0.0;
@@ -57,6 +83,7 @@ struct RouteLds {
   float logit[64 * R];
   float c[64 * R];  // for groups that are not a power of two lanes
   double wide[64 * R];
+  uint32_t order[64];
 };
 
 // In fp64 throughout.  id: lane j < topk its expert; returns how many are taken.
@@ -153,25 +180,6 @@ __device__ __forceinline__ void load_values(float (&v)[R], const void *from, boo
   }
 }
 
-// Sorts a lane's values, the earlier first among equals; at: where they came from.
-template <int R>
-__device__ __forceinline__ void sort_lane(float (&c)[R], uint32_t (&at)[R]) {
-#pragma unroll
-  for (int i = 0; i < R; ++i) at[i] = i;
-#pragma unroll
-  for (int i = 1; i < R; ++i)  // insertion: compares neighbours only, so equal values keep their order
-#pragma unroll
-    for (int j = i; j > 0; --j) {
-      const bool swap = c[j] > c[j - 1];
-      const float x = c[j], y = c[j - 1];
-      const uint32_t p = at[j], q = at[j - 1];
-      c[j - 1] = swap ? x : y;
-      c[j] = swap ? y : x;
-      at[j - 1] = swap ? p : q;
-      at[j] = swap ? q : p;
-    }
-}
-
 // R: ceil(E / 64) at most.
 template <int R, bool BIASED>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
@@ -194,11 +202,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
     lds.logit[e0 + r] = v[r];
   }
   odd = __ballot(odd) != 0ull;
-  top = wave_max(top);
-  uint32_t id = INT8W_NO_EXPERT, n = 0;
-  double total = 1.0;
-  // fp32 scores, where anything goes by them
   const bool sums = a.groups > 1u && a.top2;
+  if (!a.sigmoid) top = wave_max(top);
+  // fp32 scores, where anything goes by them
   float s[R], top_score = 1.f;
   if (BIASED || sums) {
     if (a.sigmoid) {
@@ -257,62 +263,131 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
     const float of = sums && two > ninf ? one + two : one;
     const float size_of = of > ninf ? fabsf(one) + (sums && two > ninf ? fabsf(two) : 0.f) : 0.f;
     const uint32_t lanes = a.group_lanes ? a.group_lanes : 1u, own = lane / lanes;
-    uint32_t before = 0;  // groups before this lane's
-    for (uint32_t g = 0; g < a.groups; ++g) {
-      const float other = lane_value(of, g * lanes);
-      before += other > of || (other == of && g < own) ? 1u : 0u;
-      if (BIASED || sums)
-        near |= g != own && own < a.groups && other > ninf && fabsf(other - of) <= 2.f * margin + kMarginOf * (size_of + lane_value(size_of, g * lanes));
+    const float apart = 2.f * margin;
+    unsigned long long stay = 0ull;  // groups
+    if (a.groups <= 8u) {            // lane 8 g + h compares groups g and h
+      const uint32_t g = lane >> 3, h = lane & 7u;
+      const float x = __shfl(of, (int)(g * lanes), kWave), y = __shfl(of, (int)(h * lanes), kWave);
+      const bool both = g < a.groups && h < a.groups;
+      const unsigned long long before = __ballot(both && (y > x || (y == x && h < g)));  // byte g: the groups before g
+      if (BIASED || sums) {
+        const float m = __shfl(size_of, (int)(g * lanes), kWave) + __shfl(size_of, (int)(h * lanes), kWave);
+        near |= both && g != h && y > ninf && fabsf(y - x) <= apart + kMarginOf * m;
+      }
+      const bool keep = lane < a.groups && (uint32_t)__popcll(before >> (8u * (lane & 7u)) & 0xFFull) < a.topk_groups;
+      stay = __ballot(keep);
+    } else {
+      uint32_t before = 0;  // groups before this lane's
+      for (uint32_t g = 0; g < a.groups; ++g) {
+        const float other = lane_value(of, g * lanes);
+        before += other > of || (other == of && g < own) ? 1u : 0u;
+        if (BIASED || sums)
+          near |= g != own && own < a.groups && other > ninf && fabsf(other - of) <= apart + kMarginOf * (size_of + lane_value(size_of, g * lanes));
+      }
+      const unsigned long long keep = __ballot(own < a.groups && before < a.topk_groups);  // by lanes
+      for (uint32_t g = 0; g < a.groups; ++g) stay |= (keep >> (g * lanes) & 1ull) << g;
     }
-    const unsigned long long stay = __ballot(own < a.groups && before < a.topk_groups && of > ninf);  // by lanes
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint32_t g = a.group_lanes ? own : (e0 + r) * a.group_magic >> 20;  // e / size
-      if (g >= a.groups || !(stay >> (g * lanes) & 1ull)) c[r] = ninf;
+      if (g >= a.groups || !(stay >> g & 1ull)) c[r] = ninf;
     }
   }
-  uint32_t at[R];
-  sort_lane<R>(c, at);
-  float last = 0.f;
-  const uint32_t rounds = BIASED ? a.topk + 1u : a.topk;  // the first one that is not taken tells whether the last one is surely before it
-  for (uint32_t j = 0; j < rounds; ++j) {
-    const float best = wave_max(c[0]);
-    if (!(best > ninf)) break;
-    if (BIASED && j) near |= last - best <= margin + kMarginOf * (fabsf(last) + fabsf(best));
-    last = best;
-    if (j == a.topk) break;
-    const uint32_t from = (uint32_t)__builtin_ctzll(__ballot(c[0] == best));
-    const uint32_t e = R * from + (uint32_t)__builtin_amdgcn_readlane((int)at[0], (int)from);
-    if (lane == j) id = e;
-    ++n;
+  // The lower bits of a candidate; 0: none.  BF16 logits themselves have nothing in their lower 16 bits: the whole
+  // index fits, and nothing is lost.  Otherwise the index in the lane alone, and two more candidates than are
+  // taken, so that it shows which of them are surely in their order, and before all others.
+  const bool cut = BIASED || !a.logits_bf16;
+  const uint32_t low = cut ? R - 1u : 64u * R - 1u;
+  uint32_t k[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) k[r] = c[r] > ninf ? (ordered(c[r]) & ~low) | (low - (cut ? 0u : e0) - r) : 0u;
+#pragma unroll
+  for (int i = 1; i < R; ++i)
+#pragma unroll
+    for (int j = i; j > 0; --j) {
+      const uint32_t x = k[j], y = k[j - 1];
+      k[j - 1] = x > y ? x : y;
+      k[j] = x > y ? y : x;
+    }
+  const uint32_t rounds = a.topk + (cut ? 2u : 0u);
+  uint32_t mine = 0, id = INT8W_NO_EXPERT, n = 0;  // lane j: choice j
+  for (; n < rounds; ++n) {
+    const uint32_t best = wave_max_u32(k[0]);
+    if (best == 0u) break;
+    const uint32_t from = (uint32_t)__builtin_ctzll(__ballot(k[0] == best));
+    const uint32_t e = low - (best & low) + (cut ? R * from : 0u);
+    mine = lane == n ? best : mine;
+    id = lane == n ? e : id;
     if (lane == from) {
 #pragma unroll
-      for (int r = 0; r + 1 < R; ++r) {
-        c[r] = c[r + 1];
-        at[r] = at[r + 1];
-      }
-      c[R - 1] = ninf;
+      for (int r = 0; r + 1 < R; ++r) k[r] = k[r + 1];
+      k[R - 1] = 0u;
     }
   }
-  near = (BIASED || sums) && __ballot(near) != 0ull && !odd;
-  if (!a.sigmoid && (near || !a.renorm)) {
-    total = 0.0;
+  bool again = __ballot(near) != 0ull && !odd;
+  double total = 1.0;
+  const auto sum64 = [&]() {
+    double x = 0.0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) total += v[r] > ninf ? exp((double)v[r] - (double)top) : 0.0;
-    total = wave_sum(total);
+    for (int r = 0; r < R; ++r) x += v[r] > ninf ? exp((double)v[r] - (double)top) : 0.0;
+    return wave_sum(x);
+  };
+  if (cut && !again) {
+    const uint32_t next = (uint32_t)__shfl_down((int)mine, 1, kWave);
+    const float x = unordered(mine & ~low), y = unordered(next & ~low);
+    // what the index took the place of: less than R units of 2^-23
+    const float reach = BIASED ? margin + (kMarginOf + R * 0x1p-23f) * (fabsf(x) + fabsf(y)) : R * 0x1p-23f * (fabsf(x) + fabsf(y));
+    if (__ballot(lane + 1u < n && lane < a.topk && x - y <= reach) != 0ull && !odd) {
+      // the candidates themselves in fp64; one that is not among them is at most `most_out`
+      wave_fence();
+      if (BIASED && !a.sigmoid) total = sum64();
+      double c64 = -__builtin_inf();
+      if (lane < n) c64 = BIASED ? score64(lds.logit[id], a.sigmoid, top, total) + (double)a.bias[id] : (double)lds.logit[id];
+      uint32_t place = 0;
+      for (uint32_t j = 0; j < n; ++j) {
+        const double other = __shfl(c64, (int)j, kWave);
+        const uint32_t other_id = (uint32_t)__builtin_amdgcn_readlane((int)id, (int)j);
+        place += other > c64 || (other == c64 && other_id < id) ? 1u : 0u;
+      }
+      const float last = lane_value(x, n - 1u);
+      const double most_out = n < rounds ? -__builtin_inf() : (double)last + (double)(margin + (kMarginOf + R * 0x1p-22f) * fabsf(last));
+      again = __ballot(lane < n && place < a.topk && !(c64 > most_out)) != 0ull;
+      lds.order[lane < n ? place : 63u] = id;
+      wave_fence();
+      if (lane < n) id = lds.order[lane];
+    }
   }
-  if (near) n = choose64<R>(a, v, b, BIASED, top, total, lane, lds, id);
+  if (n > a.topk) n = a.topk;
+  if (again) {
+    if (!a.sigmoid) total = sum64();
+    n = choose64<R>(a, v, b, BIASED, top, total, lane, lds, id);
+  }
   if (odd) n = 0;
-  if (lane >= a.topk) return;
+  // weights, in fp32 unless what is to be divided by its sum is all far down
   wave_fence();
-  double w = lane < n ? score64(lds.logit[id], a.sigmoid, top, total) : 0.0;
-  if (a.renorm) {
-    double sum = 0.0;
-    for (uint32_t j = 0; j < n; ++j) sum += __shfl(w, (int)j, kWave);
-    w = sum > 0.0 ? w / sum : 0.0;
+  const float l = lane < n ? lds.logit[id] : ninf, d = a.sigmoid ? l : l - top;
+  float w;
+  if (a.renorm && __ballot(d >= -40.f) == 0ull) {
+    double x = score64(l, a.sigmoid, top, 1.0), sum = 0.0;
+    for (uint32_t j = 0; j < n; ++j) sum += __shfl(x, (int)j, kWave);
+    w = sum > 0.0 ? (float)(x / sum * (double)a.scale) : 0.f;
+  } else {
+    const float e = lane < n ? expf(a.sigmoid ? -d : d) : 0.f;
+    float sum = 1.f;
+    w = a.sigmoid ? (lane < n ? __builtin_amdgcn_rcpf(1.f + e) : 0.f) : e;
+    if (a.renorm) {
+      sum = wave_add(w);
+    } else if (!a.sigmoid) {
+      sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) sum += v[r] > ninf ? expf(v[r] - top) : 0.f;
+      sum = wave_add(sum);
+    }
+    w = sum > 0.f ? w * __builtin_amdgcn_rcpf(sum) * a.scale : 0.f;
   }
+  if (lane >= a.topk) return;
   a.ids[(size_t)t * a.topk + lane] = lane < n ? id : INT8W_NO_EXPERT;
-  a.weights[(size_t)t * a.topk + lane] = odd ? __builtin_nanf("") : (float)(w * (double)a.scale);
+  a.weights[(size_t)t * a.topk + lane] = odd ? __builtin_nanf("") : w;
 }
 
 template <int R>
