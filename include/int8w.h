@@ -358,7 +358,9 @@ int int8w_mxfp4_moe_layer_routed(const int8w_mxfp4 *gate, const int8w_mxfp4 *up,
  * int8_gemm or int8w_mxfp4_gemm, in place.  Up to INT8W_MAX_MULTI pools with the same
  * num_adapters and in_features (q, k and v; gate and up) share x and ids in one call.
  * Rows may come in any order: rows of single tokens with an adapter each, runs of a prompt's
- * rows, both; an adapter's matrices are read once for neighbouring rows that share it. */
+ * rows, both; an adapter's matrices are read once for up to 16 or 64 rows that share it.  The order of a
+ * row's sum depends on m and on how many rows share its adapter: the same call gives the same bits,
+ * the same row in another batch may differ within fp32's rounding of the sums. */
 #define INT8W_NO_ADAPTER 0xFFFFFFFFu
 #define INT8W_MAX_LORA_RANK 256
 typedef struct {
@@ -385,7 +387,8 @@ typedef struct {
 
 /* x: BF16 rows x_stride elements apart (at least in_features, a multiple of 8), 16-byte aligned.
  * ids: uint32 [m], device.  m = 0 is a no-op.  workspace: device scratch, 256-byte aligned, of at least
- * int8w_lora_workspace_bytes(pools, count, m) bytes; no initial value, none kept; calls that share it must not overlap.
+ * int8w_lora_workspace_bytes(pools, count, m) bytes (none and NULL where that is 0); no initial value, none
+ * kept; calls that share it must not overlap.
  * Errors: INT8W_ERR_NULL; INT8W_ERR_SHAPE (count outside 1..INT8W_MAX_MULTI, pools that do not fit
  * each other, sizes outside the limits, m above 2^20, a stride too small or above 2^32, a workspace
  * too small); INT8W_ERR_ALIGN; INT8W_ERR_ALIAS (a y or the workspace overlapping an input or another y; columns

@@ -68,7 +68,8 @@ SIZES = [  # m, K, N, rank, adapters
     (1, 8, 1, 8, 1), (1, 256, 320, 16, 3), (1, 4096, 64, 8, 2), (2, 72, 7, 24, 2), (3, 520, 250, 64, 5), (15, 128, 96, 40, 4),
     (16, 64, 64, 16, 3), (17, 320, 257, 32, 2), (33, 1032, 130, 72, 40), (64, 128, 256, 128, 9), (65, 200, 100, 16, 70),
     (130, 96, 600, 256, 3), (256, 64, 72, 8, 20), (257, 64, 72, 8, 20), (300, 264, 514, 48, 7), (513, 72, 40, 136, 3),
-    (700, 128, 1027, 64, 11),
+    (700, 128, 1027, 64, 11), (3, 16392, 40, 8, 2), (5, 128, 96, 128, 3), (2, 2056, 1500, 64, 3), (1, 24, 513, 56, 2), (63, 16384, 24, 16, 30),
+    (1100, 64, 264, 24, 9), (2500, 72, 136, 8, 300),
 ]
 
 
@@ -204,6 +205,34 @@ def test_a_pool_past_32_bits():
         y = lora_add(pool, x, ids)
         last = LoraAdapters(a[-3:].contiguous(), b[-3:].contiguous())
         check(y, last, x, ids - (num - 3), None, f"m={m}")
+
+
+@pytest.mark.parametrize("m", [70000, (1 << 16) + 1])
+def test_more_rows_than_one_round_of_groups(m):
+    # more than 64 pieces of 1024 rows; the rows about the ends of pieces and of rounds are looked at
+    log(f"many rows m={m}")
+    g = gen(5)
+    pool, x, base = pool_of(g, 7, 8, 72, 40), randn(g, m, 72), randn(g, m, 40)
+    for kind in ("mixed", "runs"):
+        ids = ids_of(kind, m, 7, 3)
+        y = lora_add(pool, x, ids, base)
+        at = torch.tensor(sorted({t for e in range(0, m + 1024, 1024) for t in (e - 2, e - 1, e, e + 1) if 0 <= t < m} | {m - 1}))
+        check(y[at], pool, x[at], ids[at], base[at], kind)
+        e = ids.long().clamp(min=0)  # all rows, to what BF16 tells
+        u = torch.matmul(pool.a.double()[e], x.double().unsqueeze(2))
+        ref = base.double() + torch.where(ids >= 0, pool.scales.double()[e], 0.0).unsqueeze(1) * torch.matmul(pool.b.double()[e], u).squeeze(2)
+        assert ((y.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -12).all()
+
+
+def test_the_same_call_gives_the_same_bits():
+    # where groups lie in the plan depends on the order of atomics; no result may
+    log("repeats")
+    g = gen(8)
+    for m, num in ((700, 90), (300, 3), (2000, 400)):
+        pool, x, ids, base = pool_of(g, num, 24, 520, 136), randn(g, m, 520), ids_of("mixed", m, num, 1), randn(g, m, 136)
+        want = lora_add(pool, x, ids, base)
+        for _ in range(20):
+            assert torch.equal(bits(want), bits(lora_add(pool, x, ids, base)))
 
 
 def test_rows_far_apart():

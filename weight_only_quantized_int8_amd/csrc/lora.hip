@@ -3,12 +3,16 @@
 //   u[t] = A_e x[t],  y[t] = base[t] + scale_e B_e u[t],  e = ids[t];
 //   A_e [R, K], B_e [N, R], R far below K and N; id INT8W_NO_ADAPTER: y[t] = base[t].
 //
-// On the matrix cores (16x16x32 products), in two launches:
+// Bound: memory.  A product of rank R has 2 R operations for the 4 or 6 bytes of each x, base
+// and y, and where rows have an adapter each, one for each byte of it; the matrix cores are there to keep
+// the vector ALUs free.  Two launches:
 //  shrink  u in fp32, K cut into `parts` (the sum over K is the long one, and a single token's
 //          A has to come through many CUs): u [parts, m, R] in the workspace.
 //  expand  sums the parts in their order, scales, multiplies by B_e, adds base, rounds once.
 //          u enters the matrix cores as the sum of two BF16 values (u's own rounding to one
 //          would be as large as the output's); the products are exact and summed in fp32.
+// One launch (k_solo) for a few rows of small matrices: there the second launch costs more than
+// reading A again for each 512 columns.
 // No atomics in any sum: the same bits each time.
 //
 // A workgroup works on a group: rows with one adapter, wherever they are in the batch, so that its
@@ -16,10 +20,19 @@
 // ("few"), or up to 64 with the rows shared out ("many").
 //  Up to 64 rows in the batch: a workgroup stands for a row; of the rows that share an adapter each
 //   16th leads and takes the next 15 along, found by one ballot; the others end at once.
-//  More: a launch before the others (k_plan) sorts the rows of each 1024 into groups, which
-//   a fixed number of workgroups takes in turn.
+//  More: a launch before the others (k_plan, 3 to 5 us) sorts the rows of each 1024 into groups, which
+//   a fixed number of workgroups shares: with a workgroup for each group that there might be, those
+//   without one took longer than the work (200 rows: shrink 32 instead of 23 us).
 // A row is a row or column of the products, which do not mix: what another row or its adapter
 // holds (infinities, NaN) does not reach it.
+//
+// Measured, plan + shrink + expand, us (bytes that shrink and expand fetch and write):
+//  8192 rows in 5 runs, 14336x4096, rank 64:   5 + 24 + 110  (70 and 302 MB in, 235 out: 4.9 TB/s in expand)
+//  2109 rows, 24 adapters, 4096x14336, 8..64:  5 + 22 + 18   (82 MB in, 3.7 TB/s in shrink)
+//  549 rows, 16 adapters, gate and up, 16:     3 + 8 + 17    (15 MB in, 31 out: starts and ends of workgroups)
+//  200 rows, 57 adapters, 4096x14336, rank 64: 5 + 23 + 15   (111 and 35 MB in: 4.8 TB/s in shrink)
+//  33 rows, 25 adapters, q, k and v, 32:       - + 6.7 + 5.5 (9 and 8 MB in)
+//  one row, 4096x4096, rank 16, one launch:    4.9 (3.9 in a graph)
 #include "rows_stream.h"
 #include "token_stream.h"
 
@@ -34,6 +47,7 @@ constexpr uint32_t kStepK = 64;       // K of a step: a cache line of a row
 constexpr uint32_t kBlockN = 128;     // output columns of a step
 constexpr uint32_t kShrinkBlocks = 512;  // workgroups over a plan's groups: what fits the CUs
 constexpr uint32_t kExpandBlocks = 1024;
+constexpr uint32_t kManyGroups = 40;     // from so many on an XCD of expand has groups of its own
 
 #define INT8W_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) >> 4) << 14) | 0x0F70 | ((n) & 15))
 #define INT8W_LGKMCNT0() __builtin_amdgcn_s_waitcnt(0xC07F)
@@ -819,9 +833,9 @@ __global__ __launch_bounds__(256, NCH == 1 ? 4 : 2) void k_expand_items(const Lo
   runs = runs < 1u ? 1u : runs > column_blocks ? column_blocks : runs;
   const uint32_t run = (column_blocks + runs - 1u) / runs;
   runs = (column_blocks + run - 1u) / run;
-  each_share(groups.total * runs, [&](uint32_t i) {
-    groups.with(i % groups.total, list, [&](uint32_t e, uint32_t n) {
-      uint32_t at = i / groups.total * run, left = run;
+  const auto work = [&](uint32_t group, uint32_t at_run) {
+    groups.with(group, list, [&](uint32_t e, uint32_t n) {
+      uint32_t at = at_run * run, left = run;
       for (uint32_t k = 0; k < g.count && left; ++k) {
         const LoraStack s = g.s[k];
         const uint32_t blocks = (s.N + kBlockN - 1u) / kBlockN;
@@ -839,7 +853,19 @@ __global__ __launch_bounds__(256, NCH == 1 ? 4 : 2) void k_expand_items(const Lo
         left -= here;
       }
     });
-  });
+  };
+  // Many groups: a group to an XCD, whose u then comes into one L2, and whose neighbours share their B.  Few would lie
+  // unevenly: there an XCD has some columns of all groups.  us so / the other way: 57 groups, 4096 columns, rank 64
+  // 17.6 / 20.0; 128 groups of one adapter of rank 128 43 / 52; 27 groups, 28672 columns, rank 16 18.2 / 17.3.
+  if (groups.total >= kManyGroups) {
+    for (uint32_t j = blockIdx.x / 8u;; j += gridDim.x / 8u) {
+      const uint32_t group = j / runs * 8u + blockIdx.x % 8u;
+      if (group >= groups.total) break;
+      work(group, j % runs);
+    }
+  } else {
+    each_share(groups.total * runs, [&](uint32_t i) { work(i % groups.total, i / groups.total); });
+  }
 }
 
 // ---- one launch for a few rows ---------------------------------------------------------------
