@@ -836,11 +836,11 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: t
     if not (1 <= topk <= MAX_MOE_TOPK and 1 <= groups <= MAX_MOE_GROUPS and 1 <= topk_groups <= groups):  # before they size the outputs
         raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk}, groups {groups} or topk_groups {topk_groups} out of range")
     if ids is None:
-        ids = logits.new_empty((T, topk), dtype=torch.int32)
+        ids = logits.new_empty_strided((T, topk), (topk, 1), dtype=torch.int32)  # 0.2 us less than new_empty
     else:
         _need_slots(ids, "ids", (torch.int32, torch.uint32), T, topk, dev)
     if weights is None:
-        weights = logits.new_empty((T, topk), dtype=torch.float32)
+        weights = logits.new_empty_strided((T, topk), (topk, 1), dtype=torch.float32)
     else:
         _need_slots(weights, "weights", (torch.float32,), T, topk, dev)
     _call(dev, load_library().packed_route,
@@ -1040,7 +1040,7 @@ def lora_add(adapters, x: torch.Tensor, ids: torch.Tensor, base=None, y=None):
             raise ValueError("lora_add: pools on different devices")
         n, b, o = pool.out_features, bases[i], ys[i]
         if o is None:
-            o = ys[i] = x.new_empty((m, n))
+            o = ys[i] = x.new_empty_strided((m, n), (n, 1))
             os = n
         else:
             os = _rows(o, "y", m, n, dev)

@@ -442,13 +442,14 @@ __device__ __forceinline__ uint32_t b_swizzle(uint32_t c, uint32_t p) {  // as q
   return row_swizzle<8>(c, p);
 }
 
-// Load j of the 2 P of a block's rank chunk r0.  n0: its first column.
+// Load j of the 2 P of a block's rank chunk r0.  n0: its first column.  Columns of B beyond the adapter's own rank,
+// zeros, are read: they lie in the same cache lines up to rank 64, and the first loads do not wait for the rank.
 template <int P>
-__device__ __forceinline__ void dma_b(__amdgpu_buffer_rsrc_t rb, uint32_t R, uint32_t rank, uint32_t n0, uint32_t r0, uint32_t j,
-                                      uint8_t *to, uint32_t lane) {
+__device__ __forceinline__ void dma_b(__amdgpu_buffer_rsrc_t rb, uint32_t R, uint32_t n0, uint32_t r0, uint32_t j, uint8_t *to,
+                                      uint32_t lane) {
   const uint32_t row = (64u * j + lane) / P, c = row & 15u, t = row >> 4;
   const uint32_t r = r0 + 8u * b_swizzle<P>(c, lane % P), n = n0 + 8u * c + t;  // a column past the last one: zeros by the resource
-  dma(rb, r < rank ? (n * R + r) * 2u : kOutOfRange, to + 1024u * j);
+  dma(rb, r < R ? (n * R + r) * 2u : kOutOfRange, to + 1024u * j);
 }
 
 // u of 16 rows as operands: lane (c, q) of row c.  P = 2: one operand, the upper BF16 values in
@@ -630,11 +631,11 @@ struct ExpandFew {
   static constexpr uint32_t kColumns = 4u * kBlockN;
   static __device__ __forceinline__ void run(const LoraArgs &g, const LoraStack &s, uint32_t e, const uint32_t *list, uint32_t n,
                                              uint32_t n0, uint8_t *lds, uint32_t lane, uint32_t wave) {
-    const uint32_t c = lane & 15u, q = lane >> 4, rank = own_rank(s, e), w0 = n0 + kBlockN * wave;
+    const uint32_t c = lane & 15u, q = lane >> 4, w0 = n0 + kBlockN * wave;
     uint8_t *const b = lds + kBlock * wave, *const hi = lds + 4u * kBlock, *const lo = hi + kFew * kRow;
     const auto rb = make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u);
 #pragma unroll
-    for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, rank, w0, 0u, j, b, lane);
+    for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, w0, 0u, j, b, lane);
     const OutRows out(s, list, 4u * q, n);
     u32x4 o[4];
     out.load(o, w0 + 8u * c);
@@ -662,7 +663,7 @@ struct ExpandFew {
     f32x4 acc[8] = {};
 #pragma unroll
     for (int ch = 0; ch < NCH; ++ch) {
-      if (64u * ch >= rank && ch > 0) break;
+      if (64u * ch >= s.R) break;
       INT8W_VMCNT(0);
       keep_order();
       multiply_block<P, NCH>(acc, u, ch, b, lane);
@@ -670,7 +671,7 @@ struct ExpandFew {
         INT8W_LGKMCNT0();
         keep_order();
 #pragma unroll
-        for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, rank, w0, 64u * (ch + 1), j, b, lane);
+        for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, w0, 64u * (ch + 1), j, b, lane);
       }
     }
     out.add(o, acc, w0 + 8u * c);
@@ -688,7 +689,7 @@ struct ExpandMany {
     // Without this the lane's many places in LDS are all kept in registers over the loop around the
     // call, 40 to 60 of which then spill.
     asm volatile("" : "+v"(lane));
-    const uint32_t c = lane & 15u, q = lane >> 4, rank = own_rank(s, e);
+    const uint32_t c = lane & 15u, q = lane >> 4;
     const auto rb = make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u);
     const float scale = s.scales ? s.scales[e] : 1.f;
     const bool idle = 16u * wave >= n;  // a wave without a row loads its share of B
@@ -699,7 +700,7 @@ struct ExpandMany {
     auto column = [&](uint32_t i) { return n0 + kBlockN * (i + turn < blocks ? i + turn : i + turn - blocks); };
     auto load_b = [&](uint32_t block, int ch, uint8_t *to) {
 #pragma unroll
-      for (uint32_t i = 0; i < P / 2u; ++i) dma_b<P>(rb, s.R, rank, column(block), 64u * ch, wave * (P / 2u) + i, to, lane);
+      for (uint32_t i = 0; i < P / 2u; ++i) dma_b<P>(rb, s.R, column(block), 64u * ch, wave * (P / 2u) + i, to, lane);
     };
     load_b(0, 0, lds);
     keep_order();
