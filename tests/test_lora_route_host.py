@@ -58,14 +58,14 @@ NULL, SHAPE, UNSUPPORTED, ALIGN, ALIAS = (B.INT8W_ERR_NULL, B.INT8W_ERR_SHAPE, B
     (dict(m=(1 << 20) + 1), SHAPE, "more than 2^20"),
     (dict(x=0), NULL, "x, ids"),
     (dict(ids=0), NULL, "x, ids"),
-    (dict(ws=0), NULL, "workspace"),
+    (dict(pools=[pool(rank=72)], ws=0), NULL, "workspace"),
     (dict(xs=56), SHAPE, "x_stride"),
     (dict(xs=68), SHAPE, "x_stride"),
     (dict(xs=(1 << 32) + 8), SHAPE, "x_stride"),
     (dict(x=6 * A + 8), ALIGN, "x is not"),
     (dict(ids=7 * A + 2), ALIGN, "ids"),
     (dict(ws=8 * A + 128), ALIGN, "workspace"),
-    (dict(nbytes=64), SHAPE, "workspace of 64"),
+    (dict(pools=[pool(rank=72)], nbytes=64), SHAPE, "workspace of 64"),
     (dict(outs=[out(y=0)]), NULL, "y is NULL"),
     (dict(outs=[out(y=5 * A + 1)]), ALIGN, "y/base"),
     (dict(outs=[out(base=4 * A + 1)]), ALIGN, "y/base"),
@@ -77,9 +77,9 @@ NULL, SHAPE, UNSUPPORTED, ALIGN, ALIAS = (B.INT8W_ERR_NULL, B.INT8W_ERR_SHAPE, B
     (dict(outs=[out(y=3 * A)]), ALIAS, "input scales"),
     (dict(outs=[out(y=4 * A + 2)]), ALIAS, "input base"),
     (dict(outs=[out(base=4 * A, y=4 * A, bs=96, ys=104)]), ALIAS, "input base"),
-    (dict(outs=[out(y=8 * A + 16)]), ALIAS, "workspace"),
-    (dict(outs=[out(base=8 * A + 16)]), ALIAS, "workspace"),
-    (dict(ws=6 * A), ALIAS, "input x"),
+    (dict(pools=[pool(rank=72)], outs=[out(y=8 * A + 16)]), ALIAS, "workspace"),
+    (dict(pools=[pool(rank=72)], outs=[out(base=8 * A + 16)]), ALIAS, "workspace"),
+    (dict(pools=[pool(rank=72)], ws=6 * A), ALIAS, "input x"),
     (dict(pools=[pool(), pool()], outs=[out(ys=200), out(y=5 * A + 2 * 95, ys=200)]), ALIAS, "two outputs"),
     (dict(pools=[pool(), pool()], outs=[out(ys=200), out(y=5 * A + 2 * 105, ys=200)]), ALIAS, "two outputs"),
     (dict(pools=[pool(), pool()], outs=[out(ys=200), out(y=5 * A + 2 * 96, ys=208)]), ALIAS, "two outputs"),
@@ -94,8 +94,19 @@ def test_workspace_of_bad_pools_is_zero_and_of_no_rows():
     assert B.int8w_lora_workspace_bytes(pool(rank=12), 1, 8) == 0
     assert B.int8w_lora_workspace_bytes(pool(), 1, 0) == 0
     for m in (1, 16, 200, 256, 257, 4096, 1 << 20):
-        one, two = B.int8w_lora_workspace_bytes(pool(), 1, m), B.int8w_lora_workspace_bytes((B.LoraDesc * 2)(pool(), pool()), 2, m)
-        assert one >= m * 16 * 4 and one % 256 == 0 and two >= 2 * m * 16 * 4
+        p = pool(rank=72)
+        one, two = B.int8w_lora_workspace_bytes(p, 1, m), B.int8w_lora_workspace_bytes((B.LoraDesc * 2)(p, p), 2, m)
+        assert one >= m * 72 * 4 and one % 256 == 0 and two >= 2 * m * 72 * 4
+
+
+def test_few_rows_of_small_matrices_need_no_workspace():
+    assert [B.int8w_lora_workspace_bytes(pool(), 1, m) for m in (1, 8, 16)] == [0, 0, 0]
+    # refused for its output, so past the workspace, which is neither needed nor looked at
+    for kw in (dict(ws=0, nbytes=0), dict(ws=6 * A), dict(nbytes=64)):
+        rc, msg = err(add(outs=[out(y=0)], **kw))
+        assert rc == NULL and "y is NULL" in msg, (kw, msg)
+    rc, msg = err(add(ws=8 * A + 128))  # its alignment is looked at all the same
+    assert rc == ALIGN and "workspace" in msg
 
 
 def test_no_rows_are_nothing_to_do():

@@ -869,7 +869,7 @@ int int8w_lora_add(const int8w_lora *pools, const int8w_lora_out *out, uint32_t 
   int rc = validate_lora_pools(pools, count, m);
   if (rc) return rc;
   if (m == 0) return ok();
-  if (!out || !x || !ids) return fail(INT8W_ERR_NULL, "out, x or ids is NULL");
+  if (!out || !x || !ids) return fail(INT8W_ERR_NULL, "one of out, x, ids is NULL");
   LoraArgs a = lora_args(pools, count, m);
   constexpr uint64_t kMaxStride = 1ull << 32;
   if (x_stride < a.K || x_stride % 8u != 0 || x_stride > kMaxStride)
