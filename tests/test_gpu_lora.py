@@ -224,6 +224,15 @@ def test_more_rows_than_one_round_of_groups(m):
         assert ((y.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -12).all()
 
 
+@pytest.mark.parametrize("m", [64, 65, 70001])
+def test_many_rows_of_tiny_matrices(m):
+    log(f"tiny matrices m={m}")
+    g = gen(m + 3)
+    pool, x, base = pool_of(g, 3, 8, 8, 40), randn(g, m, 8), randn(g, m, 40)
+    ids = ids_of("mixed", m, 3, 7)
+    check(lora_add(pool, x, ids, base), pool, x, ids, base, m)
+
+
 def test_the_same_call_gives_the_same_bits():
     # where groups lie in the plan depends on the order of atomics; no result may
     log("repeats")

@@ -109,6 +109,11 @@ def test_few_rows_of_small_matrices_need_no_workspace():
     assert rc == ALIGN and "workspace" in msg
 
 
+@pytest.mark.parametrize("m", [65, 4096, 70001, 1 << 20])
+def test_many_rows_of_tiny_matrices_are_planned(m):
+    assert B.int8w_lora_workspace_bytes(pool(k=8, rank=8, n=40), 1, m) >= m * 8 * 4  # a row a workgroup would pass the grid
+
+
 def test_no_rows_are_nothing_to_do():
     assert add(m=0, x=0, ids=0, ws=0) == B.INT8W_OK
     assert B.int8w_moe_route(route(tokens=0, logits=0), 0) == B.INT8W_OK

@@ -985,6 +985,7 @@ uint32_t max_rank(const LoraArgs &a) {
 // gate and up of 14336x4096, rank 16: 4 rows (29 MB) 5.1 / 6.8, 8 (57 MB) 8.7 / 7.6;
 // 4096x14336, rank 16 (448 KiB): 1 row (3.7 MB) 7.1 / 8.0, 4 (15 MB) 9.4 / 8.5; rank 64 (1.8 MB): 1 row 24.8 / 9.7.
 bool solo(const LoraArgs &a) {
+  if (planned(a)) return false;  // rows enough to share an adapter's weights, and more than a grid's second axis may hold
   uint64_t all = 0;
   for (uint32_t i = 0; i < a.count; ++i) all += (uint64_t)((a.s[i].N + kSoloColumns - 1u) / kSoloColumns) * a.s[i].R;
   all *= 2u * (uint64_t)a.K * a.m;
