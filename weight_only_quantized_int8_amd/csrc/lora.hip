@@ -27,12 +27,12 @@
 // holds (infinities, NaN) does not reach it.
 //
 // Measured, plan + shrink + expand, us (bytes that shrink and expand fetch and write):
-//  8192 rows in 5 runs, 14336x4096, rank 64:   5 + 24 + 110  (70 and 302 MB in, 235 out: 4.9 TB/s in expand)
-//  2109 rows, 24 adapters, 4096x14336, 8..64:  5 + 22 + 18   (82 MB in, 3.7 TB/s in shrink)
-//  549 rows, 16 adapters, gate and up, 16:     3 + 8 + 17    (15 MB in, 31 out: starts and ends of workgroups)
-//  200 rows, 57 adapters, 4096x14336, rank 64: 5 + 23 + 15   (111 and 35 MB in: 4.8 TB/s in shrink)
-//  33 rows, 25 adapters, q, k and v, 32:       - + 6.7 + 5.5 (9 and 8 MB in)
-//  one row, 4096x4096, rank 16, one launch:    4.9 (3.9 in a graph)
+//  8192 rows in 5 runs, 14336x4096, rank 64:   5 + 24 + 113  (71 and 437 MB in, 235 out: 6.0 TB/s in expand)
+//  2109 rows, 24 adapters, 4096x14336, 8..64:  4 + 22 + 18   (84 and 44 MB in, 5 and 17 out: 4.0 TB/s in shrink)
+//  549 rows, 16 adapters, gate and up, 16:     4 + 8 + 18    (8 and 15 MB in, 31 out: starts and ends of workgroups)
+//  200 rows, 57 adapters, 4096x14336, rank 64: 4 + 24 + 15   (114 and 33 MB in: 4.8 TB/s in shrink)
+//  33 rows, 25 adapters, q, k and v, 32:       - + 6.6 + 6.0 (9 and 8 MB in)
+//  one row, 4096x4096, rank 16, one launch:    4.7 (3.9 in a graph)
 #include "rows_stream.h"
 #include "token_stream.h"
 
@@ -858,6 +858,7 @@ __global__ __launch_bounds__(256, NCH == 1 ? 4 : 2) void k_expand_items(const Lo
   // Many groups: a group to an XCD, whose u then comes into one L2, and whose neighbours share their B.  Few would lie
   // unevenly: there an XCD has some columns of all groups.  us so / the other way: 57 groups, 4096 columns, rank 64
   // 17.6 / 20.0; 128 groups of one adapter of rank 128 43 / 52; 27 groups, 28672 columns, rank 16 18.2 / 17.3.
+  // All groups of an XCD at one run of columns before the next: 8192 rows 110 instead of 113, 2109 18.6 for 17.9.
   if (groups.total >= kManyGroups) {
     for (uint32_t j = blockIdx.x / 8u;; j += gridDim.x / 8u) {
       const uint32_t group = j / runs * 8u + blockIdx.x % 8u;

@@ -5,6 +5,9 @@
 //   r_j = p_j / sum of the chosen p (renormalized) or p_j, times routed_scale;
 //   y[t] = x_resid[t] + sum_j r_j  Wd_j ( silu(Wg_j x_t) * (Wu_j x_t) ).
 //
+// The choice and its weights may be given instead of logits: then k_moe_route, or for one token
+// k_moe1_up, only takes them over.
+//
 // One token: two launches (k_moe1_up, k_moe1_down, token_stream.h).  More: four launches on
 // one stream, up to 64 tokens a pass:
 //  k_moe_route   one workgroup: each wave takes tokens.  Its result is a list of

@@ -10,6 +10,11 @@
 // the lanes' first ones and a step in the lane that had it.
 // Which experts are taken must not hang on how a score was rounded or cut off: scores are formed within
 // a known error (below), and a token with two values too near to tell is done again in fp64.
+//
+// Bound: a launch up to some thousand tokens, then the vector ALUs' issue.  us, under a tracer: 1 token of 64
+// experts 3.1, 131 of 60 3.6, 64 of 256 in 8 groups 5.6, 16384 of those 22 (17.8 MB, which a copy moves in 3.6; about
+// 590 vector instructions a token, most of them in the groups' and the choices' maxima over the lanes).
+// All in fp64 16384 tokens took 35.
 #include "rows_stream.h"
 #include "wave_ops.h"
 
