@@ -130,6 +130,23 @@ def test_own_ranks(m):
     assert torch.equal(bits(y), bits(lora_add(full, x, ids, base)))
 
 
+@pytest.mark.parametrize("m", [1, 20, 64, 400])
+def test_own_ranks_of_nothing_and_beyond_the_pool(m):
+    # rank 0: base itself in value; above the pool's: the pool's
+    log(f"rank 0 and large ranks m={m}")
+    for rank, K in ((16, 64), (72, 520)):
+        g = gen(m + rank)
+        pool, x, base = pool_of(g, 4, rank, K, 300), randn(g, m, K), randn(g, m, 300)
+        pool.a[1], pool.b[1] = 0, 0
+        own = LoraAdapters(pool.a, pool.b, pool.scales, torch.tensor([rank, 0, rank + 9, -1], dtype=torch.int32, device="cuda"))
+        for kind in ("mixed", "runs"):
+            ids = ids_of(kind, m, 4, m)
+            ids[0] = 1
+            y = lora_add(own, x, ids, base)
+            check(y, pool, x, ids, base, kind)
+            assert torch.equal(y[0], base[0]) and torch.equal(bits(y), bits(lora_add(pool, x, ids, base)))
+
+
 @pytest.mark.parametrize("m", [20, 70, 400])
 def test_what_one_row_holds_stays_in_it(m):
     log(f"infinities and NaN m={m}")

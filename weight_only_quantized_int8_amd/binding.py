@@ -918,7 +918,7 @@ class LoraAdapters:
     b:      bfloat16 [num_adapters, out_features, rank]
     scales: float32 [num_adapters], the factor of b (a x); None: 1
     ranks:  int32/uint32 [num_adapters], where adapters of smaller ranks share the pool: beyond an adapter's
-            own rank its rows of a and columns of b hold zeros, which are then not read
+            own rank its rows of a and columns of b must hold zeros, which are not always read
     """
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor | None = None,
