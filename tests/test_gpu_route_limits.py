@@ -1,0 +1,47 @@
+"""The routing to experts where values are equal, too near to tell, infinite or at the end of fp32's range, against its 64-bit
+definition (tests/adapter_reference.py), with one to eight experts a lane.  Every test prints its case first."""
+import numpy as np
+import pytest
+import torch
+
+import adapter_reference as A
+from test_gpu_moe_route import same
+from weight_only_quantized_int8_amd import moe_route
+
+pytestmark = pytest.mark.gpu
+
+LOW = float(np.finfo(np.float32).min)
+
+
+def log(msg):
+    print(msg, flush=True)
+
+
+def run(l, topk, bf16=False, scoring="softmax", bias=None, groups=1, topk_groups=None, group_score="top2", renorm=True, what=None):
+    ld = torch.from_numpy(l).cuda()
+    if bf16:
+        ld = ld.bfloat16()
+        assert np.array_equal(ld.float().cpu().numpy(), l)
+    got = moe_route(ld, topk, scoring, None if bias is None else torch.from_numpy(bias).cuda(), groups, topk_groups, group_score, renorm)
+    same(got, A.route(l.astype(np.float64), topk, scoring, bias, groups, topk_groups, group_score, renorm), what)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E", [12, 60, 128, 256, 500, 512])
+def test_zeros_of_both_signs_are_equal(E, bf16):
+    log(f"signed zeros E={E} bf16={bf16}")
+    rng = np.random.default_rng(E)
+    step = 2.0 ** -133 if bf16 else 2.0 ** -149  # the smallest value
+    rows = [np.full(E, -1.0) for _ in range(4)]
+    for row, (a, b) in zip(rows, ((0, 1), (1, 2), (3, E - 1), (E // 2 - 1, E // 2))):
+        row[a], row[b] = -0.0, 0.0
+    rows += [np.resize([-0.0, 0.0], E), np.resize([0.0, -0.0], E), np.full(E, -0.0)]
+    rows += [np.where(rng.random(E) < 0.5, -0.0, 0.0) for _ in range(4)]
+    rows += [np.where(rng.random(E) < 0.2, np.where(rng.random(E) < 0.5, -0.0, 0.0), -2.0) for _ in range(4)]
+    rows += [step * rng.integers(-9, 10, E) * rng.choice([-1.0, 1.0], E) for _ in range(4)]  # about zero, many of them equal
+    l = np.array(rows, np.float32)
+    assert np.signbit(l[0, 0]) and l[0, 0] == 0 and (l[-1] != 0).any()
+    for topk in (1, 5):
+        for scoring in ("softmax", "sigmoid"):
+            for groups, topk_groups, group_score in ((1, 1, "max"), (4, 2, "max"), (4, 2, "top2")):
+                run(l, topk, bf16, scoring, None, groups, topk_groups, group_score, what=(topk, scoring, groups, group_score))

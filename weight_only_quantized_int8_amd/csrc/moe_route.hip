@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
   }
   float c[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) c[r] = BIASED ? s[r] : v[r];
+  for (int r = 0; r < R; ++r) c[r] = BIASED ? s[r] : v[r] + 0.f;  // -0 is 0: equal as floats, and not as the integers below
   const float margin = score_margin(a.sigmoid, top_score);
   bool near = false;  // two values that cannot be told apart
   if (a.groups > 1u) {
