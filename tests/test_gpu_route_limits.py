@@ -45,3 +45,48 @@ def test_zeros_of_both_signs_are_equal(E, bf16):
         for scoring in ("softmax", "sigmoid"):
             for groups, topk_groups, group_score in ((1, 1, "max"), (4, 2, "max"), (4, 2, "top2")):
                 run(l, topk, bf16, scoring, None, groups, topk_groups, group_score, what=(topk, scoring, groups, group_score))
+
+
+@pytest.mark.parametrize("E", [12, 128, 256, 512])
+def test_infinities_are_equal(E):
+    # more and fewer of them than are taken, at all places in their lanes
+    log(f"infinities E={E}")
+    inf, rng = np.inf, np.random.default_rng(E)
+    rows = []
+    for at in ((1, 2), (2, 5), (3, 4, E - 1), tuple(range(1, 9)), tuple(range(E - 9, E, 2)), tuple(range(E))):
+        rows.append(rng.standard_normal(E))
+        rows[-1][list(at)] = inf
+    rows += [np.where(rng.random(E) < p, inf, rng.standard_normal(E)) for p in (0.02, 0.1, 0.5)]
+    rows += [np.where(rng.random(E) < 0.1, inf, -inf), np.where(rng.random(E) < 0.3, inf, 1.0), rng.standard_normal(E)]
+    l = np.array(rows, np.float32)
+    biases = [None, 0.1 * rng.standard_normal(E), np.zeros(E), np.zeros(E), np.where(rng.random(E) < 0.2, inf, 0.0), np.full(E, inf)]
+    biases[2][[3, 4]] = inf
+    biases[3][[5, E - 2, 7]] = inf
+    for bias in biases:
+        for topk in (1, 5):
+            for groups, topk_groups in ((1, 1), (4, 2)):
+                for group_score in ("max", "top2"):
+                    for bf16 in (False, True):
+                        for scoring in ("softmax", "sigmoid"):
+                            v = np.where(l == inf, 3.0, l).astype(np.float32) if scoring == "softmax" else l
+                            if bf16:
+                                v = torch.from_numpy(v).bfloat16().float().numpy()
+                            run(v, topk, bf16, scoring, None if bias is None else bias.astype(np.float32), groups, topk_groups, group_score,
+                                what=(bias, topk, groups, group_score, bf16, scoring))
+
+
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (512, 16), (500, 20)])
+def test_near_values_with_several_experts_a_lane(E, groups):
+    # a unit of fp32 and less apart: cut off in a candidate, lost in a biased score
+    log(f"near values E={E}")
+    rng = np.random.default_rng(E)
+    T = 150
+    l = (0.5 + 2.0 ** -24 * rng.integers(0, 40, (T, E))).astype(np.float32)
+    few = np.where(rng.random((T, E)) < 0.03, l, -4.0).astype(np.float32)
+    bias = (16.0 + 2.0 ** -19 * rng.integers(0, 2, E)).astype(np.float32)
+    for v in (l, -l, few):
+        for scoring in ("softmax", "sigmoid"):
+            run(v, 8, False, scoring, None, what=("alone", scoring))
+            run(v, 8, False, scoring, None, groups, groups // 2, "max", what=("groups", scoring))
+            run(v, 8, False, scoring, bias, groups, groups // 2, "max", what=("biased", scoring))
+            run(v, 1, False, scoring, bias, what=("one", scoring))

@@ -342,7 +342,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
     const float x = unordered(mine & ~low), y = unordered(next & ~low);
     // what the index took the place of: less than R units of 2^-23
     const float reach = BIASED ? margin + (kMarginOf + R * 0x1p-23f) * (fabsf(x) + fabsf(y)) : R * 0x1p-23f * (fabsf(x) + fabsf(y));
-    if (__ballot(lane + 1u < n && lane < a.topk && x - y <= reach) != 0ull && !odd) {
+    // two infinities differ by a NaN: not surely in their order either
+    if (__ballot(lane + 1u < n && lane < a.topk && !(x - y > reach)) != 0ull && !odd) {
       // the candidates themselves in fp64; one that is not among them is at most `most_out`
       wave_fence();
       if (BIASED && !a.sigmoid) total = sum64();
