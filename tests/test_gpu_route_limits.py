@@ -90,3 +90,27 @@ def test_near_values_with_several_experts_a_lane(E, groups):
             run(v, 8, False, scoring, None, groups, groups // 2, "max", what=("groups", scoring))
             run(v, 8, False, scoring, bias, groups, groups // 2, "max", what=("biased", scoring))
             run(v, 1, False, scoring, bias, what=("one", scoring))
+
+
+@pytest.mark.parametrize("E", [16, 60, 64, 128, 256])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_group_sums_past_the_range_of_fp32(E, scoring):
+    # the sum of two biases is no infinity where it is compared
+    log(f"large group sums E={E} {scoring}")
+    inf, rng = np.inf, np.random.default_rng(E)
+    l = rng.standard_normal((6, E)).astype(np.float32)
+    l[5, E // 2:] = -inf
+    for groups in (4, 2) if E != 60 else (6, 12):
+        size = E // groups
+        for pairs in (((3e38, 1e38), (3e38, 3e38), (2.5e38, 2.5e38), (0, 0)), ((LOW, LOW), (-2e38, -2e38), (-3e38, -1e38), (LOW, -3e38)),
+                      ((-inf, -inf), (LOW, LOW), (-inf, -inf), (-inf, LOW)), ((inf, 1), (3e38, 3e38), (inf, inf), (3.4e38, 3.4e38)),
+                      ((-inf, -inf), (LOW, LOW), (1, LOW), (-inf, 3e38))):
+            bias = np.empty(E, np.float32)
+            for g in range(groups):
+                two = pairs[g % 4]
+                low = min(two) if min(two) < 0 else -1.0
+                bias[g * size:(g + 1) * size] = low
+                bias[g * size + g % 2], bias[(g + 1) * size - 1] = two
+            for topk_groups in (1, groups // 2, groups):
+                for topk in (1, min(3, size)):
+                    run(l, topk, False, scoring, bias, groups, topk_groups, "top2", what=(groups, pairs, topk_groups, topk))

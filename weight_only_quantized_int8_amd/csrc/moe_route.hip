@@ -266,6 +266,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
         }
     }
     const float of = sums && two > ninf ? one + two : one;
+    near |= sums && two > ninf && one < __builtin_inff() && fabsf(of) == __builtin_inff();  // a sum past fp32's range, not fp64's
     const float size_of = of > ninf ? fabsf(one) + (sums && two > ninf ? fabsf(two) : 0.f) : 0.f;
     const uint32_t lanes = a.group_lanes ? a.group_lanes : 1u, own = lane / lanes;
     const float apart = 2.f * margin;
