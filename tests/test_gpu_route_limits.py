@@ -114,3 +114,17 @@ def test_group_sums_past_the_range_of_fp32(E, scoring):
             for topk_groups in (1, groups // 2, groups):
                 for topk in (1, min(3, size)):
                     run(l, topk, False, scoring, bias, groups, topk_groups, "top2", what=(groups, pairs, topk_groups, topk))
+
+
+def test_more_tokens_than_one_launch_has_threads_for():
+    # 64 threads a token; a launch has fewer than 2^32
+    T = (1 << 26) + 5
+    log(f"many tokens T={T}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    l = torch.randint(-9, 9, (T, 2), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    ids = torch.full((T + 1, 1), 7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, 1), 7.0, device="cuda")
+    moe_route(l, 1, ids=ids[:T], weights=w[:T])
+    assert torch.equal(ids[:T, 0], (l[:, 1] > l[:, 0]).int()) and (w[:T] == 1).all()
+    assert int(ids[T]) == 7 and float(w[T]) == 7

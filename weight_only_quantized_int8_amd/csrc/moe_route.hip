@@ -405,11 +405,18 @@ void launch_route_r(RouteArgs a, hipStream_t stream) {
   a.whole_bias = a.E % R == 0u && reinterpret_cast<uintptr_t>(a.bias) % (R * 4u) == 0u;
   const uint32_t lanes = a.group_size % R == 0u ? a.group_size / R : 0u;
   a.group_lanes = lanes <= 32u && (lanes & (lanes - 1u)) == 0u ? lanes : 0u;
-  const dim3 grid((a.tokens + kRouteWaves - 1u) / kRouteWaves);
-  if (a.bias)
-    k_route<R, true><<<grid, 64 * kRouteWaves, 0, stream>>>(a);
-  else
-    k_route<R, false><<<grid, 64 * kRouteWaves, 0, stream>>>(a);
+  constexpr uint32_t kMost = 1u << 25;  // tokens a launch, which has fewer than 2^32 threads
+  for (uint32_t left = a.tokens; left; left -= a.tokens) {
+    a.tokens = left < kMost ? left : kMost;
+    const dim3 grid((a.tokens + kRouteWaves - 1u) / kRouteWaves);
+    if (a.bias)
+      k_route<R, true><<<grid, 64 * kRouteWaves, 0, stream>>>(a);
+    else
+      k_route<R, false><<<grid, 64 * kRouteWaves, 0, stream>>>(a);
+    a.logits = (const uint8_t *)a.logits + (size_t)a.tokens * a.E * el;
+    a.ids += (size_t)a.tokens * a.topk;
+    a.weights += (size_t)a.tokens * a.topk;
+  }
 }
 
 }  // namespace
