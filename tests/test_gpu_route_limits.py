@@ -128,3 +128,16 @@ def test_more_tokens_than_one_launch_has_threads_for():
     moe_route(l, 1, ids=ids[:T], weights=w[:T])
     assert torch.equal(ids[:T, 0], (l[:, 1] > l[:, 0]).int()) and (w[:T] == 1).all()
     assert int(ids[T]) == 7 and float(w[T]) == 7
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_slots_without_an_expert_weigh_nothing_whatever_the_factor(scoring, renorm):
+    log(f"factor {scoring} renorm={renorm}")
+    l = torch.full((4, 6), -float("inf"), device="cuda")
+    l[1, 2], l[2, 0], l[2, 5], l[3] = 0.5, -60.0, -61.0, 0.25
+    for factor in (float("inf"), float("nan"), -float("inf")):
+        ids, w = moe_route(l, 3, scoring, renormalize=renorm, routed_scale=factor)
+        assert torch.equal(ids.cpu(), torch.tensor([[-1, -1, -1], [2, -1, -1], [0, 5, -1], [0, 1, 2]], dtype=torch.int32))
+        none = ids < 0
+        assert (w[none] == 0).all() and not torch.isfinite(w[~none]).any(), factor

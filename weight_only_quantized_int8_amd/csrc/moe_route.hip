@@ -394,7 +394,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const RouteArgs a) {
   }
   if (lane >= a.topk) return;
   a.ids[(size_t)t * a.topk + lane] = lane < n ? id : INT8W_NO_EXPERT;
-  a.weights[(size_t)t * a.topk + lane] = odd ? __builtin_nanf("") : w;
+  a.weights[(size_t)t * a.topk + lane] = odd ? __builtin_nanf("") : lane < n ? w : 0.f;  // 0 whatever the factor
 }
 
 template <int R>
