@@ -1,0 +1,66 @@
+"""Low-rank adapters at the ends of their ranges: own ranks beside infinities, large factors, values beyond BF16's largest; against
+their 64-bit definition (tests/adapter_reference.py), in each of the forms a call can take.  Every test prints its case first."""
+import numpy as np
+import pytest
+import torch
+
+import adapter_reference as R
+from test_gpu_lora import bits, f64, gen, ids_of, pool_of, randn
+from weight_only_quantized_int8_amd import LoraAdapters, lora_add
+
+pytestmark = pytest.mark.gpu
+
+# rows, K, N, rank: one launch; a workgroup a row; groups of up to 16 and of up to 64 rows
+FORMS = [(1, 64, 96, 16), (7, 72, 300, 8), (40, 520, 130, 48), (1, 520, 96, 72), (30, 136, 600, 136), (64, 256, 96, 256), (65, 64, 96, 16),
+         (90, 136, 300, 72), (400, 520, 130, 16), (700, 136, 96, 64), (600, 72, 264, 136)]
+
+
+def log(msg):
+    print(msg, flush=True)
+
+
+def check(y, ref, lim, what):
+    """Finite values within their limits, NaN where NaN is wanted, infinities of the wanted sign."""
+    got = f64(y)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), f"{what}: NaN in rows {np.flatnonzero((np.isnan(got) != np.isnan(ref)).any(1))[:8]}"
+    with np.errstate(invalid="ignore"):
+        ok = np.isnan(ref) | (got == ref) | (np.isfinite(ref) & (np.abs(got - ref) <= lim))
+    assert ok.all(), f"{what}: {np.count_nonzero(~ok)} outside; first {np.argwhere(~ok)[0]} got {got[~ok][0]} want {ref[~ok][0]}"
+
+
+@pytest.mark.parametrize("m,K,N,rank", FORMS)
+@pytest.mark.parametrize("kind", ["mixed", "runs"])
+def test_an_own_rank_beside_infinities(m, K, N, rank, kind):
+    # an adapter of rank r is a sum over r: what x holds meets no padding, and of rank 0 nothing at all
+    log(f"own ranks and infinities m={m} K={K} N={N} rank={rank} {kind}")
+    g = gen(m + rank)
+    num = 6
+    own = [0, 1, min(rank, 3), 8, rank, min(rank, 17)]
+    pool, x, base = pool_of(g, num, rank, K, N), randn(g, m, K), randn(g, m, N)
+    for e, r in enumerate(own):
+        pool.a[e, r:] = 0
+        pool.b[e, :, r:] = 0
+    pool = LoraAdapters(pool.a, pool.b, pool.scales, torch.tensor(own, dtype=torch.int32, device="cuda"))
+    for first in range(num) if m == 1 else (0,):
+        ids = ids_of(kind, m, num, m)
+        ids[0] = first
+        wrong = x.clone()
+        wrong[0::3, 5] = float("inf")
+        wrong[0::6, K - 1] = -float("inf")
+        if m > 4:
+            wrong[4, 9] = float("nan")
+        y = lora_add(pool, wrong, ids, base)
+        host, xs, bs = ids.cpu().numpy(), f64(wrong), f64(base)
+        ref, lim = np.empty((m, N)), np.zeros((m, N))
+        for e in range(-1, num):
+            at, r = np.flatnonzero(host == e), own[e] if e >= 0 else 1
+            if not len(at):
+                continue
+            if r == 0:  # base itself
+                ref[at] = bs[at]
+                continue
+            with np.errstate(invalid="ignore"):
+                ref[at], lim[at] = R.lora(xs[at], f64(pool.a)[max(e, 0):max(e, 0) + 1, :r], f64(pool.b)[max(e, 0):max(e, 0) + 1, :, :r],
+                                          f64(pool.scales)[max(e, 0):max(e, 0) + 1], np.zeros(len(at), int) if e >= 0 else np.full(len(at), -1), bs[at])
+        check(y, ref, lim, (kind, first))
+        assert first != 0 or torch.equal(bits(y[0]), bits(base[0]))

@@ -70,11 +70,18 @@ __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t from, uint32_t off, u
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)off, 0, 0, 0);
 }
 
-// The adapter's own rank, rounded up to whole 16-byte pieces of a row of B.
+// The adapter's own rank.  Rows of A from it on are not read, and their u is 0 whatever x holds: infinities and NaN
+// meet no padding.
 __device__ __forceinline__ uint32_t own_rank(const LoraStack &s, uint32_t e) {
   if (!s.ranks) return s.R;
   const uint32_t r = s.ranks[e];
-  return r < s.R ? (r + 7u) & ~7u : s.R;
+  return uniform32(r < s.R ? r : s.R);
+}
+// u of four rows from `row`.
+__device__ __forceinline__ f32x4 within_rank(f32x4 v, uint32_t row, uint32_t rank) {
+#pragma unroll
+  for (uint32_t i = 0; i < 4u; ++i) v[i] = row + i < rank ? v[i] : 0.f;
+  return v;
 }
 
 // ---- groups --------------------------------------------------------------------------------
@@ -318,7 +325,7 @@ struct ShrinkFew {
         f32x4 v = sums[p];
 #pragma unroll
         for (uint32_t w = 1; w < 4u; ++w) v += sums[w * RT * 64u + p];
-        *(g_f32x4 *)((g_f32 *)s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = v;
+        *(g_f32x4 *)((g_f32 *)s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = within_rank(v, row, rank);
       }
       __syncthreads();
     }
@@ -387,7 +394,8 @@ struct ShrinkMany {
 #pragma unroll
       for (uint32_t t = 0; t < RT; ++t) {
         const uint32_t row = r0 + 16u * t + 4u * (lane >> 4);
-        if (io < n && row < s.R) *(g_f32x4 *)((g_f32 *)s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = acc[t];
+        if (io < n && row < s.R)
+          *(g_f32x4 *)((g_f32 *)s.u + ((size_t)part_k.part * g.m + out_row) * s.R + row) = within_rank(acc[t], row, rank);
       }
     }
   }
@@ -915,12 +923,12 @@ __global__ __launch_bounds__(1024) void k_solo(const LoraArgs g) {
   bool staged = false;
   for (uint32_t r = halves ? wave % 8u : wave; r < s.R; r += 16u) {
     float sum = 0.f;
-    for (uint32_t c = c0; c < c1; c += kAhead) {
+    for (uint32_t c = c0; c < c1 && r < rank; c += kAhead) {
       u32x4 a[kAhead];
 #pragma unroll
       for (uint32_t j = 0; j < kAhead; ++j) {
         const uint32_t k = (c + j) * kChunk + 8u * lane;
-        a[j] = buf_load_b128(ra, r < rank && c + j < c1 && k < g.K ? (r * g.K + k) * 2u : kOutOfRange);
+        a[j] = buf_load_b128(ra, c + j < c1 && k < g.K ? (r * g.K + k) * 2u : kOutOfRange);
       }
       keep_order();
       if (!staged) {
