@@ -64,3 +64,18 @@ def test_an_own_rank_beside_infinities(m, K, N, rank, kind):
                                           f64(pool.scales)[max(e, 0):max(e, 0) + 1], np.zeros(len(at), int) if e >= 0 else np.full(len(at), -1), bs[at])
         check(y, ref, lim, (kind, first))
         assert first != 0 or torch.equal(bits(y[0]), bits(base[0]))
+
+
+@pytest.mark.parametrize("m,K,N,rank", FORMS)
+def test_a_large_factor_of_small_products(m, K, N, rank):
+    # the factor comes last: times u alone it would pass fp32's range, B u it does not
+    log(f"large factors m={m} K={K} N={N} rank={rank}")
+    g = gen(m + K)
+    pool, x, base, ids = pool_of(g, 3, rank, K, N), randn(g, m, K, gain=2.0 ** 20), randn(g, m, N, gain=2.0 ** 12), ids_of("mixed", m, 3, 2)
+    ids[0] = 1
+    pool = LoraAdapters(pool.a, pool.b * 2.0 ** -100, torch.tensor([2.0 ** 118, 1.5 * 2.0 ** 112, 2.0 ** 96], device="cuda"))
+    for b in (base, None):
+        y = lora_add(pool, x, ids, b)
+        ref, lim = R.lora(f64(x), f64(pool.a), f64(pool.b), f64(pool.scales), ids.cpu().numpy(), f64(b) if b is not None else None)
+        assert np.isfinite(ref).all() and (np.abs(ref) < 2.0 ** 120).all()
+        check(y, ref, lim, b is None)

@@ -8,7 +8,7 @@
 // the vector ALUs free.  Two launches:
 //  shrink  u in fp32, K cut into `parts` (the sum over K is the long one, and a single token's
 //          A has to come through many CUs): u [parts, m, R] in the workspace.
-//  expand  sums the parts in their order, scales, multiplies by B_e, adds base, rounds once.
+//  expand  sums the parts in their order, multiplies by B_e, scales, adds base, rounds once.
 //          u enters the matrix cores as the sum of two BF16 values (u's own rounding to one
 //          would be as large as the output's); the products are exact and summed in fp32.
 // One launch (k_solo) for a few rows of small matrices: there the second launch costs more than
@@ -481,10 +481,10 @@ __device__ __forceinline__ void split_bf16(const f32x4 &v, u32x2 &hi, u32x2 &lo)
   }
 }
 
-// COUNT pieces of four values of u, piece i of row(i) from offset at(i) of it: the parts added in their order,
-// scaled.  All pieces of several parts are in flight at a time.
+// COUNT pieces of four values of u, piece i of row(i) from offset at(i) of it: the parts added in their order.
+// All pieces of several parts are in flight at a time.
 template <int COUNT, class Row, class At>
-__device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, const LoraStack &s, uint32_t parts, float scale, Row row,
+__device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, const LoraStack &s, uint32_t parts, Row row,
                                           At at) {
   constexpr uint32_t kAhead = 8 / COUNT;
   const size_t next = (size_t)g.m * s.R;
@@ -511,8 +511,6 @@ __device__ __forceinline__ void sum_parts(f32x4 (&v)[COUNT], const LoraArgs &g, 
 #pragma unroll
       for (int i = 0; i < COUNT; ++i) v[i] += w[j][i];
   }
-#pragma unroll
-  for (int i = 0; i < COUNT; ++i) v[i] *= scale;
 }
 
 // Whether eight columns of a row from a multiple of 8 are a 16-byte access.
@@ -522,7 +520,7 @@ __device__ __forceinline__ bool wide_rows(const LoraStack &s) {
   return (at & 15u) == 0u;
 }
 
-// Four rows of a lane: y = base + v for eight columns from n.
+// Four rows of a lane: y = base + scale v for eight columns from n.
 struct OutRows {
   const g_u16 *base[4];
   g_u16 *y[4];
@@ -530,7 +528,9 @@ struct OutRows {
   bool wide;  // 16-byte accesses are aligned
   uint32_t N;
   bool read;
-  __device__ __forceinline__ OutRows(const LoraStack &s, const uint32_t *list, uint32_t i0, uint32_t n) {
+  float scale;  // last, as in k_solo: times u it might pass fp32's range where the product does not
+  __device__ __forceinline__ OutRows(const LoraStack &s, float scale_, const uint32_t *list, uint32_t i0, uint32_t n) {
+    scale = scale_;
     wide = wide_rows(s);
     read = s.base != nullptr;
     N = s.N;
@@ -559,12 +559,12 @@ struct OutRows {
       if (wide && n + 8u <= N) {
         u32x4 w;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = pack_bf16x2(bf16_lo(o[i][t]) + v[2 * t][i], bf16_hi(o[i][t]) + v[2 * t + 1][i]);
+        for (int t = 0; t < 4; ++t) w[t] = pack_bf16x2(__builtin_fmaf(scale, v[2 * t][i], bf16_lo(o[i][t])), __builtin_fmaf(scale, v[2 * t + 1][i], bf16_hi(o[i][t])));
         *(g_u32x4 *)(y[i] + n) = w;
       } else {
 #pragma unroll
         for (uint32_t t = 0; t < 8u; ++t)
-          if (n + t < N) y[i][n + t] = to_bf16_bits((read ? bf16_bits_to_f32(base[i][n + t]) : 0.f) + v[t][i]);
+          if (n + t < N) y[i][n + t] = to_bf16_bits(__builtin_fmaf(scale, v[t][i], read ? bf16_bits_to_f32(base[i][n + t]) : 0.f));
       }
     }
   }
@@ -644,14 +644,13 @@ struct ExpandFew {
     const auto rb = make_rsrc(s.b + (size_t)e * s.N * s.R, s.N * s.R * 2u);
 #pragma unroll
     for (uint32_t j = 0; j < 2u * P; ++j) dma_b<P>(rb, s.R, w0, 0u, j, b, lane);
-    const OutRows out(s, list, 4u * q, n);
+    const OutRows out(s, s.scales ? s.scales[e] : 1.f, list, 4u * q, n);
     u32x4 o[4];
     out.load(o, w0 + 8u * c);
-    const float scale = s.scales ? s.scales[e] : 1.f;
     for (uint32_t p = threadIdx.x; p < kFew * kRanks / 4u; p += 256u) {
       const uint32_t i = p / (kRanks / 4u), r = 4u * (p % (kRanks / 4u)), from = i < n ? list[i] : g.m;
       f32x4 v[1];
-      sum_parts(v, g, s, g.parts, scale, [&](int) { return from; }, [&](int) { return r; });
+      sum_parts(v, g, s, g.parts, [&](int) { return from; }, [&](int) { return r; });
       u32x2 h, l;
       split_bf16(v[0], h, l);
       *reinterpret_cast<u32x2 *>(hi + i * kRow + 2u * r) = h;
@@ -720,7 +719,7 @@ struct ExpandMany {
       constexpr int kPieces = P / 2;  // a lane: 16 rows of 8 P values
       f32x4 v[kPieces];
       auto piece = [&](int i) { return 64u * i + lane; };
-      sum_parts(v, g, s, parts, scale,
+      sum_parts(v, g, s, parts,
                 [&](int i) {
                   const uint32_t at = 16u * wave + piece(i) / (2u * P);
                   return at < n ? list[at] : g.m;
@@ -748,7 +747,7 @@ struct ExpandMany {
         }
       }
     }
-    const OutRows out(s, list, 16u * wave + 4u * q, n);
+    const OutRows out(s, scale, list, 16u * wave + 4u * q, n);
     f32x4 acc[8];
     u32x4 o[4];
     // One chunk of a block's rank, from stage `at`; the next one goes to `other`.  Two stages with constant places: the
@@ -973,7 +972,7 @@ __global__ __launch_bounds__(1024) void k_solo(const LoraArgs g) {
     }
   }
   v += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0xB1, 0xF, 0xF, true));  // the neighbour's
-  if (write) ((g_u16 *)s.y)[i * s.y_stride + n] = to_bf16_bits(base + scale * v);
+  if (write) ((g_u16 *)s.y)[i * s.y_stride + n] = to_bf16_bits(__builtin_fmaf(scale, v, base));
 }
 
 // ---- host ----------------------------------------------------------------------------------
