@@ -79,3 +79,26 @@ def test_a_large_factor_of_small_products(m, K, N, rank):
         ref, lim = R.lora(f64(x), f64(pool.a), f64(pool.b), f64(pool.scales), ids.cpu().numpy(), f64(b) if b is not None else None)
         assert np.isfinite(ref).all() and (np.abs(ref) < 2.0 ** 120).all()
         check(y, ref, lim, b is None)
+
+
+@pytest.mark.parametrize("m,K,N,rank", FORMS)
+def test_values_between_the_largest_of_bf16_and_of_fp32(m, K, N, rank):
+    # u is BF16's largest value and half a unit of it: finite, though its rounding to BF16 is not
+    log(f"u beyond BF16 m={m} K={K} N={N} rank={rank}")
+    g = gen(m + N)
+    a, b = torch.zeros(2, rank, K, dtype=torch.bfloat16, device="cuda"), randn(g, 2, N, rank, gain=2.0 ** -120)
+    most = torch.finfo(torch.bfloat16).max
+    a[:, :, 3], a[:, :, 11] = 1.0, torch.tensor([1.0, -1.0], device="cuda").repeat(rank // 2)
+    x = torch.zeros(m, K, dtype=torch.bfloat16, device="cuda")
+    x[:, 3], x[:, 11] = most, 2.0 ** 119
+    x[1::2] = -x[1::2]
+    pool, ids = LoraAdapters(a, b), ids_of("runs", m, 2, 1)
+    base = randn(g, m, N)
+    y = lora_add(pool, x, ids, base)
+    ref, lim = R.lora(f64(x), f64(a), f64(b), np.ones(2), ids.cpu().numpy(), f64(base))
+    assert np.isfinite(ref).all()
+    check(y, ref, lim, "u beyond BF16")
+    x[0, 3], x[m - 1, 5] = float("inf"), float("nan")  # these stay what they are
+    a[:, :, 5] = 1.0
+    y = lora_add(pool, x, ids, base)
+    assert not torch.isfinite(y[0]).any() and torch.isnan(y[m - 1]).all()

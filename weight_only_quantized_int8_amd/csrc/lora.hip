@@ -468,16 +468,14 @@ struct UOperand {
   u32x4 hi[kAll], lo[P == 2 ? 1 : kAll];
 };
 
-// Two BF16 values that add up to each of four.  A value beyond BF16's range has an infinity for
-// its upper part, and no lower one.
+// Two BF16 values that add up to each of four.  The upper one is at most BF16's largest, so that a value beyond that,
+// an infinity or a NaN is in the lower one.
 __device__ __forceinline__ void split_bf16(const f32x4 &v, u32x2 &hi, u32x2 &lo) {
+  constexpr float kMost = 0x1.FEp127f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    float d0 = v[2 * i] - bf16_lo(hi[i]), d1 = v[2 * i + 1] - bf16_hi(hi[i]);
-    d0 = fabsf(d0) < __builtin_inff() ? d0 : 0.f;
-    d1 = fabsf(d1) < __builtin_inff() ? d1 : 0.f;
-    lo[i] = pack_bf16x2(d0, d1);
+    hi[i] = pack_bf16x2(fminf(fmaxf(v[2 * i], -kMost), kMost), fminf(fmaxf(v[2 * i + 1], -kMost), kMost));
+    lo[i] = pack_bf16x2(v[2 * i] - bf16_lo(hi[i]), v[2 * i + 1] - bf16_hi(hi[i]));
   }
 }
 
