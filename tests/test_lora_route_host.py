@@ -239,3 +239,76 @@ def test_packed_arguments_are_the_structures():
     packed = B._ROUTE_CALL.pack(A, 9 * A, 2 * A, 3 * A, 7, 60, 3, 1, 1, 6, 2, 1, 1, 1.0)
     assert bytes(B.RouteCall.from_buffer_copy(packed))[:72] == bytes(c)[:72]
     assert B._LORA_OUT.pack(4 * A, 5 * A, 96, 97) == bytes(out(ys=97))
+
+
+def fake_pool(a, b, scales=None):
+    p = LoraAdapters.__new__(LoraAdapters)
+    p.a, p.b, p.scales, p.ranks, p.device = a, b, scales, None, a.device
+    (p.num_adapters, p.rank, p.in_features), p.out_features = a.shape, b.shape[1]
+    p.desc = B.LoraDesc(a.data_ptr(), b.data_ptr(), None, None, p.num_adapters, p.rank, p.in_features, p.out_features)
+    p.packed = bytes(p.desc)
+    return p
+
+
+def test_inputs_that_require_a_gradient_are_refused(monkeypatch):
+    bf = torch.bfloat16
+    zeros = {"x": (2, 16), "a": (3, 8, 16), "b": (3, 24, 8), "scales": (3,), "base": (2, 24)}
+    ids = torch.zeros(2, dtype=torch.int32)
+    launched = []
+    monkeypatch.setattr(B, "_call", lambda dev, entry, *args: launched.append(entry))
+    monkeypatch.setattr(B, "_stream_of", lambda dev: 0)
+
+    class Projection:  # what gemm_lora asks of its weight
+        in_features = k = 16
+        out_features = rows = 24
+
+        def gemm(self, x, y):
+            launched.append("gemm")
+            return torch.zeros(2, 24, dtype=bf)
+    for trained in ("x", "a", "b", "scales", "base", None):
+        t = {k: torch.zeros(s, dtype=torch.float32 if k == "scales" else bf, requires_grad=k == trained) for k, s in zeros.items()}
+        pool, other = fake_pool(t["a"], t["b"], t["scales"]), fake_pool(*(torch.zeros(zeros[k], dtype=bf) for k in "ab"))
+        calls = [lambda: lora_add(pool, t["x"], ids, t["base"]), lambda: lora_add([other, pool], t["x"], ids, [None, t["base"]])]
+        if trained != "base":
+            calls += [lambda: B.Int8Weight.gemm_lora(Projection(), t["x"], pool, ids), lambda: Mxfp4Weight.gemm_lora(Projection(), t["x"], pool, ids)]
+        for call in calls:
+            del launched[:]
+            if trained:
+                with pytest.raises(B.Int8wError, match="has no backward") as e:
+                    call()
+                assert e.value.code == UNSUPPORTED and not launched
+            with torch.no_grad():
+                call()
+            assert launched
+            if not trained:
+                call()
+
+    class Logits(torch.Tensor):  # as if on a GPU
+        device = torch.device("cuda", 0)
+    monkeypatch.setattr(B, "_need_slots", lambda *a: None)
+    slots = dict(ids=torch.zeros(2, 2, dtype=torch.int32), weights=torch.zeros(2, 2))
+    for trained in ("logits", "bias", None):
+        logits = torch.zeros(2, 4).as_subclass(Logits).requires_grad_(trained == "logits")
+        bias = torch.zeros(4).as_subclass(Logits).requires_grad_(trained == "bias") if trained != "logits" else None
+        if trained:
+            with pytest.raises(B.Int8wError, match="moe_route has no backward"):
+                moe_route(logits, 2, "sigmoid", bias, **slots)
+        with torch.no_grad():
+            moe_route(logits, 2, "sigmoid", bias, **slots)
+
+    def host(rows, k):
+        codes, scales = torch.zeros(rows, k // 2, dtype=torch.uint8), torch.zeros(rows, k // 32, dtype=torch.uint8)
+        w = Mxfp4Weight.__new__(Mxfp4Weight)
+        w._set(codes, scales, rows, k, codes.device, codes.data_ptr(), scales.data_ptr())
+        return w
+    weights = host(E * I, H), host(E * I, H), host(E * H, I)
+    for trained in ("x", "weights", "x_resid", None):
+        t = {"x": torch.zeros(2, H, dtype=bf), "weights": torch.zeros(2, 2), "x_resid": torch.zeros(2, H, dtype=bf)}
+        if trained:
+            t[trained].requires_grad_()
+        call = lambda: moe_layer_routed(*weights, E, t["x"], torch.zeros(2, 2, dtype=torch.int32), t["weights"], t["x_resid"])  # noqa: E731
+        if trained:
+            with pytest.raises(B.Int8wError, match="moe_layer_routed has no backward"):
+                call()
+        with torch.no_grad():
+            call()

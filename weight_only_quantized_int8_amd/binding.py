@@ -819,7 +819,8 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: t
              group_score stay: "max", a group's largest biased score, or "top2", the sum of its two largest
     A slot that no expert is left for (those at -inf are never taken) holds id -1 and weight 0; a token with NaN
     among its logits has id -1 and weight NaN in all its slots.  ids goes to moe_gemv (which gives NaN for an
-    id of -1), both to moe_layer_routed.
+    id of -1), both to moe_layer_routed.  There is no backward: an input that requires a gradient is refused
+    where gradients are recorded.
     """
     dev, f32 = logits.device, logits.dtype is torch.float32
     if not (f32 or logits.dtype is torch.bfloat16) or logits.dim() != 2 or not logits.is_contiguous() or dev.type != "cuda":
@@ -831,6 +832,8 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: t
     if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (E,) or bias.device != dev
                              or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 [{E}] tensor on the logits' GPU")
+    if logits.requires_grad or (bias is not None and bias.requires_grad):
+        _no_backward("moe_route")
     topk, groups = int(topk), int(groups)
     topk_groups = groups if topk_groups is None else int(topk_groups)
     if not (1 <= topk <= MAX_MOE_TOPK and 1 <= groups <= MAX_MOE_GROUPS and 1 <= topk_groups <= groups):  # before they size the outputs
@@ -857,6 +860,7 @@ def moe_layer_routed(gate, up, down, num_experts: int, x: torch.Tensor, ids: tor
     ids:     int32/uint32 [tokens, topk]; a slot whose id is not below num_experts (-1) runs no expert
     weights: float32 [tokens, topk], of the slots' experts in the token's sum; any NaN makes the token's output NaN
     returns  bfloat16 [tokens, hidden]: x_resid + the weighted sum over the slots.  The rest as moe_layer.
+    There is no backward: an input that requires a gradient is refused where gradients are recorded.
     """
     mx = isinstance(gate, Mxfp4Weight)
     kind = Mxfp4Weight if mx else Int8Weight
@@ -877,6 +881,8 @@ def moe_layer_routed(gate, up, down, num_experts: int, x: torch.Tensor, ids: tor
     _need_slots(weights, "weights", (torch.float32,), T, topk, dev)
     if x_resid is not None:
         _need_bf16(x_resid, "x_resid", T * hidden, dev)
+    if x.requires_grad or weights.requires_grad or (x_resid is not None and x_resid.requires_grad):
+        _no_backward("moe_layer_routed")
     if not 1 <= topk <= MAX_MOE_TOPK:  # before it sizes the scratch
         raise Int8wError(INT8W_ERR_SHAPE, f"topk {topk} outside 1..{MAX_MOE_TOPK}")
     if y is None:
@@ -909,6 +915,14 @@ def _call(device: torch.device, entry, *args) -> None:
             rc = entry(*args)
     if rc != INT8W_OK:
         _check(rc)
+
+
+def _no_backward(what: str) -> None:
+    """For a call with an input that requires a gradient: refused where gradients are recorded, as a backward pass would
+    stop at it without a word."""
+    if torch.is_grad_enabled():
+        raise Int8wError(INT8W_ERR_UNSUPPORTED, f"{what} has no backward, and an input requires a gradient: call it under "
+                                                "torch.no_grad(), or on detached tensors")
 
 
 class LoraAdapters:
@@ -967,6 +981,10 @@ class LoraAdapters:
                    torch.tensor(ranks, dtype=torch.int32, device=dev))
 
 
+def _trained(pool: LoraAdapters) -> bool:
+    return pool.a.requires_grad or pool.b.requires_grad or (pool.scales is not None and pool.scales.requires_grad)
+
+
 def _rows(t: torch.Tensor, name: str, m: int, n: int, device: torch.device) -> int:
     """Checks a [m, n] matrix of bfloat16 whose rows may be apart (columns of a wider one); returns its row stride."""
     if t.dtype is not torch.bfloat16:
@@ -990,6 +1008,8 @@ def _need_pool(pool: LoraAdapters, k: int, n: int, x: torch.Tensor, ids: torch.T
     if x.dim() != 2 or x.device != pool.device:
         raise ValueError(f"X must be [m, {k}] on {pool.device}")
     _need_ids(ids, x.shape[0], pool.device)
+    if x.requires_grad or _trained(pool):
+        _no_backward("gemm_lora")
 
 
 def _need_ids(ids: torch.Tensor, m: int, device: torch.device) -> None:
@@ -1015,6 +1035,7 @@ def lora_add(adapters, x: torch.Tensor, ids: torch.Tensor, base=None, y=None):
     y:        the output, base itself for in place; None: a new one
     x, base and y may have rows apart (columns of a wider matrix; x's a multiple of 8 values).
     Scratch is allocated for the call on the current stream, so calls may overlap on several streams.
+    There is no backward: an input or adapter that requires a gradient is refused where gradients are recorded.
     """
     one = isinstance(adapters, LoraAdapters)
     if one:
@@ -1039,6 +1060,8 @@ def lora_add(adapters, x: torch.Tensor, ids: torch.Tensor, base=None, y=None):
         if pool.device != dev:
             raise ValueError("lora_add: pools on different devices")
         n, b, o = pool.out_features, bases[i], ys[i]
+        if x.requires_grad or _trained(pool) or (b is not None and b.requires_grad):
+            _no_backward("lora_add")
         if o is None:
             o = ys[i] = x.new_empty_strided((m, n), (n, 1))
             os = n
