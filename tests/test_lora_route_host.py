@@ -261,6 +261,7 @@ def test_inputs_that_require_a_gradient_are_refused(monkeypatch):
     class Projection:  # what gemm_lora asks of its weight
         in_features = k = 16
         out_features = rows = 24
+        device = torch.device("cpu")
 
         def gemm(self, x, y):
             launched.append("gemm")
@@ -312,3 +313,36 @@ def test_inputs_that_require_a_gradient_are_refused(monkeypatch):
                 call()
         with torch.no_grad():
             call()
+
+
+def test_gemm_lora_makes_the_weights_device_current_for_its_product(monkeypatch):
+    seen = []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(self.device)
+
+        def __exit__(self, *exc):
+            seen.append("back")
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(B, "_need_pool", lambda *a: None)
+    monkeypatch.setattr(B, "_add_in_place", lambda pool, x, ids, y: seen.append("adapters") or y)
+
+    class Projection:
+        in_features = k = out_features = rows = 16
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+        def gemm(self, x, y):
+            seen.append("gemm")
+            return y
+    for cls in (B.Int8Weight, Mxfp4Weight):
+        for index, want in ((0, [torch.device("cuda", 0), "gemm", "back", "adapters"]), (1, ["gemm", "adapters"])):
+            del seen[:]
+            assert cls.gemm_lora(Projection(index), None, None, None, "y") == "y"
+            assert seen == want

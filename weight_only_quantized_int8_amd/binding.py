@@ -11,6 +11,7 @@ in_features.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -561,7 +562,9 @@ class Int8Weight:
                   y: torch.Tensor | None = None) -> torch.Tensor:
         """gemm with each row's low-rank adapter beside it: lora_add in place on gemm's Y (which gemm has rounded)."""
         _need_pool(adapters, self.in_features, self.out_features, x, ids)
-        return _add_in_place(adapters, x, ids, self.gemm(x, y))
+        with _current(self.device):
+            y = self.gemm(x, y)
+        return _add_in_place(adapters, x, ids, y)
 
 
 # One gemm workspace per device (scratch for split-K partials), grown on
@@ -745,7 +748,9 @@ class Mxfp4Weight:
                   y: torch.Tensor | None = None) -> torch.Tensor:
         """gemm with each row's low-rank adapter beside it: lora_add in place on gemm's Y (which gemm has rounded)."""
         _need_pool(adapters, self.k, self.rows, x, ids)
-        return _add_in_place(adapters, x, ids, self.gemm(x, y))
+        with _current(self.device):
+            y = self.gemm(x, y)
+        return _add_in_place(adapters, x, ids, y)
 
     def gemm_mx(self, x: "Mxfp4Weight", y: torch.Tensor | None = None) -> torch.Tensor:
         """Y = X W^T with both operands in MXFP4 (x e.g. from Mxfp4Weight.quantize)."""
@@ -905,10 +910,15 @@ def _need_slots(t: torch.Tensor, name: str, dtypes, tokens: int, topk: int, devi
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # without a check for initialisation
 
 
+def _current(device: torch.device):
+    """Makes another device than the current one current: kernels go to the current device where the stream is the
+    default one (handle 0)."""
+    return contextlib.nullcontext() if device.index is None or device.index == _current_device() else torch.cuda.device(device)
+
+
 def _call(device: torch.device, entry, *args) -> None:
-    """Calls a C entry that launches on `device`.  Kernels go to the current device where the stream is the default
-    one (handle 0), so another device is made current for the launch."""
-    if device.index is None or device.index == _current_device():
+    """Calls a C entry that launches on `device`."""
+    if device.index is None or device.index == _current_device():  # mostly: without a context object
         rc = entry(*args)
     else:
         with torch.cuda.device(device):
