@@ -346,3 +346,38 @@ def test_gemm_lora_makes_the_weights_device_current_for_its_product(monkeypatch)
             del seen[:]
             assert cls.gemm_lora(Projection(index), None, None, None, "y") == "y"
             assert seen == want
+
+
+def test_gemm_lora_refuses_rows_before_its_product():
+    class Projection:
+        in_features = k = 8
+        out_features = rows = 8
+        device = torch.device("cpu")
+
+        def gemm(self, x, y):
+            pytest.fail("the product was launched")
+    bf, m = torch.bfloat16, (1 << 20) + 1
+    pool = fake_pool(torch.zeros(1, 8, 8, dtype=bf), torch.zeros(1, 8, 8, dtype=bf))
+    for cls in (B.Int8Weight, Mxfp4Weight):
+        with pytest.raises(B.Int8wError, match="more than 2\\^20") as e:
+            cls.gemm_lora(Projection(), torch.zeros(m, 8, dtype=bf), pool, torch.zeros(m, dtype=torch.int32))
+        assert e.value.code == SHAPE
+
+
+@pytest.mark.parametrize("num,k,n,shift,code,text", [
+    (0, 16, 24, 0, NULL, "missing a tensor"), (2, 1 << 20, 24, 0, SHAPE, "below 2^20"), (2, 16, 1 << 20, 0, SHAPE, "below 2^20"),
+    (2, 16, 24, 4, ALIGN, "a or b"), (2, 16, 24, 0, None, ""),
+])
+def test_a_pool_that_no_call_takes_is_not_made(num, k, n, shift, code, text):
+    class Gpu(torch.Tensor):  # as if on a GPU
+        device = torch.device("cuda", 0)
+
+    def zeros(*shape):
+        count = shape[0] * shape[1] * shape[2]
+        return torch.zeros(count + 16, dtype=torch.bfloat16)[shift:shift + count].view(shape).as_subclass(Gpu)
+    if code is None:
+        assert LoraAdapters(zeros(num, 8, k), zeros(num, n, 8)).num_adapters == num
+        return
+    with pytest.raises(B.Int8wError) as e:
+        LoraAdapters(zeros(num, 8, k), zeros(num, n, 8))
+    assert e.value.code == code and text in str(e.value)

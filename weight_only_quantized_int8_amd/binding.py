@@ -53,6 +53,7 @@ MAX_MOE_EXPERTS, MAX_MOE_TOPK = 512, 16  # INT8W_MAX_MOE_EXPERTS, INT8W_MAX_MOE_
 MAX_MULTI = 4  # INT8W_MAX_MULTI
 MAX_MOE_GROUPS = 64  # INT8W_MAX_MOE_GROUPS
 MAX_LORA_RANK = 256  # INT8W_MAX_LORA_RANK
+MAX_LORA_ROWS = 1 << 20  # of a call
 ROUTE_SCORING = {"softmax": 0, "sigmoid": 1}  # INT8W_ROUTE_*
 GROUP_SCORES = {"max": 0, "top2": 1}  # INT8W_GROUP_*
 MAX_MOE_SLOTS = 65536  # INT8W_MAX_MOE_SLOTS
@@ -968,6 +969,8 @@ class LoraAdapters:
         self.desc = LoraDesc(a.data_ptr(), b.data_ptr(), scales.data_ptr() if scales is not None else None,
                              ranks.data_ptr() if ranks is not None else None, num, rank, k, n)
         self.packed = bytes(self.desc)  # as lora_add passes it
+        # what no call would take is refused here: a call of no rows checks the pool and launches nothing
+        _check(load_library().packed_lora_add(self.packed, None, 1, None, 0, None, 0, None, 0, 0))
 
     @classmethod
     def from_list(cls, adapters) -> "LoraAdapters":
@@ -1017,6 +1020,8 @@ def _need_pool(pool: LoraAdapters, k: int, n: int, x: torch.Tensor, ids: torch.T
         raise ValueError(f"adapters must be LoraAdapters of in_features {k} and out_features {n}")
     if x.dim() != 2 or x.device != pool.device:
         raise ValueError(f"X must be [m, {k}] on {pool.device}")
+    if x.shape[0] > MAX_LORA_ROWS:
+        raise Int8wError(INT8W_ERR_SHAPE, f"m={x.shape[0]} rows are more than 2^20")
     _need_ids(ids, x.shape[0], pool.device)
     if x.requires_grad or _trained(pool):
         _no_backward("gemm_lora")
