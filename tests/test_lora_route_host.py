@@ -244,6 +244,7 @@ def test_packed_arguments_are_the_structures():
 def fake_pool(a, b, scales=None):
     p = LoraAdapters.__new__(LoraAdapters)
     p.a, p.b, p.scales, p.ranks, p.device = a, b, scales, None, a.device
+    p.trained = a.requires_grad or b.requires_grad or (scales is not None and scales.requires_grad)
     (p.num_adapters, p.rank, p.in_features), p.out_features = a.shape, b.shape[1]
     p.desc = B.LoraDesc(a.data_ptr(), b.data_ptr(), None, None, p.num_adapters, p.rank, p.in_features, p.out_features)
     p.packed = bytes(p.desc)
