@@ -47,7 +47,9 @@ constexpr uint32_t kStepK = 64;       // K of a step: a cache line of a row
 constexpr uint32_t kBlockN = 128;     // output columns of a step
 constexpr uint32_t kShrinkBlocks = 512;  // workgroups over a plan's groups: what fits the CUs
 constexpr uint32_t kExpandBlocks = 1024;
-constexpr uint32_t kManyGroups = 40;     // from so many on an XCD of expand has groups of its own
+constexpr uint32_t kXcdGroups = 24;      // where an XCD of expand has groups of its own: three each,
+constexpr uint32_t kXcdColumns = 4096;   // few columns
+constexpr uint32_t kXcdValues = 2048;    // or much of u in a group
 
 #define INT8W_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) >> 4) << 14) | 0x0F70 | ((n) & 15))
 #define INT8W_LGKMCNT0() __builtin_amdgcn_s_waitcnt(0xC07F)
@@ -860,11 +862,16 @@ __global__ __launch_bounds__(256, NCH == 1 ? 4 : 2) void k_expand_items(const Lo
       }
     });
   };
-  // Many groups: a group to an XCD, whose u then comes into one L2, and whose neighbours share their B.  Few would lie
-  // unevenly: there an XCD has some columns of all groups.  us so / the other way: 57 groups, 4096 columns, rank 64
-  // 17.6 / 20.0; 128 groups of one adapter of rank 128 43 / 52; 27 groups, 28672 columns, rank 16 18.2 / 17.3.
+  // A group to an XCD, whose u then comes into one L2, or some columns of all groups to an XCD.  The first pays where u is much
+  // of what is read: many rows of a large rank, or few columns.  On wide outputs of small u it loses, and with fewer
+  // than three groups each the XCDs are unevenly loaded.  us of whole calls so / the other way, K 4096: 57 groups of 64 rows, 4096 columns,
+  // rank 64 43 / 51, rank 16 28.0 / 29.1, rank 128 72 / 84; 64 of 64, 8192 columns, rank 64 62 / 75; 57 of 4 rows, 4096 columns (K
+  // 14336), rank 64 43.4 / 44.1; 64 of 17, 2 x 14336 columns, rank 16 76 / 62; 80 of 17, 14336, rank 32 62 / 51; 12 of 64, 14336, rank
+  // 64 30.6 / 28.1.  Over 850 such sizes this rule is within 0.5 % of the better one on average (16 % at worst), either alone 1.7 (26).
   // All groups of an XCD at one run of columns before the next: 8192 rows 110 instead of 113, 2109 18.6 for 17.9.
-  if (groups.total >= kManyGroups) {
+  constexpr uint32_t kRows = 64u * kLoraPlanRows;  // of a round of plans
+  const uint32_t rows = g.m - kRows * blockIdx.y < kRows ? g.m - kRows * blockIdx.y : kRows;
+  if (groups.total >= kXcdGroups && (column_blocks * kBlockN <= kXcdColumns || rows * (8u * P * NCH) >= kXcdValues * groups.total)) {
     for (uint32_t j = blockIdx.x / 8u;; j += gridDim.x / 8u) {
       const uint32_t group = j / runs * 8u + blockIdx.x % 8u;
       if (group >= groups.total) break;
