@@ -102,3 +102,25 @@ def test_values_between_the_largest_of_bf16_and_of_fp32(m, K, N, rank):
     a[:, :, 5] = 1.0
     y = lora_add(pool, x, ids, base)
     assert not torch.isfinite(y[0]).any() and torch.isnan(y[m - 1]).all()
+
+
+@pytest.mark.parametrize("m,N,rank,num", [(700, 4200, 8, 90), (1600, 4100, 64, 24), (1300, 5000, 16, 1300), (400, 4097, 136, 30), (2600, 130, 16, 30),
+                                          (3100, 4104, 32, 26)])
+def test_groups_on_an_xcd_of_their_own_and_spread(m, N, rank, num):
+    # from 24 groups on an XCD has whole groups where u is much or columns are few; wide outputs of small u are spread
+    log(f"groups m={m} N={N} rank={rank} num={num}")
+    g = gen(m + N)
+    K = 64
+    pool, x, base = pool_of(g, num, rank, K, N), randn(g, m, K), randn(g, m, N)
+    for kind in ("runs", "mixed"):
+        ids = ids_of(kind, m, num, 4)
+        y = lora_add(pool, x, ids, base)
+        at = np.unique(np.concatenate([np.arange(0, m, max(1, m // 100)), [m - 1]]))
+        ref, lim = R.lora(f64(x)[at], f64(pool.a), f64(pool.b), f64(pool.scales), ids.cpu().numpy()[at], f64(base)[at])
+        check(y[torch.from_numpy(at).cuda()], ref, lim, kind)
+        e = ids.long().clamp(min=0)  # all rows, to what BF16 tells
+        u = torch.matmul(pool.a.double()[e], x.double().unsqueeze(2)).squeeze(2)
+        for t in range(0, m, 200):
+            own = torch.matmul(pool.b.double()[e[t:t + 200]], u[t:t + 200].unsqueeze(2)).squeeze(2) * pool.scales.double()[e[t:t + 200]].unsqueeze(1)
+            ref = base[t:t + 200].double() + torch.where(ids[t:t + 200, None] >= 0, own, 0.0)
+            assert ((y[t:t + 200].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -12).all()
