@@ -293,8 +293,8 @@ int int8w_mxfp4_moe_layer(const int8w_mxfp4 *gate, const int8w_mxfp4 *up, const 
  *   the topk experts of largest c in them are taken, largest first;
  *   weight = routed_scale * s_e, with renormalize routed_scale * s_e / (sum of the taken s)
  *   (0 where that sum is 0).
- * Equal values go to the lower index.  Scores are compared as if formed in 64 bits.  An expert whose l or c is -inf is never
- * taken; the slots that no expert is left for hold the id INT8W_NO_EXPERT and weight 0.  A token
+ * Equal values (-0 and 0, two +inf) go to the lower index.  Scores are compared as if formed in 64 bits.  An
+ * expert whose l or c is -inf is never taken; the slots that no expert is left for hold the id INT8W_NO_EXPERT and weight 0.  A token
  * with a NaN among its l or c, or with softmax a +inf among its l, gets INT8W_NO_EXPERT and NaN
  * weights in all its slots.
  *   logits   f32 or BF16 [tokens, num_experts] (logits_format), on the device;
@@ -370,7 +370,8 @@ typedef struct {
   const uint16_t *b;      /* BF16 [num_adapters, out_features, rank] (device), 16-byte aligned */
   const float *scales;    /* f32 [num_adapters] (device), or NULL: 1 */
   const uint32_t *ranks;  /* uint32 [num_adapters] (device), or NULL: an adapter's own rank, beyond which its
-                             rows of A and columns of B must be zeros (they are not always read) */
+                             rows of A and columns of B must be zeros (they are not always read), and A x is 0
+                             whatever x holds */
   uint32_t num_adapters;
   uint32_t rank;          /* a multiple of 8, 8..INT8W_MAX_LORA_RANK */
   uint32_t in_features;   /* K: a multiple of 8, below 2^20 */
