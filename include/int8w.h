@@ -354,7 +354,7 @@ int int8w_mxfp4_moe_layer_routed(const int8w_mxfp4 *gate, const int8w_mxfp4 *up,
  * pairs of BF16 matrices; row t of a batch takes the adapter that ids[t] names:
  *   y[t] = RNE_bf16( base[t] + scales[e] * B_e (A_e x[t]) ),  e = ids[t],
  * fp32 sums, the factor after B_e's product, one rounding to BF16.  Unless few rows of small matrices go in one
- * launch, A_e x[t] enters B_e's product as the sum of two BF16 values, within 2^-16 of itself.  Infinities in x,
+ * launch, A_e x[t] enters B_e's product as the sum of two BF16 values, within 2^-16 of itself or 2^-134.  Infinities in x,
  * A or B give infinities or NaN, in the rows that meet them alone; one in B may give NaN where the formula has an
  * infinity.  A row with id INT8W_NO_ADAPTER gets base[t] itself; any other id not below num_adapters gives a row of
  * the quiet NaN 0x7FC0.  base is typically the output of int8_gemm or int8w_mxfp4_gemm, in place.  Up to
